@@ -15,9 +15,15 @@
  *   gptq_pack_ordered        the codes in a column order (act-order layers stored in processing order)
  *   gptq_permute_columns     inputs gathered by the same order
  *
- * and one call that uses the stored layer:
+ * the calls that use the stored layer:
  *
  *   gptq_dequant_gemm        y = x W^T for a few input rows, read straight from the packed codes
+ *   gptq_lora_gemm           low-rank adapters of many requests added beside it
+ *
+ * and the attention half of a decoder block:
+ *
+ *   gptq_norm_rotate         per-head norm of queries and keys with the position rotation
+ *   gptq_attention           attention over packed sequences: shared heads, masks, capped scores
  *
  * Sources (web pages on GPTQ): the GPTQ tools page at ozercemkelahmet.com ("How it works",
  * Steps 3-8, "Optional refinements", "A minimal Python sketch", "Memory arithmetic"); "GPTQ
@@ -310,6 +316,130 @@ gptq_status_t gptq_dequant_gemm(const void *x, int32_t x_dtype, int64_t m, int64
                                 int32_t bits, int32_t layout, const float *scales, const int32_t *zeros,
                                 const int32_t *g_idx, int64_t rows, int64_t d, int32_t group_size, float *y,
                                 int64_t ld_y, void *stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection (the stored layer's product, or any
+ * other): row i of x names adapter a = index[i], and
+ *   y[i, r] = base[i, r] + scales[a] * sum_k T[i, k] B_a[r, k],   T[i, k] = sum_c x[i, c] A_a[k, c].
+ * A row whose index is outside [0, adapters) has no adapter: y[i] = base[i].
+ *
+ *   x        device array [m x ld_x] of dtype (GPTQ_F32, GPTQ_F16 or GPTQ_BF16), d features a row.
+ *            Not modified.
+ *   m        input rows, >= 0 (0: nothing is queued); ld_x >= d.
+ *   A, B     device arrays of dtype: A [adapters x rank x d], B [adapters x rows x rank], contiguous.
+ *   ranks    device int32[adapters], the rank each adapter uses (clamped to [0, rank]; what A's rows and
+ *            B's columns hold beyond it takes no part), or NULL: every adapter uses `rank`.
+ *   scales   device float[adapters], or NULL: 1.
+ *   adapters >= 0; rank 1..256.
+ *   index    device int32[m], in any order; rows may share an adapter.
+ *   rows     outputs, >= 0 (0: nothing is queued); d input features, >= 1.
+ *   base     device float[m x ld_base], ld_base >= rows, or NULL: zeros. May be y itself with the same
+ *            pitch (added in place), or not overlap it; another overlap is GPTQ_EINVAL.
+ *   y        device float[m x ld_y], output, ld_y >= rows. Must not overlap the other arrays.
+ *   work     device workspace of at least gptq_lora_workspace_bytes(m, d, rows, adapters, rank) bytes,
+ *            not shared with a concurrent call; 16-byte aligned.
+ * Products of x and A are exact in fp32 (fp16 and bf16), T and all sums are fp32. Results do not depend
+ * on scheduling. Two launches on `stream`; the call may be captured in a graph.
+ */
+gptq_status_t gptq_lora_gemm(const void *x, int32_t dtype, int64_t m, int64_t ld_x, const void *A, const void *B,
+                             const int32_t *ranks, const float *scales, int64_t adapters, int32_t rank,
+                             const int32_t *index, int64_t rows, int64_t d, const float *base, int64_t ld_base,
+                             float *y, int64_t ld_y, void *work, size_t work_bytes, void *stream);
+
+/* Workspace bytes for gptq_lora_gemm; 0 for invalid arguments (or m, rows or adapters of 0). */
+size_t gptq_lora_workspace_bytes(int64_t m, int64_t d, int64_t rows, int64_t adapters, int32_t rank);
+
+/*
+ * Sizes and strides of gptq_norm_rotate. Element (t, h, c) of a tensor x is at t * x_ld + h * x_hp + c:
+ * x_ld is the pitch of tokens, x_hp the pitch of heads (head_dim for heads side by side).
+ */
+typedef struct {
+  int64_t n;          /* tokens, >= 0 (0: nothing is queued)                                      */
+  int64_t q_ld, q_hp, k_ld, k_hp;                    /* pitches of q and k                        */
+  int64_t q_out_ld, q_out_hp, k_out_ld, k_out_hp;    /* pitches of the outputs                    */
+  double eps;         /* norm's epsilon, >= 0                                                     */
+  int32_t dtype;      /* of q, k and the outputs: GPTQ_F32, GPTQ_F16 or GPTQ_BF16                 */
+  int32_t w_dtype;    /* of the norm's weights                                                    */
+  int32_t q_heads;    /* 1..65535                                                                 */
+  int32_t k_heads;    /* 0..65535 (0: k and k_out are not used)                                   */
+  int32_t head_dim;   /* 1..1024                                                                  */
+  int32_t rotary_dim; /* rotated columns of each head: even, 0..head_dim (0: no rotation)         */
+  int32_t interleaved; /* 0: pair i is columns i and i + rotary_dim / 2; 1: columns 2i and 2i + 1 */
+  int32_t axes;       /* rows of positions, 1..64 (time, height, width: 3)                        */
+  int32_t norm;       /* 1: each head is divided by the root of its mean square (plus eps); 0: not */
+} gptq_norm_rotate_t;
+
+/*
+ * Per-head norm of queries and keys and their position rotation in one pass. For each head x of each
+ * token: y = x / sqrt(mean(x^2) + eps), times its weights (norm = 0: y = x), and pair i of the first
+ * rotary_dim columns, (a, b), becomes (a cos t - b sin t, b cos t + a sin t) with the angle
+ * t = positions[axis of pair i][token] * inv_freq[i].
+ *
+ *   q, k          device arrays, not modified (k is not used with k_heads = 0).
+ *   q_weight      device array of w_dtype [head_dim] (k_weight the same), or NULL: ones. With norm = 0
+ *                 both must be NULL.
+ *   positions     device int32[axes * n], any values; inv_freq device float[rotary_dim / 2].
+ *   pair_axis     device int32[rotary_dim / 2], the row of positions each pair takes (clamped into
+ *                 [0, axes)), or NULL: row 0. positions, inv_freq and pair_axis are not used with
+ *                 rotary_dim = 0.
+ *   q_out, k_out  device arrays, output; each may be its input itself with the same pitches (in place),
+ *                 and may otherwise share no element with q, k or the other output (column ranges of one
+ *                 array with one token pitch are apart). Heads and tokens of an output must not overlap.
+ * The angle is formed in 64 bits, so far positions lose nothing; sums and products are fp32, rounded
+ * once to dtype. 16-byte accesses are used where columns, pitches and pointers allow them.
+ */
+gptq_status_t gptq_norm_rotate(const gptq_norm_rotate_t *a, const void *q, const void *k, const void *q_weight,
+                               const void *k_weight, const int32_t *positions, const float *inv_freq,
+                               const int32_t *pair_axis, void *q_out, void *k_out, void *stream);
+
+/* Sizes, strides and settings of gptq_attention; pitches as in gptq_norm_rotate_t. */
+typedef struct {
+  int64_t seqs;       /* sequences, >= 0 (0: nothing is queued)                                   */
+  int64_t n_q, n_kv;  /* rows of q and out, rows of k and v; 0..2^31 - 1                          */
+  int64_t q_ld, q_hp, k_ld, k_hp, v_ld, v_hp, out_ld, out_hp;
+  double scale;       /* score scale, finite (1 / sqrt(head_dim) as a rule)                       */
+  double softcap;     /* c > 0: scores become c tanh(score / c); 0: no cap                        */
+  int32_t dtype;      /* of q, k, v and out: GPTQ_F32, GPTQ_F16 or GPTQ_BF16                      */
+  int32_t q_heads;    /* 1..65535                                                                 */
+  int32_t kv_heads;   /* 1..65535, dividing q_heads: query head h reads head h / (q_heads / kv_heads) */
+  int32_t head_dim;   /* 1..1024                                                                  */
+  int32_t causal;     /* 1: a query sees the keys up to its own position; 0: all of its sequence's */
+} gptq_attention_t;
+
+/*
+ * Softmax attention over packed sequences. Sequence s holds rows [q_start[s], q_start[s + 1]) of q and
+ * rows [kv_start[s], kv_start[s + 1]) of k and v, lq and lk of them. Its queries are its last tokens:
+ * query i has position p = i + lk - lq (one new token against a cache: lq = 1). For key j of the same
+ * sequence:
+ *   score = scale * q . k_j, capped (softcap), minus slopes[head] * |p - j|
+ *   seen  = (j <= p, or j < prefix[s], or causal = 0), and, with documents, q_doc = kv_doc[j] >= 0
+ *   out   = sum of v_j exp(score) / sum of exp(score) over the keys that are seen
+ * A query that sees no key gets zeros. A key that is not seen takes no part, whatever k and v hold there
+ * (infinities and NaN included). Rows of out that belong to no sequence are left as they were.
+ *
+ *   q, k, v        device arrays, not modified (k and v may be NULL with n_kv = 0).
+ *   q_start        device int32[seqs + 1], ascending, or NULL: seqs equal ranges (n_q a multiple of seqs);
+ *   kv_start       the same for k and v. Values are clamped so that every access stays inside n_q and
+ *                  n_kv rows; ranges that overlap are computed more than once.
+ *   slopes         device float[q_heads], or NULL: no distance bias.
+ *   q_doc, kv_doc  device int32[n_q] and int32[n_kv], documents of queries and keys in any order, or both
+ *                  NULL. A negative document (padding) sees nothing and is not seen.
+ *   prefix         device int32[seqs]: the first prefix[s] keys are seen by every query of the sequence
+ *                  (with causal = 1; it changes nothing otherwise), or NULL.
+ *   out            device array, output; must not overlap q, k or v, nor its heads and tokens each other.
+ *   work           device workspace of work_bytes bytes (16-byte aligned), or NULL. With at least
+ *                  gptq_attention_workspace_bytes(a) bytes, long key ranges are split across workgroups
+ *                  when there are few queries and joined in key order; with less (or NULL) they are not.
+ *                  It must not be shared with a concurrent call, two captured graphs included.
+ * Scores, the softmax's maximum and sum and the output are fp32. Results do not depend on scheduling.
+ */
+gptq_status_t gptq_attention(const gptq_attention_t *a, const void *q, const void *k, const void *v,
+                             const int32_t *q_start, const int32_t *kv_start, const float *slopes,
+                             const int32_t *q_doc, const int32_t *kv_doc, const int32_t *prefix, void *out, void *work,
+                             size_t work_bytes, void *stream);
+
+/* Workspace bytes with which gptq_attention splits key ranges; 0 when it would not (or for invalid arguments). */
+size_t gptq_attention_workspace_bytes(const gptq_attention_t *a);
 
 /*
  * One pre-norm decoder block for gptq_quantize_block. The pages fix the order in which a block's

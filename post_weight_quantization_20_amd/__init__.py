@@ -4,6 +4,13 @@ The solver's steps are HIP kernels behind a C ABI (include/gptq.h, libgptq.so); 
 Python binding. Build the library with `python -m post_weight_quantization_20_amd.build`.
 """
 
+from .attention import (  # noqa: F401
+    gptq_attention,
+    gptq_attention_workspace_bytes,
+    gptq_lora_gemm,
+    gptq_lora_workspace_bytes,
+    gptq_norm_rotate,
+)
 from .solver import (  # noqa: F401
     BLOCK_LAYERS,
     GPTQ_BF16,

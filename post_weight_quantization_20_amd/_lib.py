@@ -38,6 +38,19 @@ class gptq_block_layer_t(ctypes.Structure):
                 ("perm", c_void_p), ("loss", c_void_p), ("w_dtype", c_int32)]
 
 
+class gptq_norm_rotate_t(ctypes.Structure):
+    _fields_ = ([(f, c_int64) for f in ("n", "q_ld", "q_hp", "k_ld", "k_hp", "q_out_ld", "q_out_hp", "k_out_ld",
+                                        "k_out_hp")] + [("eps", c_double)] +
+                [(f, c_int32) for f in ("dtype", "w_dtype", "q_heads", "k_heads", "head_dim", "rotary_dim",
+                                        "interleaved", "axes", "norm")])
+
+
+class gptq_attention_t(ctypes.Structure):
+    _fields_ = ([(f, c_int64) for f in ("seqs", "n_q", "n_kv", "q_ld", "q_hp", "k_ld", "k_hp", "v_ld", "v_hp",
+                                        "out_ld", "out_hp")] + [("scale", c_double), ("softcap", c_double)] +
+                [(f, c_int32) for f in ("dtype", "q_heads", "kv_heads", "head_dim", "causal")])
+
+
 # name -> (restype, argtypes), mirroring include/gptq.h
 SIGNATURES = {
     "gptq_hessian_accumulate": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_size_t,
@@ -61,6 +74,13 @@ SIGNATURES = {
                                        c_void_p]),
     "gptq_dequant_gemm": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int32, c_int32, c_void_p,
                                     c_void_p, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_int64, c_void_p]),
+    "gptq_lora_gemm": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                 c_int32, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                 c_size_t, c_void_p]),
+    "gptq_lora_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int64, c_int32]),
+    "gptq_norm_rotate": (c_int32, [ctypes.POINTER(gptq_norm_rotate_t)] + [c_void_p] * 10),
+    "gptq_attention": (c_int32, [ctypes.POINTER(gptq_attention_t)] + [c_void_p] * 11 + [c_size_t, c_void_p]),
+    "gptq_attention_workspace_bytes": (c_size_t, [ctypes.POINTER(gptq_attention_t)]),
     "gptq_block_workspace_bytes": (c_size_t, [ctypes.POINTER(gptq_block_shape_t), ctypes.POINTER(gptq_params_t)]),
     "gptq_quantize_block": (c_int32, [ctypes.POINTER(gptq_block_shape_t), c_void_p, c_int32,
                                       ctypes.POINTER(gptq_params_t), c_int32, ctypes.POINTER(gptq_block_layer_t),

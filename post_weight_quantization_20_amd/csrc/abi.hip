@@ -257,6 +257,143 @@ gptq_status_t gptq_dequant_gemm(const void* x, int32_t x_dtype, int64_t m, int64
 
 namespace {
 
+// A strided [tokens x heads x width] array of esz-byte elements.
+struct Tensor3 {
+  const void* p;
+  int64_t n, heads, width, ld, hp;
+  int64_t esz;
+  const char* begin() const { return static_cast<const char*>(p); }
+  int64_t bytes() const {
+    return n <= 0 || heads <= 0 ? 0 : ((n - 1) * ld + (heads - 1) * hp + width) * esz;
+  }
+};
+
+// Pitches are not negative, and the array's bytes stay far inside int64.
+bool pitches_ok(const Tensor3& t) {
+  constexpr int64_t most = (int64_t)1 << 56;
+  if (t.ld < 0 || t.ld > most || t.hp < 0 || t.hp > most) return false;
+  const __int128 span = (__int128)t.n * t.ld + (__int128)t.heads * t.hp + t.width;
+  return span * t.esz <= most;
+}
+
+// No two elements of an output share an address: tokens outside heads or heads outside tokens.
+bool elements_apart(const Tensor3& t) {
+  if (t.heads > 1 && t.hp < t.width) return false;
+  if (t.n > 1 && t.ld < t.width) return false;
+  if (t.heads <= 1 || t.n <= 1) return true;
+  return t.ld >= (t.heads - 1) * t.hp + t.width || t.hp >= (t.n - 1) * t.ld + t.width;
+}
+
+// True when the arrays can be seen to share no element: address ranges apart, or column ranges of
+// rows with one pitch that do not meet.
+bool apart(const Tensor3& a, const Tensor3& b) {
+  if (!a.bytes() || !b.bytes()) return true;
+  if (a.begin() + a.bytes() <= b.begin() || b.begin() + b.bytes() <= a.begin()) return true;
+  if (a.ld != b.ld || a.esz != b.esz || a.ld <= 0) return false;
+  const int64_t row = a.ld * a.esz, ra = ((a.heads - 1) * a.hp + a.width) * a.esz,
+                rb = ((b.heads - 1) * b.hp + b.width) * b.esz;
+  int64_t off = (b.begin() - a.begin()) % row;
+  if (off < 0) off += row;
+  return off >= ra && off + rb <= row;
+}
+
+bool same(const Tensor3& a, const Tensor3& b) {
+  return a.p == b.p && (a.ld == b.ld || a.n <= 1) && (a.hp == b.hp || a.heads <= 1);
+}
+
+int64_t elem_bytes(int32_t t) { return t == GPTQ_F32 ? 4 : 2; }
+
+bool attention_ok(const gptq_attention_t* a) {
+  if (!a || !dtype_ok(a->dtype) || a->seqs < 0 || a->seqs >= kMaxDim) return false;
+  if (a->n_q < 0 || a->n_q >= kMaxDim || a->n_kv < 0 || a->n_kv >= kMaxDim) return false;
+  if (a->q_heads < 1 || a->q_heads > 65535 || a->kv_heads < 1 || a->kv_heads > a->q_heads ||
+      a->q_heads % a->kv_heads != 0 || a->head_dim < 1 || a->head_dim > 1024)
+    return false;
+  if (a->causal != 0 && a->causal != 1) return false;
+  return std::isfinite(a->scale) && std::isfinite(a->softcap) && a->softcap >= 0.0;
+}
+
+}  // namespace
+
+size_t gptq_lora_workspace_bytes(int64_t m, int64_t d, int64_t rows, int64_t adapters, int32_t rank) {
+  if (m <= 0 || m > kMaxDim || d < 1 || d > kMaxDim || rows <= 0 || rows > kMaxDim || adapters <= 0 ||
+      adapters > kMaxDim || rank < 1 || rank > 256)
+    return 0;
+  return gptq::lora_workspace_bytes(m, d, rows, adapters, rank);
+}
+
+gptq_status_t gptq_lora_gemm(const void* x, int32_t dtype, int64_t m, int64_t ld_x, const void* A, const void* B,
+                             const int32_t* ranks, const float* scales, int64_t adapters, int32_t rank,
+                             const int32_t* index, int64_t rows, int64_t d, const float* base, int64_t ld_base,
+                             float* y, int64_t ld_y, void* work, size_t work_bytes, void* stream) {
+  if (m < 0 || m > kMaxDim || rows < 0 || rows > kMaxDim || d < 1 || d > kMaxDim || !dtype_ok(dtype)) return GPTQ_EINVAL;
+  if (adapters < 0 || adapters > kMaxDim || rank < 1 || rank > 256) return GPTQ_EINVAL;
+  if (ld_x < d || ld_x > kMaxDim || ld_y < rows || ld_y > kMaxDim) return GPTQ_EINVAL;
+  if (base && (ld_base < rows || ld_base > kMaxDim)) return GPTQ_EINVAL;
+  if (m == 0 || rows == 0) return GPTQ_OK;
+  if (!x || !index || !y || (adapters > 0 && (!A || !B || !work))) return GPTQ_EINVAL;
+  const Tensor3 ty{y, m, 1, rows, ld_y, 0, 4}, tb{base, m, 1, rows, ld_base, 0, 4};
+  if (base && !same(ty, tb) && !apart(ty, tb)) return GPTQ_EINVAL;
+  if (reinterpret_cast<uintptr_t>(work) % 16 != 0) return GPTQ_EINVAL;
+  if (adapters > 0 && work_bytes < gptq::lora_workspace_bytes(m, d, rows, adapters, rank)) return GPTQ_ENOMEM;
+  return hip_status(gptq::lora_gemm(x, dtype, m, ld_x, A, B, ranks, scales, adapters, rank, index, rows, d, base,
+                                    ld_base, y, ld_y, work, static_cast<hipStream_t>(stream)));
+}
+
+gptq_status_t gptq_norm_rotate(const gptq_norm_rotate_t* a, const void* q, const void* k, const void* q_weight,
+                               const void* k_weight, const int32_t* positions, const float* inv_freq,
+                               const int32_t* pair_axis, void* q_out, void* k_out, void* stream) {
+  if (!a || !dtype_ok(a->dtype) || !dtype_ok(a->w_dtype) || a->n < 0 || a->n >= kMaxDim) return GPTQ_EINVAL;
+  if (a->q_heads < 1 || a->q_heads > 65535 || a->k_heads < 0 || a->k_heads > 65535) return GPTQ_EINVAL;
+  if (a->head_dim < 1 || a->head_dim > 1024 || a->rotary_dim < 0 || a->rotary_dim > a->head_dim || a->rotary_dim % 2)
+    return GPTQ_EINVAL;
+  if ((a->interleaved != 0 && a->interleaved != 1) || (a->norm != 0 && a->norm != 1) || a->axes < 1 || a->axes > 64)
+    return GPTQ_EINVAL;
+  if (!std::isfinite(a->eps) || a->eps < 0.0 || (!a->norm && (q_weight || k_weight))) return GPTQ_EINVAL;
+  const int64_t esz = elem_bytes(a->dtype), hk = a->k_heads, dh = a->head_dim;
+  const Tensor3 q3{q, a->n, a->q_heads, dh, a->q_ld, a->q_hp, esz}, k3{k, a->n, hk, dh, a->k_ld, a->k_hp, esz},
+      qo{q_out, a->n, a->q_heads, dh, a->q_out_ld, a->q_out_hp, esz},
+      ko{k_out, a->n, hk, dh, a->k_out_ld, a->k_out_hp, esz};
+  if (!pitches_ok(q3) || !pitches_ok(qo) || (hk && (!pitches_ok(k3) || !pitches_ok(ko)))) return GPTQ_EINVAL;
+  if (a->n == 0) return GPTQ_OK;
+  if (!q || !q_out || (hk && (!k || !k_out))) return GPTQ_EINVAL;
+  if (a->rotary_dim && (!positions || !inv_freq)) return GPTQ_EINVAL;
+  if (!elements_apart(qo) || (!same(qo, q3) && !apart(qo, q3))) return GPTQ_EINVAL;
+  if (hk && (!elements_apart(ko) || (!same(ko, k3) && !apart(ko, k3)) || !apart(qo, ko) || !apart(qo, k3) ||
+             !apart(ko, q3)))
+    return GPTQ_EINVAL;
+  return hip_status(gptq::norm_rotate(*a, q, k, q_weight, k_weight, positions, inv_freq, pair_axis, q_out, k_out,
+                                      static_cast<hipStream_t>(stream)));
+}
+
+size_t gptq_attention_workspace_bytes(const gptq_attention_t* a) {
+  if (!attention_ok(a) || a->seqs == 0 || a->n_q == 0) return 0;
+  return gptq::attention_workspace_bytes(*a);
+}
+
+gptq_status_t gptq_attention(const gptq_attention_t* a, const void* q, const void* k, const void* v,
+                             const int32_t* q_start, const int32_t* kv_start, const float* slopes,
+                             const int32_t* q_doc, const int32_t* kv_doc, const int32_t* prefix, void* out, void* work,
+                             size_t work_bytes, void* stream) {
+  if (!attention_ok(a)) return GPTQ_EINVAL;
+  if ((q_doc == nullptr) != (kv_doc == nullptr) && a->n_kv > 0) return GPTQ_EINVAL;
+  const int64_t esz = elem_bytes(a->dtype), dh = a->head_dim;
+  const Tensor3 q3{q, a->n_q, a->q_heads, dh, a->q_ld, a->q_hp, esz},
+      k3{k, a->n_kv, a->kv_heads, dh, a->k_ld, a->k_hp, esz}, v3{v, a->n_kv, a->kv_heads, dh, a->v_ld, a->v_hp, esz},
+      o3{out, a->n_q, a->q_heads, dh, a->out_ld, a->out_hp, esz};
+  if (!pitches_ok(q3) || !pitches_ok(k3) || !pitches_ok(v3) || !pitches_ok(o3)) return GPTQ_EINVAL;
+  if (a->seqs == 0 || a->n_q == 0) return GPTQ_OK;
+  if (!q_start && a->n_q % a->seqs != 0) return GPTQ_EINVAL;
+  if (!kv_start && a->n_kv % a->seqs != 0) return GPTQ_EINVAL;
+  if (!q || !out || (a->n_kv > 0 && (!k || !v))) return GPTQ_EINVAL;
+  if (!elements_apart(o3) || !apart(o3, q3) || !apart(o3, k3) || !apart(o3, v3)) return GPTQ_EINVAL;
+  if (reinterpret_cast<uintptr_t>(work) % 16 != 0) return GPTQ_EINVAL;
+  return hip_status(gptq::attention(*a, q, k, v, q_start, kv_start, slopes, q_doc, kv_doc, prefix, out, work,
+                                    work ? work_bytes : 0, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
 bool block_shape_ok(const gptq_block_shape_t* sh) {
   if (!sh) return false;
   if (sh->hidden < 8 || sh->hidden > kMaxDim || sh->inter < 8 || sh->inter > kMaxDim) return false;

@@ -32,6 +32,12 @@ GPTQ_DEV float load_as_f32(const void* p, int dtype, int64_t idx) {
   return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[idx]);
 }
 
+// The C++ type of an element type, for kernels instantiated per type.
+template <int DT> struct ElemOf;
+template <> struct ElemOf<F32> { typedef float T; };
+template <> struct ElemOf<F16> { typedef _Float16 T; };
+template <> struct ElemOf<BF16> { typedef __bf16 T; };
+
 // ------------------------------------------------------------------ the quantization grid
 // Min/max grid of one group. Asymmetric: scale = max(wmax - wmin, 1e-8) / maxq,
 // zero = round(-wmin / scale) (GPTQ tools page, "A minimal Python sketch"; round half to even).
@@ -183,6 +189,24 @@ hipError_t permute_columns(const void* in, int64_t m, int64_t d, int64_t ld_in, 
 hipError_t dequant_gemm(const void* x, int dtype, int64_t m, int64_t ldx, const int32_t* packed, int bits, int dense,
                         const float* scales, const int32_t* zeros, const int32_t* gidx, int64_t rows, int64_t d,
                         int64_t g, float* y, int64_t ldy, hipStream_t s);
+
+// y = base + s_a (x A_a^T) B_a^T for rows that each name an adapter (see lora.hip).
+size_t lora_workspace_bytes(int64_t m, int64_t d, int64_t rows, int64_t adapters, int32_t rank);
+hipError_t lora_gemm(const void* x, int dtype, int64_t m, int64_t ldx, const void* A, const void* B,
+                     const int32_t* ranks, const float* scales, int64_t adapters, int32_t rank, const int32_t* index,
+                     int64_t rows, int64_t d, const float* base, int64_t ld_base, float* y, int64_t ldy, void* work,
+                     hipStream_t s);
+
+// Per-head norm and rotation of queries and keys (rotate.hip).
+hipError_t norm_rotate(const gptq_norm_rotate_t& r, const void* q, const void* k, const void* qw, const void* kw,
+                       const int32_t* pos, const float* inv_freq, const int32_t* pair_axis, void* qo, void* ko,
+                       hipStream_t s);
+
+// Attention over packed sequences (attention.hip).
+size_t attention_workspace_bytes(const gptq_attention_t& t);
+hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, const void* v, const int32_t* q_start,
+                     const int32_t* kv_start, const float* slopes, const int32_t* q_doc, const int32_t* kv_doc,
+                     const int32_t* prefix, void* out, void* work, size_t work_bytes, hipStream_t s);
 
 // ------------------------------------------------------------------ fp16 products (gemm_f16.hip)
 // C[M x N] = alpha A B^T + beta C with A [M x K], B [N x K] fp16 row-major (k contiguous); K a

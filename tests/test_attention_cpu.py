@@ -1,0 +1,199 @@
+"""Refusals of gptq_norm_rotate, gptq_attention and gptq_lora_gemm (C ABI and binding), and pins of their
+float64 oracle (CPU only: no call here launches a kernel)."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import attn_ref
+
+FAKE = 0x100000          # never dereferenced: every call below is rejected or has nothing to do
+EINVAL, ENOMEM = -1, -5
+
+
+def _lib():
+    from test_abi_cpu import _lib as load
+    return load()
+
+
+# ------------------------------------------------------------------------------------- norm_rotate
+
+def _rotate(over=None, **kw):
+    L = _lib()
+    d = dict(n=4, q_ld=64, q_hp=16, k_ld=32, k_hp=16, q_out_ld=64, q_out_hp=16, k_out_ld=32, k_out_hp=16, eps=1e-6,
+             dtype=1, w_dtype=0, q_heads=4, k_heads=2, head_dim=16, rotary_dim=16, interleaved=0, axes=1, norm=1)
+    d.update(kw)
+    p = dict(q=FAKE, k=2 * FAKE, q_weight=0, k_weight=0, positions=3 * FAKE, inv_freq=4 * FAKE, pair_axis=0,
+             q_out=5 * FAKE, k_out=6 * FAKE)
+    p.update(over or {})
+    a = L.gptq_norm_rotate_t(**d)
+    return L.lib().gptq_norm_rotate(ctypes.byref(a), *[ctypes.c_void_p(v) for v in p.values()], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=-1), dict(n=1 << 31), dict(dtype=3), dict(w_dtype=-1), dict(q_heads=0), dict(k_heads=-1),
+    dict(q_heads=70000), dict(head_dim=0), dict(head_dim=1025), dict(rotary_dim=18), dict(rotary_dim=-2),
+    dict(rotary_dim=7), dict(interleaved=2), dict(norm=2), dict(axes=0), dict(axes=65), dict(eps=-1.0),
+    dict(eps=float("nan")), dict(q_ld=-1), dict(q_hp=-1), dict(q_ld=1 << 60), dict(k_out_ld=-5),
+    dict(q_out_hp=8),              # heads of the output overlap
+    dict(q_out_ld=63),             # tokens of the output overlap
+], ids=str)
+def test_norm_rotate_rejects_settings(kw):
+    assert _rotate(**kw) == EINVAL
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=0), dict(k=0), dict(q_out=0), dict(k_out=0), dict(positions=0), dict(inv_freq=0),
+    dict(q_out=FAKE + 32),         # overlaps q without being q
+    dict(q_out=6 * FAKE),          # both outputs in one place
+    dict(k_out=FAKE),              # the key output over q
+], ids=str)
+def test_norm_rotate_rejects_pointers(over):
+    assert _rotate(over) == EINVAL
+
+
+def test_norm_rotate_weights_need_the_norm():
+    assert _rotate(dict(q_weight=7 * FAKE), norm=0) == EINVAL
+
+
+def test_norm_rotate_null_and_empty():
+    L = _lib()
+    assert L.lib().gptq_norm_rotate(None, *[ctypes.c_void_p(FAKE)] * 9, None) == EINVAL
+    assert _rotate(n=0) == 0
+    assert _rotate(dict(q=0, q_out=0), n=0) == 0
+
+
+# --------------------------------------------------------------------------------------- attention
+
+def _attention(over=None, work_bytes=0, **kw):
+    L = _lib()
+    d = dict(seqs=2, n_q=8, n_kv=8, q_ld=64, q_hp=16, k_ld=32, k_hp=16, v_ld=32, v_hp=16, out_ld=64, out_hp=16,
+             scale=0.25, softcap=0.0, dtype=1, q_heads=4, kv_heads=2, head_dim=16, causal=1)
+    d.update(kw)
+    p = dict(q=FAKE, k=2 * FAKE, v=3 * FAKE, q_start=0, kv_start=0, slopes=0, q_doc=0, kv_doc=0, prefix=0,
+             out=5 * FAKE, work=0)
+    p.update(over or {})
+    a = L.gptq_attention_t(**d)
+    return L.lib().gptq_attention(ctypes.byref(a), *[ctypes.c_void_p(v) for v in p.values()], work_bytes, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(seqs=-1), dict(seqs=1 << 31), dict(n_q=-1), dict(n_q=1 << 31), dict(n_kv=-1), dict(dtype=9), dict(q_heads=0),
+    dict(kv_heads=0), dict(kv_heads=3), dict(kv_heads=8), dict(head_dim=0), dict(head_dim=1025), dict(causal=2),
+    dict(scale=float("inf")), dict(scale=float("nan")), dict(softcap=-1.0), dict(softcap=float("nan")),
+    dict(q_ld=-1), dict(v_hp=-1), dict(k_ld=1 << 60), dict(out_hp=15), dict(out_ld=32),
+    dict(seqs=3),                  # equal ranges need a multiple
+    dict(n_kv=9),
+], ids=str)
+def test_attention_rejects_settings(kw):
+    assert _attention(**kw) == EINVAL
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(q_doc=FAKE), dict(kv_doc=FAKE), dict(out=FAKE),
+    dict(out=2 * FAKE + 8), dict(out=3 * FAKE), dict(work=FAKE + 4),
+], ids=str)
+def test_attention_rejects_pointers(over):
+    assert _attention(over) == EINVAL
+
+
+def test_attention_empty():
+    assert _attention(dict(q=0, out=0), seqs=0) == 0
+    assert _attention(dict(q=0, out=0), n_q=0) == 0
+
+
+def test_attention_workspace_query():
+    L = _lib()
+    f = L.lib().gptq_attention_workspace_bytes
+    assert f(None) == 0
+    a = L.gptq_attention_t(seqs=1, n_q=8, n_kv=8, q_heads=4, kv_heads=3, head_dim=16)
+    assert f(ctypes.byref(a)) == 0
+
+
+# -------------------------------------------------------------------------------------------- lora
+
+def _lora(**kw):
+    L = _lib()
+    d = dict(x=FAKE, dtype=1, m=4, ld_x=64, A=2 * FAKE, B=3 * FAKE, ranks=0, scales=0, adapters=2, rank=8,
+             index=4 * FAKE, rows=32, d=64, base=0, ld_base=0, y=5 * FAKE, ld_y=32, work=6 * FAKE, work_bytes=1 << 20)
+    d.update(kw)
+    args = [ctypes.c_void_p(v) if n in ("x", "A", "B", "ranks", "scales", "index", "base", "y", "work") else v
+            for n, v in d.items()]
+    return L.lib().gptq_lora_gemm(*args, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=0), dict(A=0), dict(B=0), dict(index=0), dict(y=0), dict(work=0), dict(work=6 * FAKE + 8), dict(dtype=3),
+    dict(m=-1), dict(rows=-1), dict(d=0), dict(ld_x=63), dict(ld_y=31), dict(adapters=-1), dict(rank=0),
+    dict(rank=257), dict(base=7 * FAKE, ld_base=31), dict(base=5 * FAKE + 4, ld_base=32),
+    dict(base=5 * FAKE, ld_base=40),       # y's place with another pitch
+], ids=str)
+def test_lora_rejects(kw):
+    assert _lora(**kw) == EINVAL
+
+
+def test_lora_workspace():
+    L = _lib()
+    f = L.lib().gptq_lora_workspace_bytes
+    need = f(4, 64, 32, 2, 8)
+    assert need > 0
+    assert _lora(work_bytes=need - 1) == ENOMEM
+    for bad in ((0, 64, 32, 2, 8), (4, 0, 32, 2, 8), (4, 64, 0, 2, 8), (4, 64, 32, 0, 8), (4, 64, 32, 2, 0),
+                (4, 64, 32, 2, 257)):
+        assert f(*bad) == 0
+    assert _lora(m=0) == 0 and _lora(rows=0, ld_y=0) == 0
+
+
+# ----------------------------------------------------------------------------------------- binding
+
+def test_binding_wants_gpu_tensors():
+    torch = pytest.importorskip("torch")
+    import post_weight_quantization_20_amd as g
+    t = torch.zeros(2, 2, 4)
+    with pytest.raises(ValueError):
+        g.gptq_norm_rotate(t)
+    with pytest.raises(ValueError):
+        g.gptq_attention(t, t, t)
+    with pytest.raises(ValueError):
+        g.gptq_lora_gemm(t[0], t, t, torch.zeros(2, dtype=torch.int32))
+
+
+# ------------------------------------------------------------------------------------- oracle pins
+
+def test_oracle_rotation_by_hand():
+    """A quarter turn takes (a, b) to (-b, a); half a turn changes the sign; other columns stay."""
+    x = np.arange(1.0, 7.0).reshape(1, 1, 6)
+    pos = np.array([[1], [2]])
+    f = np.array([np.pi / 2, np.pi / 2])
+    out, _ = attn_ref.norm_rotate(x, None, pos, f, np.array([0, 1]), norm=False)
+    assert np.allclose(out[0, 0], [-3, -2, 1, -4, 5, 6])
+    out, _ = attn_ref.norm_rotate(x, None, pos, f, np.array([0, 1]), norm=False, interleaved=True)
+    assert np.allclose(out[0, 0], [-2, 1, -3, -4, 5, 6])
+    out, _ = attn_ref.norm_rotate(x[..., :2], np.array([2.0, 1.0]), eps=0.0)
+    assert np.allclose(out[0, 0], np.array([2.0, 2.0]) / np.sqrt(2.5))
+
+
+def test_oracle_attention_by_hand():
+    """Two keys with scores 0 and ln 3 weigh 1/4 and 3/4; masks take keys away; an empty row is zero."""
+    k = np.array([[[0.0]], [[np.log(3.0)]]])
+    v = np.array([[[4.0]], [[8.0]]])
+    q = np.ones((2, 1, 1))
+    seq = [(0, 2, 0, 2)]
+    assert np.allclose(attn_ref.attention(q, k, v, seq, 1.0)[0].ravel(), [4, 7])
+    assert np.allclose(attn_ref.attention(q, k, v, seq, 1.0, causal=False)[0].ravel(), [7, 7])
+    assert np.allclose(attn_ref.attention(q, k, v, seq, 1.0, prefix=[2])[0].ravel(), [7, 7])
+    d = np.array([0, -1])
+    assert np.allclose(attn_ref.attention(q, k, v, seq, 1.0, causal=False, q_doc=d, kv_doc=d)[0].ravel(), [4, 0])
+    # one step away with slope ln 3: the weights become equal for the first query
+    assert np.allclose(attn_ref.attention(q, k, v, seq, 1.0, causal=False, slopes=[np.log(3.0)])[0].ravel()[0], 6)
+    # a tiny cap makes all scores equal
+    assert np.allclose(attn_ref.attention(q, k, v, seq, 1.0, causal=False, softcap=1e-9)[0].ravel(), 6)
+
+
+def test_oracle_lora_by_hand():
+    x = np.array([[1.0, 2.0], [3.0, 4.0]])
+    A = np.array([[[1.0, 1.0], [5.0, 5.0]]])
+    B = np.array([[[2.0, 7.0]]])
+    y, _ = attn_ref.lora(x, A, B, [0, -1], scales=[0.5], ranks=[1], base=np.array([[10.0], [20.0]]))
+    assert np.allclose(y.ravel(), [13, 20])
