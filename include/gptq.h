@@ -395,7 +395,7 @@ gptq_status_t gptq_norm_rotate(const gptq_norm_rotate_t *a, const void *q, const
 /* Sizes, strides and settings of gptq_attention; pitches as in gptq_norm_rotate_t. */
 typedef struct {
   int64_t seqs;       /* sequences, >= 0 (0: nothing is queued)                                   */
-  int64_t n_q, n_kv;  /* rows of q and out, rows of k and v; 0..2^31 - 1                          */
+  int64_t n_q, n_kv;  /* rows of q and out, rows of k and v; 0..2^30                              */
   int64_t q_ld, q_hp, k_ld, k_hp, v_ld, v_hp, out_ld, out_hp;
   double scale;       /* score scale, finite (1 / sqrt(head_dim) as a rule)                       */
   double softcap;     /* c > 0: scores become c tanh(score / c); 0: no cap                        */
@@ -420,7 +420,7 @@ typedef struct {
  *   q, k, v        device arrays, not modified (k and v may be NULL with n_kv = 0).
  *   q_start        device int32[seqs + 1], ascending, or NULL: seqs equal ranges (n_q a multiple of seqs);
  *   kv_start       the same for k and v. Values are clamped so that every access stays inside n_q and
- *                  n_kv rows; ranges that overlap are computed more than once.
+ *                  n_kv rows. Key ranges may overlap; query ranges must not.
  *   slopes         device float[q_heads], or NULL: no distance bias.
  *   q_doc, kv_doc  device int32[n_q] and int32[n_kv], documents of queries and keys in any order, or both
  *                  NULL. A negative document (padding) sees nothing and is not seen.
@@ -432,6 +432,7 @@ typedef struct {
  *                  when there are few queries and joined in key order; with less (or NULL) they are not.
  *                  It must not be shared with a concurrent call, two captured graphs included.
  * Scores, the softmax's maximum and sum and the output are fp32. Results do not depend on scheduling.
+ * Returns GPTQ_EUNSUPPORTED for more than 2^24 tiles of 32 queries (times the shared heads' group).
  */
 gptq_status_t gptq_attention(const gptq_attention_t *a, const void *q, const void *k, const void *v,
                              const int32_t *q_start, const int32_t *kv_start, const float *slopes,

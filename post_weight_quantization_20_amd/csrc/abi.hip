@@ -30,7 +30,9 @@ gptq_status_t check_params(const gptq_params_t* p, int64_t d, bool quant) {
   return GPTQ_OK;
 }
 
-gptq_status_t hip_status(hipError_t e) { return e == hipSuccess ? GPTQ_OK : GPTQ_EHIP; }
+gptq_status_t hip_status(hipError_t e) {
+  return e == hipSuccess ? GPTQ_OK : e == hipErrorNotSupported ? GPTQ_EUNSUPPORTED : GPTQ_EHIP;
+}
 
 }  // namespace
 
@@ -305,7 +307,7 @@ int64_t elem_bytes(int32_t t) { return t == GPTQ_F32 ? 4 : 2; }
 
 bool attention_ok(const gptq_attention_t* a) {
   if (!a || !dtype_ok(a->dtype) || a->seqs < 0 || a->seqs >= kMaxDim) return false;
-  if (a->n_q < 0 || a->n_q >= kMaxDim || a->n_kv < 0 || a->n_kv >= kMaxDim) return false;
+  if (a->n_q < 0 || a->n_q > kMaxDim / 2 || a->n_kv < 0 || a->n_kv > kMaxDim / 2) return false;
   if (a->q_heads < 1 || a->q_heads > 65535 || a->kv_heads < 1 || a->kv_heads > a->q_heads ||
       a->q_heads % a->kv_heads != 0 || a->head_dim < 1 || a->head_dim > 1024)
     return false;

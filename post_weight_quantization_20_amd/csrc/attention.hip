@@ -9,6 +9,7 @@
 // not seen takes no part: whatever its k and v hold (infinities and NaN too) leaves o as it is.
 #include "common.hpp"
 
+#include <atomic>
 #include <cmath>
 
 namespace gptq {
@@ -26,6 +27,10 @@ struct AttnArgs {
   float scale, cap;
   const int32_t *q_start, *kv_start, *q_doc, *kv_doc, *prefix;
   const float* slopes;
+  int o_vec;                   // out takes 8-byte stores
+  int64_t tiles;               // row tiles of one key head, over all sequences (an upper bound)
+  int nsplit;                  // ranges that a sequence's keys are split into
+  float *part_ml, *part_o;     // nsplit > 1: [nsplit][nq][hq][2] and [nsplit][nq][hq][dh]
 };
 
 // The query and key ranges of a sequence. Offsets are clamped to the tokens there are.
@@ -67,27 +72,73 @@ GPTQ_DEV float wave_add(float v) {
   return v;
 }
 
-// One query and head by one wave, 64 keys at a time: a lane takes a key for the scores and columns
-// lane, lane + 64, ... for the output. Only keys that are seen are read into the output.
-template <int DT>
-GPTQ_DEV void attn_row(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i, int h, int lane) {
+// The keys a query may see end at this index: its own position or the prefix, whichever is later, and
+// nothing for a padding document.
+GPTQ_DEV int64_t key_limit_nodoc(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i) {
+  if (!a.causal) return sq.lk;
+  const int64_t p = i + sq.lk - sq.lq + 1, pre = a.prefix ? (int64_t)a.prefix[s] : 0;
+  return clamp64(p > pre ? p : pre, 0, sq.lk);
+}
+
+GPTQ_DEV int64_t key_limit(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i) {
+  if (a.q_doc && a.q_doc[sq.q0 + i] < 0) return 0;
+  return key_limit_nodoc(a, sq, s, i);
+}
+
+// Whether a sequence holds this row of q.
+GPTQ_DEV bool in_a_sequence(const AttnArgs& a, int64_t row, int lane) {
+  if (!a.q_start) return true;
+  for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
+    const int64_t s = s0 + lane;
+    bool in = false;
+    if (s < a.seqs) {
+      const int64_t q0 = clamp64(a.q_start[s], 0, a.nq);
+      in = row >= q0 && row < clamp64(a.q_start[s + 1], q0, a.nq);
+    }
+    if (__ballot(in)) return true;
+  }
+  return false;
+}
+
+// The XOR of a 16-byte unit's place in row `row` of a staged tile, for rows of UN units. K: eight rows in
+// a row put one unit in eight distinct places; V: four rows put a pair of units in four.
+template <int UN>
+GPTQ_DEV int swz_k(int row) {
+  return UN % 8 == 0 ? (row & 7) : ((row >> 1) & 3);
+}
+template <int UN>
+GPTQ_DEV int swz_v(int row) {
+  return UN % 8 == 0 ? 2 * (row & 3) : (row & 2);
+}
+
+GPTQ_DEV uint64_t uniform64(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v) |
+         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32;
+}
+
+// One query and head by one wave over keys [j0, j1), 64 at a time: a lane takes a key for the scores and
+// columns lane, lane + 64, ... of the output. Only keys that are seen are read into the output, so this is
+// also the exact path for a row whose tile held infinities or NaN that it may not see. NC: columns a lane.
+template <int DT, int NC>
+GPTQ_DEV void attn_row(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i, int h, int lane, int64_t j0, int64_t j1,
+                       float (&acc)[NC], float& m, float& l) {
   typedef typename ElemOf<DT>::T T;
   const T* q = static_cast<const T*>(a.q) + (sq.q0 + i) * a.q_ld + h * a.q_hp;
   const T* kb = static_cast<const T*>(a.k) + sq.k0 * a.k_ld + (h / a.group) * a.k_hp;
   const T* vb = static_cast<const T*>(a.v) + sq.k0 * a.v_ld + (h / a.group) * a.v_hp;
   const int64_t p = i + sq.lk - sq.lq;
-  const int64_t pre = a.prefix ? (int64_t)a.prefix[s] : 0;
   const int32_t doc = a.q_doc ? a.q_doc[sq.q0 + i] : 0;
   const float slope = a.slopes ? a.slopes[h] : 0.f;
-  float m = -INFINITY, l = 0.f, acc[kMaxHead / 64];
+  m = -INFINITY;
+  l = 0.f;
 #pragma unroll
-  for (int c = 0; c < kMaxHead / 64; ++c) acc[c] = 0.f;
-  int64_t end = a.causal ? (p + 1 > pre ? p + 1 : pre) : sq.lk;
-  end = end > sq.lk ? sq.lk : end;
-  for (int64_t j0 = 0; j0 < end; j0 += 64) {
-    const int64_t j = j0 + lane;
-    bool seen = j < end && (!a.causal || j <= p || j < pre);
-    if (seen && a.q_doc) seen = doc >= 0 && a.kv_doc[sq.k0 + j] == doc;
+  for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+  const int64_t lim = key_limit(a, sq, s, i);
+  const int64_t end = lim < j1 ? lim : j1;
+  for (int64_t jb = j0; jb < end; jb += 64) {
+    const int64_t j = jb + lane;
+    bool seen = j < end;
+    if (seen && a.q_doc) seen = a.kv_doc[sq.k0 + j] == doc;
     float sc = -INFINITY;
     if (seen) {
       float dot = 0.f;
@@ -96,51 +147,747 @@ GPTQ_DEV void attn_row(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i, i
       if (a.cap > 0.f) sc = a.cap * tanhf(sc / a.cap);
       if (a.slopes) sc -= slope * fabsf((float)(p - j));
     }
+    if (!__ballot(seen && !(sc == -INFINITY))) continue;
     const float mn = fmaxf(m, wave_max(sc));
-    const uint64_t any = __ballot(seen && !(sc == -INFINITY));
-    if (!any) continue;
     const float w = seen ? expf(sc - mn) : 0.f;
     const float f = expf(m - mn);
     m = mn;
     l = l * f + wave_add(w);
 #pragma unroll
-    for (int c = 0; c < kMaxHead / 64; ++c) acc[c] *= f;
+    for (int c = 0; c < NC; ++c) acc[c] *= f;
     const uint64_t vis = __ballot(seen);
     for (int e = 0; e < 64; ++e) {
       if (!((vis >> e) & 1)) continue;
       const float we = __shfl(w, e, 64);
-      const T* vr = vb + (j0 + e) * a.v_ld;
+      const T* vr = vb + (jb + e) * a.v_ld;
 #pragma unroll
-      for (int c = 0; c < kMaxHead / 64; ++c)
+      for (int c = 0; c < NC; ++c)
         if (c * 64 + lane < a.dh) acc[c] = __builtin_fmaf(we, (float)vr[c * 64 + lane], acc[c]);
     }
   }
-  T* o = static_cast<T*>(a.out) + (sq.q0 + i) * a.o_ld + h * a.o_hp;
+}
+
+template <int DT, int NC>
+GPTQ_DEV void store_row(const AttnArgs& a, int64_t row, int h, int lane, const float (&acc)[NC], float l) {
+  typedef typename ElemOf<DT>::T T;
+  T* o = static_cast<T*>(a.out) + row * a.o_ld + h * a.o_hp;
 #pragma unroll
-  for (int c = 0; c < kMaxHead / 64; ++c)
+  for (int c = 0; c < NC; ++c)
     if (c * 64 + lane < a.dh) o[c * 64 + lane] = (T)(l == 0.f ? 0.f : acc[c] / l);
 }
 
-// Waves over (sequence, query, head).
+// Heads wider than the matrix-core kernels take: waves over (sequence, query, head).
 template <int DT>
 __global__ __launch_bounds__(256) void attn_row_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t s = blockIdx.y;
-  const Seq sq = sequence(a, s);
-  const int64_t items = sq.lq * a.hq;
-  for (int64_t it = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); it < items; it += (int64_t)gridDim.x * 4)
-    attn_row<DT>(a, sq, s, it / a.hq, (int)(it % a.hq), lane);
+  for (int64_t s = blockIdx.y; s < a.seqs; s += gridDim.y) {
+    const Seq sq = sequence(a, s);
+    const int64_t items = sq.lq * a.hq;
+    for (int64_t it = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); it < items; it += (int64_t)gridDim.x * 4) {
+      float acc[kMaxHead / 64], m, l;
+      const int64_t i = it / a.hq;
+      const int h = (int)(it - i * a.hq);
+      attn_row<DT>(a, sq, s, i, h, lane, 0, sq.lk, acc, m, l);
+      store_row<DT>(a, sq.q0 + i, h, lane, acc, l);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ 16-bit types, matrix cores
+//
+// The query heads that share a key head are rows of one tile: packed row r of a sequence is query
+// r / group and head r % group, so a key tile is read once for all of them, and a single new token still
+// gives `group` rows. A wave owns 32 packed rows. Scores are formed transposed, S^T = K Q^T
+// (v_mfma_f32_32x32x16: lane l holds row l % 32 and, of each 8 keys, the four of its half l / 32), so that
+// the softmax of a row runs inside a lane and its mirror lane, and the probabilities, rounded to the 16-bit
+// type, are the next product's operand O^T += V^T P^T as they lie: the contraction takes the keys in the
+// order the lanes hold them, and the transposing LDS reads of V follow that order.
+//
+// Keys and values stream into LDS in 16-byte units (buffer_load ... lds), double-buffered; units of a row
+// are XOR-swizzled so that the operand reads of K (one unit of 32 rows) and the transposing reads of V
+// (four rows of two units) fall in distinct banks. Units beyond the head or the keys read as zero through
+// the descriptor's range. Tensors that are not 16-byte aligned are staged through registers instead.
+//
+// WM = 4: the four waves hold 128 rows and share tiles of 64 keys. WM = 1: up to 32 rows (few queries),
+// each wave takes its own tiles of 32 keys and the four partial results are joined in LDS.
+//
+// The maximum is raised only when a score exceeds it by 8 (in powers of two); probabilities are kept 2^7
+// larger, so they stay below 2^15 and small ones keep their bits in fp16. A masked key's probability is
+// an exact zero, but zero times an infinity or NaN in V is NaN: a row whose result is not finite is
+// computed again by attn_row, which reads the keys that are seen and no others.
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+#define GPTQ_LDS __attribute__((address_space(3)))
+
+GPTQ_DEV void dma16(i32x4 rsrc, uint32_t voff, uint32_t lds_addr) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds_addr)
+               : "memory");
+}
+
+// Buffer descriptor of n 16-bit elements from a wave-uniform address.
+GPTQ_DEV i32x4 descriptor(uint64_t base, int64_t n) {
+  const uint64_t b = uniform64(base);
+  return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), __builtin_amdgcn_readfirstlane((int)(2 * n)), 0x00020000};
+}
+
+template <int DT>
+GPTQ_DEV floatx16 mfma16(v8s a, v8s b, floatx16 c) {
+  if constexpr (DT == F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
+template <int DT>
+GPTQ_DEV v8s round8(const float* p) {
+  if constexpr (DT == F16) {
+    half8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (_Float16)p[i];
+    return __builtin_bit_cast(v8s, r);
+  } else {
+    bf16x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (__bf16)p[i];
+    return __builtin_bit_cast(v8s, r);
+  }
+}
+
+// The value of the lane 32 away.
+GPTQ_DEV float mirror(float v) { return __shfl_xor(v, 32, 64); }
+
+// Row tile t of a key head: its sequence and the tile's place in it (seq = -1: past the last tile).
+struct TileAt {
+  int64_t seq, tile;
+};
+
+GPTQ_DEV TileAt find_tile(const AttnArgs& a, int64_t t, int rows, int lane) {
+  TileAt r{-1, 0};
+  if (!a.q_start) {
+    const int64_t per = (a.nq / a.seqs * a.group + rows - 1) / rows;
+    if (per > 0 && t < per * a.seqs) r = {t / per, t % per};
+    return r;
+  }
+  int64_t before = 0;
+  for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
+    const int64_t s = s0 + lane;
+    int64_t n = 0;
+    if (s < a.seqs) {
+      const int64_t q0 = clamp64(a.q_start[s], 0, a.nq), q1 = clamp64(a.q_start[s + 1], q0, a.nq);
+      n = ((q1 - q0) * a.group + rows - 1) / rows;
+    }
+    int64_t sum = n;   // inclusive prefix sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t v = __shfl_up(sum, o, 64);
+      if (lane >= o) sum += v;
+    }
+    const uint64_t past = __ballot(before + sum > t);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      r.seq = s0 + at;
+      r.tile = t - (before + __shfl(sum, at, 64) - __shfl(n, at, 64));
+      return r;
+    }
+    before += __shfl(sum, 63, 64);
+  }
+  return r;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kShift = 7.0f, kRaise = 8.0f;
+
+// DHP: head width padded to 32. DMA: 16-byte aligned tensors. MODE 0: scores only scaled, 1: also capped,
+// biased (or scaled by zero).
+template <int DT, int DHP, int WM, bool DMA, int MODE>
+__global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_kernel(AttnArgs a) {
+  constexpr int KT = WM == 4 ? 64 : 32;         // keys of a tile
+  constexpr int NT = KT / 32, NF = DHP / 32, NK = DHP / 16;
+  constexpr int UN = DHP / 8;                   // 16-byte units of a row
+  constexpr int ROWB = DHP * 2, TILEB = KT * ROWB, BUFB = 2 * TILEB;
+  constexpr int LOADS = KT * UN / 64 / WM;      // units a lane stages of K (and of V)
+  constexpr int ROWS = 32 * WM;
+  extern __shared__ char smem_raw[];
+  GPTQ_LDS char* smem = (GPTQ_LDS char*)smem_raw;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  // small LDS area behind the tiles: documents of a tile per wave, tile masks
+  GPTQ_LDS char* tail = smem + (WM == 4 ? 2 * BUFB : 8 * BUFB);
+  GPTQ_LDS int32_t* docs = (GPTQ_LDS int32_t*)tail + 64 * wave;
+  GPTQ_LDS uint32_t* masks = (GPTQ_LDS uint32_t*)(tail + 1024);   // [wave]: 16 active bits, 16 whole bits
+
+  // the workgroup's key head, tile of rows and range of keys
+  const int64_t per_head = a.tiles * a.nsplit, nb = per_head * a.hk;
+  int64_t kvh, rem;
+  if (a.hk % 8 == 0) {   // workgroups go to the 8 XCDs in turn: each takes whole heads, which its L2 keeps
+    const int64_t idx = (int64_t)(blockIdx.x & 7) * (nb >> 3) + (blockIdx.x >> 3);
+    kvh = idx / per_head;
+    rem = idx - kvh * per_head;
+  } else {
+    rem = blockIdx.x / a.hk;
+    kvh = blockIdx.x - rem * a.hk;
+  }
+  const int64_t tord = rem / a.nsplit;
+  const int z = (int)(rem - tord * a.nsplit);
+  TileAt at = find_tile(a, a.tiles - 1 - tord, ROWS, lane);   // long (late) tiles first
+  at.seq = (int64_t)uniform64((uint64_t)at.seq);
+  at.tile = (int64_t)uniform64((uint64_t)at.tile);
+  if (at.seq < 0) return;
+  const Seq sq = sequence(a, at.seq);
+  const int64_t nrows = sq.lq * a.group, row0 = at.tile * ROWS;
+
+  // this lane's row
+  const int64_t r = row0 + (WM == 4 ? 32 * wave : 0) + col;
+  const bool live = r < nrows;
+  const int64_t qi = live ? r / a.group : 0;
+  const int g = live ? (int)(r - qi * a.group) : 0;
+  const int h = (int)kvh * a.group + g;
+  const int32_t lim = live ? (int32_t)key_limit(a, sq, at.seq, qi) : 0;
+  const int32_t qdoc = live && a.q_doc ? a.q_doc[sq.q0 + qi] : 0;
+  const int32_t pos = (int32_t)(qi + sq.lk - sq.lq);
+  float slope = 0.f;
+  if (MODE == 1 && a.slopes) slope = a.slopes[h];
+
+  // keys: the workgroup's range [kb, ke) and, per wave, where masking starts and ends
+  const int64_t last_row = (row0 + ROWS < nrows ? row0 + ROWS : nrows) - 1;
+  int64_t ke = key_limit_nodoc(a, sq, at.seq, last_row / a.group);
+  int64_t kb = 0;
+  if (a.nsplit > 1) {
+    const int64_t nt = (ke + KT - 1) / KT, per = (nt + a.nsplit - 1) / a.nsplit;
+    kb = z * per * KT;
+    if (ke > kb + per * KT) ke = kb + per * KT;
+  }
+  int32_t wmin = live ? lim : 0x7fffffff, wmax = lim, dmin = live && lim > 0 ? qdoc : 0x7fffffff,
+          dmax = live && lim > 0 ? qdoc : -1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    wmin = min(wmin, __shfl_xor(wmin, o, 64));
+    wmax = max(wmax, __shfl_xor(wmax, o, 64));
+    dmin = min(dmin, __shfl_xor(dmin, o, 64));
+    dmax = max(dmax, __shfl_xor(dmax, o, 64));
+  }
+  wmin = __builtin_amdgcn_readfirstlane(wmin);
+  wmax = __builtin_amdgcn_readfirstlane(wmax);
+  const bool one_doc = __builtin_amdgcn_readfirstlane(dmin == dmax);   // every live row of the wave
+  if (a.q_doc && WM == 4) {   // the workgroup's range of documents
+    if (lane == 0) {
+      docs[0] = dmin;
+      docs[1] = dmax;
+    }
+    __syncthreads();
+    for (int w = 0; w < 4; ++w) {
+      dmin = min(dmin, ((GPTQ_LDS int32_t*)tail)[64 * w]);
+      dmax = max(dmax, ((GPTQ_LDS int32_t*)tail)[64 * w + 1]);
+    }
+    __syncthreads();
+  }
+  dmin = __builtin_amdgcn_readfirstlane(dmin);
+  dmax = __builtin_amdgcn_readfirstlane(dmax);
+
+  typedef typename ElemOf<DT>::T T;
+  const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sq.k0 * a.k_ld + kvh * a.k_hp;
+  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sq.k0 * a.v_ld + kvh * a.v_hp;
+
+  // Q^T operand: row col, columns 16 ks + 8 half .. + 7; negated for a negative scale, so that the largest
+  // score is the largest product
+  v8s qf[NK];
+  {
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (sq.q0 + qi) * a.q_ld + h * a.q_hp;
+    const short flip = MODE == 0 && a.scale < 0.f ? (short)0x8000 : (short)0;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      const int c0 = 16 * ks + 8 * half;
+      v8s f = {};
+      if (live) {
+        if (DMA) {
+          if (c0 < a.dh) f = *reinterpret_cast<const v8s*>(qp + c0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c0 + e < a.dh) f[e] = (short)qp[c0 + e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] ^= flip;
+      qf[ks] = f;
+    }
+  }
+
+  // staging: load q of this wave fills 16-byte units 64 (q + LOADS wave') + lane of a tile
+  const int sub = WM == 4 ? wave : 0;
+  int srow[LOADS], ku[LOADS], vu[LOADS];
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const int unit = 64 * (LOADS * sub + i) + lane;
+    const int row = unit / UN, up = unit - row * UN;
+    srow[i] = row;
+    ku[i] = up ^ swz_k<UN>(row);
+    vu[i] = up ^ swz_v<UN>(row);
+  }
+  constexpr uint32_t OOB = 0x80000000u;   // beyond any descriptor's range: reads as zero
+  uint32_t kvo[LOADS], vvo[LOADS];
+  if (DMA) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      kvo[i] = ku[i] * 8 < a.dh ? (uint32_t)((srow[i] * a.k_ld + ku[i] * 8) * 2) : OOB;
+      vvo[i] = vu[i] * 8 < a.dh ? (uint32_t)((srow[i] * a.v_ld + vu[i] * 8) * 2) : OOB;
+    }
+  }
+  GPTQ_LDS char* base = smem + (WM == 4 ? 0 : wave * 2 * BUFB);
+  auto stage = [&](int64_t j0, int buf) {
+    const int64_t left = sq.lk - j0;
+    const int rows = left < KT ? (int)left : KT;
+    GPTQ_LDS char* kd = base + buf * BUFB + LOADS * sub * 1024;
+    GPTQ_LDS char* vd = kd + TILEB;
+    if (DMA) {
+      const uint64_t ka = (uint64_t)(uintptr_t)(kp + j0 * a.k_ld), va = (uint64_t)(uintptr_t)(vp + j0 * a.v_ld);
+      const i32x4 kr = descriptor(ka, (rows - 1) * a.k_ld + a.dh), vr = descriptor(va, (rows - 1) * a.v_ld + a.dh);
+      const uint32_t k32 = (uint32_t)(uintptr_t)kd, v32 = (uint32_t)(uintptr_t)vd;
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) dma16(kr, kvo[i], k32 + 1024 * i);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) dma16(vr, vvo[i], v32 + 1024 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        v8s kx = {}, vx = {};
+        if (srow[i] < rows) {
+          const uint16_t* ks = kp + (j0 + srow[i]) * a.k_ld;
+          const uint16_t* vs = vp + (j0 + srow[i]) * a.v_ld;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (ku[i] * 8 + e < a.dh) kx[e] = (short)ks[ku[i] * 8 + e];
+            if (vu[i] * 8 + e < a.dh) vx[e] = (short)vs[vu[i] * 8 + e];
+          }
+        }
+        *(GPTQ_LDS v8s*)(kd + 1024 * i + 16 * lane) = kx;
+        *(GPTQ_LDS v8s*)(vd + 1024 * i + 16 * lane) = vx;
+      }
+    }
+  };
+
+  // operand addresses inside a tile
+  int koff[4], voff[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) koff[i] = col * ROWB + (((2 * i + half) ^ swz_k<UN>(col)) << 4);
+  {
+    const int s = lane & 15, trow = 4 * half + (s >> 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      voff[i] = trow * ROWB + (((4 * i + 2 * ((lane >> 4) & 1) + ((s & 3) >> 1)) ^ swz_v<UN>(trow)) << 4) + 8 * (s & 1);
+  }
+
+  floatx16 acc[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) acc[f] = floatx16{};
+  float m = -INFINITY, l = 0.f;
+  const float c = MODE == 0 ? fabsf(a.scale) * kLog2e : kLog2e;
+  const float raise = kRaise / c;
+  const float inv_cap = a.cap > 0.f ? 1.0f / a.cap : 0.f;
+
+  auto compute = [&](int64_t j0, int buf, bool whole) {
+    GPTQ_LDS char* kt = base + buf * BUFB;
+    GPTQ_LDS char* vt = kt + TILEB;
+    floatx16 S[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      S[t] = floatx16{};
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        const v8s kf = *(GPTQ_LDS v8s*)(kt + 32 * t * ROWB + koff[ks & 3] + 128 * (ks >> 2));
+        S[t] = mfma16<DT>(kf, qf[ks], S[t]);
+      }
+    }
+    const int32_t jb = (int32_t)j0 + 4 * half;   // the key of register i of subtile t: jb + 32 t + 8 (i / 4) + i % 4
+    if (MODE == 1) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x = S[t][i] * a.scale;
+          if (a.cap > 0.f) {
+            // tanh y = 1 - 2 / (e^2y + 1)
+            const float e2 = __builtin_amdgcn_exp2f(x * inv_cap * (2.0f * kLog2e));
+            x = a.cap - 2.0f * a.cap * __builtin_amdgcn_rcpf(e2 + 1.0f);
+          }
+          if (a.slopes) x -= slope * fabsf((float)(pos - (jb + 32 * t + 8 * (i / 4) + i % 4)));
+          S[t][i] = x;
+        }
+    }
+    const bool doc_mask = a.q_doc && !(whole && one_doc);
+    if (j0 + KT > wmin || doc_mask) {
+      if (doc_mask) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int64_t j = j0 + 32 * t + col;
+          if (half == 0) docs[32 * t + col] = j < sq.lk ? a.kv_doc[sq.k0 + j] : -1;
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const i32x4 kd = *(GPTQ_LDS i32x4*)(docs + 32 * t + 8 * b + 4 * half);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (kd[e] != qdoc) S[t][4 * b + e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (jb + 32 * t + 8 * (i / 4) + i % 4 >= lim) S[t][i] = -INFINITY;
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, S[t][i]);
+    mx = fmaxf(mx, mirror(mx));
+    if (__ballot(!(mx <= m + raise))) {
+      const float m2 = fmaxf(m, mx);
+      const float f = m2 == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - m2) * c);
+      m = m2;
+      l *= f;
+#pragma unroll
+      for (int ft = 0; ft < NF; ++ft)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[ft][i] *= f;
+    }
+    const float off = kShift - (m == -INFINITY ? 0.f : m * c);
+    float p[NT][16];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[t][i], c, off));
+        l += p[t][i];
+      }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const v8s pf = round8<DT>(&p[t][8 * e]);
+#pragma unroll
+        for (int ft = 0; ft < NF; ++ft) {
+          GPTQ_LDS char* va = vt + (32 * t + 16 * e) * ROWB + voff[ft & 1] + 128 * (ft >> 1);
+          const v4s v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((GPTQ_LDS v4s*)va);
+          const v4s v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((GPTQ_LDS v4s*)(va + 8 * ROWB));
+          acc[ft] = mfma16<DT>(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7), pf, acc[ft]);
+        }
+      }
+  };
+
+  auto ready = [&]() {   // the staged tile is in LDS, and the other buffer is no longer read
+    if (DMA) {
+      if (WM == 4) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  };
+
+  // Tiles in order, 64 at a time (a block): with documents, the block's tiles that hold a document of the
+  // rows' range are found first, a quarter tile a thread. `ready` in the unaligned WM = 1 form is a workgroup
+  // barrier, so there every wave takes the same number of steps.
+  const int64_t step = WM == 4 ? KT : 4 * KT;
+  for (int64_t b0 = kb; b0 < ke; b0 += 64 * step) {
+    uint64_t active = ~0ull, whole = 0;
+    const int64_t left = (ke - b0 + step - 1) / step;
+    if (left < 64) active = (1ull << left) - 1;
+    if (a.q_doc && WM == 4) {
+      const int64_t j0 = b0 + 16 * (int64_t)threadIdx.x;
+      int32_t lo = 0x7fffffff, hi = (int32_t)0x80000000;
+      for (int e = 0; e < 16; ++e)
+        if (j0 + e < ke) {
+          const int32_t d = a.kv_doc[sq.k0 + j0 + e];
+          lo = min(lo, d);
+          hi = max(hi, d);
+        }
+      lo = min(lo, __shfl_xor(lo, 1, 64));
+      hi = max(hi, __shfl_xor(hi, 1, 64));
+      lo = min(lo, __shfl_xor(lo, 2, 64));
+      hi = max(hi, __shfl_xor(hi, 2, 64));
+      uint64_t on = __ballot(lo <= dmax && hi >= dmin), full = __ballot(lo == hi && lo == dmin && dmin == dmax);
+      // one bit of each four
+      uint32_t b_on = 0, b_full = 0;
+      for (int e = 0; e < 16; ++e) {
+        b_on |= (uint32_t)((on >> (4 * e)) & 1) << e;
+        b_full |= (uint32_t)((full >> (4 * e)) & 1) << e;
+      }
+      __syncthreads();
+      if (lane == 0) masks[wave] = b_on | (b_full << 16);
+      __syncthreads();
+      uint64_t m_on = 0, m_full = 0;
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t v = masks[w];
+        m_on |= (uint64_t)(v & 0xffffu) << (16 * w);
+        m_full |= (uint64_t)(v >> 16) << (16 * w);
+      }
+      active &= m_on;
+      whole = m_full;
+    }
+    active = uniform64(active);
+    whole = uniform64(whole);
+    if (!active) continue;
+    const int64_t my = WM == 4 ? 0 : wave * KT;   // WM = 1: the wave's tile of each step
+    auto tile_of = [&](int t) { return b0 + t * step + my; };
+    auto exists = [&](int t) { return WM == 4 || tile_of(t) < ke; };
+    int t = __builtin_ctzll(active), buf = 0;
+    // every wave is done with both buffers (of the block before)
+    if (WM == 4 || !DMA) __syncthreads();
+    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (exists(t)) stage(tile_of(t), 0);
+    while (true) {
+      const int64_t j0 = tile_of(t);
+      const bool have = exists(t), full = (whole >> t) & 1;
+      active &= active - 1;
+      ready();
+      if (active) {
+        t = __builtin_ctzll(active);
+        if (exists(t)) stage(tile_of(t), buf ^ 1);
+      }
+      if (have && j0 < wmax) compute(j0, buf, full);
+      if (!active) break;
+      buf ^= 1;
+    }
+  }
+  l += mirror(l);
+
+  if (WM == 1) {
+    // join the waves' partial results in wave order; the tiles' area is free now
+    __syncthreads();
+    GPTQ_LDS float* sh = (GPTQ_LDS float*)smem;
+    constexpr int PITCH = 64 * (16 * NF + 1);
+    GPTQ_LDS float* mine = sh + (wave & 1) * PITCH;
+    GPTQ_LDS float* ml = (GPTQ_LDS float*)tail;
+    if (half == 0) {
+      ml[64 * wave + col] = m;
+      ml[64 * wave + 32 + col] = l;
+    }
+    __syncthreads();
+    float mj = m;
+    for (int w = 0; w < 4; ++w) mj = fmaxf(mj, ml[64 * w + col]);
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - mj) * c);
+    l = 0.f;
+    for (int w = 0; w < 4; ++w) {
+      const float mw = ml[64 * w + col];
+      l += mw == -INFINITY ? 0.f : ml[64 * w + 32 + col] * __builtin_amdgcn_exp2f((mw - mj) * c);
+    }
+    m = mj;
+#pragma unroll
+    for (int ft = 0; ft < NF; ++ft)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[ft][i] *= f;
+    // (0 + 2) and (1 + 3), then the two sums
+    for (int round = 0; round < 2; ++round) {
+      const bool give = round == 0 ? wave >= 2 : wave == 1, take = round == 0 ? wave < 2 : wave == 0;
+      if (give) {
+#pragma unroll
+        for (int ft = 0; ft < NF; ++ft)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[(16 * ft + i) * 64 + lane] = acc[ft][i];
+      }
+      __syncthreads();
+      if (take) {
+        GPTQ_LDS float* other = round == 0 ? mine : sh + PITCH;
+#pragma unroll
+        for (int ft = 0; ft < NF; ++ft)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[ft][i] += other[(16 * ft + i) * 64 + lane];
+      }
+      __syncthreads();
+    }
+    if (wave != 0) return;
+  }
+
+  // rows whose sum is not finite: computed again without the keys they do not see
+  bool odd = !(fabsf(l) < INFINITY);
+#pragma unroll
+  for (int ft = 0; ft < NF; ++ft)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) odd |= !(fabsf(acc[ft][i]) < INFINITY);
+  uint32_t redo = 0;
+  {
+    const uint64_t o = __ballot(odd && live);
+    redo = (uint32_t)o | (uint32_t)(o >> 32);
+  }
+  const float mexp = m == -INFINITY ? -INFINITY : m * c - kShift;   // O and l are in units of 2^mexp
+  if (live && !((redo >> col) & 1)) {
+    const int64_t row = sq.q0 + qi;
+    if (a.nsplit > 1) {
+      const int64_t pr = ((int64_t)z * a.nq + row) * a.hq + h;
+      if (half == 0) {
+        a.part_ml[2 * pr] = mexp;
+        a.part_ml[2 * pr + 1] = l;
+      }
+      float* po = a.part_o + pr * a.dh;
+#pragma unroll
+      for (int ft = 0; ft < NF; ++ft)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int f = 32 * ft + 8 * b + 4 * half + e;
+            if (f < a.dh) po[f] = acc[ft][4 * b + e];
+          }
+    } else {
+      T* po = static_cast<T*>(a.out) + row * a.o_ld + h * a.o_hp;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      const bool vec = DMA && a.o_vec;
+#pragma unroll
+      for (int ft = 0; ft < NF; ++ft)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int f = 32 * ft + 8 * b + 4 * half;
+          typedef T T4 __attribute__((ext_vector_type(4)));
+          T4 o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = (T)(acc[ft][4 * b + e] * inv);
+          if (vec) {
+            if (f < a.dh) *reinterpret_cast<T4*>(po + f) = o;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (f + e < a.dh) po[f + e] = o[e];
+          }
+        }
+    }
+  }
+  while (redo) {
+    const int rr = __builtin_ctz(redo);
+    redo &= redo - 1;
+    const int64_t rw = __shfl(r, rr, 64);
+    const int64_t i2 = rw / a.group;
+    const int h2 = (int)kvh * a.group + (int)(rw - i2 * a.group);
+    constexpr int NC = (DHP + 63) / 64;
+    float ar[NC], m2, l2;
+    attn_row<DT>(a, sq, at.seq, i2, h2, lane, kb, ke, ar, m2, l2);
+    if (a.nsplit > 1) {
+      const int64_t pr = ((int64_t)z * a.nq + sq.q0 + i2) * a.hq + h2;
+      if (lane == 0) {
+        a.part_ml[2 * pr] = m2 * kLog2e;
+        a.part_ml[2 * pr + 1] = l2;
+      }
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+        if (64 * cc + lane < a.dh) a.part_o[pr * a.dh + 64 * cc + lane] = ar[cc];
+    } else {
+      store_row<DT>(a, sq.q0 + i2, h2, lane, ar, l2);
+    }
+  }
+}
+
+// Joins the key ranges of each row, in order: one wave per (query, head), columns over the lanes.
+template <int DT>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  typedef typename ElemOf<DT>::T T;
+  const int lane = threadIdx.x & 63;
+  const int64_t total = a.nq * a.hq;
+  for (int64_t it = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); it < total; it += (int64_t)gridDim.x * 4) {
+    const int64_t row = it / a.hq;
+    if (!in_a_sequence(a, row, lane)) continue;
+    const int h = (int)(it - row * a.hq);
+    float m = -INFINITY, l = 0.f;
+    for (int z = 0; z < a.nsplit; ++z) m = fmaxf(m, a.part_ml[2 * ((int64_t)z * total + it)]);
+    constexpr int NC = 4;
+    float acc[NC] = {};
+    for (int z = 0; z < a.nsplit; ++z) {
+      const int64_t pr = (int64_t)z * total + it;
+      const float mz = a.part_ml[2 * pr], lz = a.part_ml[2 * pr + 1];
+      if (mz == -INFINITY && lz == 0.f) continue;   // a range that the row does not see
+      const float f = __builtin_amdgcn_exp2f(mz - m);
+      l += lz * f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        if (64 * c + lane < a.dh) acc[c] += a.part_o[pr * a.dh + 64 * c + lane] * f;
+    }
+    T* o = static_cast<T*>(a.out) + row * a.o_ld + h * a.o_hp;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (64 * c + lane < a.dh) o[64 * c + lane] = (T)(l == 0.f ? 0.f : acc[c] / l);
+  }
+}
+
+template <int DT, int DHP, int WM, bool DMA, int MODE>
+hipError_t launch_mfma(const AttnArgs& a, hipStream_t s) {
+  constexpr size_t tile = (size_t)(WM == 4 ? 64 : 32) * DHP * 2;
+  constexpr size_t lds = 2 * 2 * tile * (WM == 4 ? 1 : 4) + 1024 + 64;
+  auto f = attn_mfma_kernel<DT, DHP, WM, DMA, MODE>;
+  // the LDS beyond 64 KB is asked for once per device
+  static std::atomic<uint64_t> asked{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if (lds > 65536 && (dev > 63 || !(asked.load() & bit))) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    asked |= bit;
+  }
+  hipLaunchKernelGGL(f, dim3((unsigned)(a.tiles * a.hk * a.nsplit)), dim3(256), lds, s, a);
+  return hipGetLastError();
+}
+
+template <int DT, int DHP, int WM>
+hipError_t by_mode(const AttnArgs& a, bool dma, bool extra, hipStream_t s) {
+  if (dma) return extra ? launch_mfma<DT, DHP, WM, true, 1>(a, s) : launch_mfma<DT, DHP, WM, true, 0>(a, s);
+  return launch_mfma<DT, DHP, WM, false, 1>(a, s);
+}
+
+template <int DT>
+hipError_t by_head(const AttnArgs& a, bool dma, bool extra, bool few, hipStream_t s) {
+  // few rows: each wave needs its own double buffer, which 160 KB of LDS holds up to 128-wide heads
+  if (few) {
+    if (a.dh <= 64) return by_mode<DT, 64, 1>(a, dma, extra, s);
+    if (a.dh <= 96) return by_mode<DT, 96, 1>(a, dma, extra, s);
+    return by_mode<DT, 128, 1>(a, dma, extra, s);
+  }
+  if (a.dh <= 64) return by_mode<DT, 64, 4>(a, dma, extra, s);
+  if (a.dh <= 96) return by_mode<DT, 96, 4>(a, dma, extra, s);
+  if (a.dh <= 128) return by_mode<DT, 128, 4>(a, dma, extra, s);
+  return by_mode<DT, 256, 4>(a, dma, extra, s);
+}
+
+// The launch's plan: rows a tile holds, tiles, ranges that keys are split into.
+struct Plan {
+  bool mfma, few;
+  int64_t tiles;
+  int nsplit;
+};
+
+Plan plan(const gptq_attention_t& t) {
+  Plan p{};
+  p.mfma = t.dtype != GPTQ_F32 && t.head_dim <= 256;
+  if (!p.mfma) return p;
+  const int64_t group = t.q_heads / t.kv_heads;
+  // sequences of at most 32 packed rows on average: the four waves split the keys instead of the rows
+  p.few = t.head_dim <= 128 && t.n_q * group <= 32 * t.seqs;
+  const int64_t rows = p.few ? 32 : 128;
+  p.tiles = t.n_q * group / rows + t.seqs;
+  // Fewer than two workgroups a CU: split the keys until there are about four, in ranges of at least
+  // 256 keys (of the average sequence).
+  const int64_t items = p.tiles * t.kv_heads, keys = t.n_kv / t.seqs;
+  p.nsplit = 1;
+  if (items < 512) p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>((1024 + items - 1) / items, keys / 256));
+  return p;
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(const gptq_attention_t&) { return 0; }
+size_t attention_workspace_bytes(const gptq_attention_t& t) {
+  const Plan p = plan(t);
+  if (!p.mfma || p.nsplit <= 1) return 0;
+  return (size_t)p.nsplit * t.n_q * t.q_heads * (t.head_dim + 2) * sizeof(float);
+}
 
 hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, const void* v, const int32_t* q_start,
                      const int32_t* kv_start, const float* slopes, const int32_t* q_doc, const int32_t* kv_doc,
                      const int32_t* prefix, void* out, void* work, size_t work_bytes, hipStream_t s) {
-  (void)work;
-  (void)work_bytes;
   AttnArgs a{};
   a.q = q; a.k = k; a.v = v; a.out = out;
   a.q_ld = t.q_ld; a.k_ld = t.k_ld; a.v_ld = t.v_ld; a.o_ld = t.out_ld;
@@ -150,11 +897,37 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
   a.causal = t.causal; a.scale = (float)t.scale; a.cap = (float)t.softcap;
   a.q_start = q_start; a.kv_start = kv_start; a.q_doc = q_doc; a.kv_doc = kv_doc; a.prefix = prefix;
   a.slopes = slopes;
-  const int64_t waves = a.nq * a.hq;
-  const dim3 grid((unsigned)std::min<int64_t>((waves + 3) / 4, 4096), (unsigned)t.seqs);
-  if (t.dtype == F32) hipLaunchKernelGGL(attn_row_kernel<F32>, grid, dim3(256), 0, s, a);
-  else if (t.dtype == F16) hipLaunchKernelGGL(attn_row_kernel<F16>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(attn_row_kernel<BF16>, grid, dim3(256), 0, s, a);
+  Plan p = plan(t);
+  if (!p.mfma) {
+    const int64_t waves = a.nq * a.hq;
+    const dim3 grid((unsigned)std::min<int64_t>((waves + 3) / 4, 4096), (unsigned)std::min<int64_t>(t.seqs, 4096));
+    if (t.dtype == F32) hipLaunchKernelGGL(attn_row_kernel<F32>, grid, dim3(256), 0, s, a);
+    else if (t.dtype == F16) hipLaunchKernelGGL(attn_row_kernel<F16>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(attn_row_kernel<BF16>, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  const size_t need = attention_workspace_bytes(t);
+  if (!work || work_bytes < need) p.nsplit = 1;
+  a.tiles = p.tiles;
+  a.nsplit = p.nsplit;
+  if (p.nsplit > 1) {
+    a.part_ml = static_cast<float*>(work);
+    a.part_o = a.part_ml + (int64_t)p.nsplit * a.nq * a.hq * 2;
+  }
+  if (a.tiles * a.hk * a.nsplit >= ((int64_t)1 << 24)) return hipErrorNotSupported;   // a grid's 2^32 threads
+  // 16-byte units: pointers, pitches and head width multiples of 8 elements, and a tile inside 31-bit offsets
+  auto al = [&](const void* ptr, int64_t ld, int64_t hp) {
+    return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0 && hp % 8 == 0;
+  };
+  const bool dma = a.dh % 8 == 0 && al(q, a.q_ld, a.q_hp) && al(k, a.k_ld, a.k_hp) && al(v, a.v_ld, a.v_hp) &&
+                   std::max(a.k_ld, a.v_ld) < ((int64_t)1 << 23);
+  a.o_vec = reinterpret_cast<uintptr_t>(out) % 8 == 0 && a.o_ld % 4 == 0 && a.o_hp % 4 == 0;
+  const bool extra = a.cap > 0.f || a.slopes || a.scale == 0.f;
+  hipError_t e = t.dtype == F16 ? by_head<F16>(a, dma, extra, p.few, s) : by_head<BF16>(a, dma, extra, p.few, s);
+  if (e != hipSuccess || p.nsplit <= 1) return e;
+  const dim3 grid((unsigned)std::min<int64_t>((a.nq * a.hq + 3) / 4, 65536));
+  if (t.dtype == F16) hipLaunchKernelGGL(attn_join_kernel<F16>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(attn_join_kernel<BF16>, grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
