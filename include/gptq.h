@@ -332,14 +332,14 @@ gptq_status_t gptq_dequant_gemm(const void *x, int32_t x_dtype, int64_t m, int64
  *   scales   device float[adapters], or NULL: 1.
  *   adapters >= 0; rank 1..256.
  *   index    device int32[m], in any order; rows may share an adapter.
- *   rows     outputs, >= 0 (0: nothing is queued); d input features, >= 1.
+ *   rows     outputs, 0..2^24 (0: nothing is queued); d input features, >= 1.
  *   base     device float[m x ld_base], ld_base >= rows, or NULL: zeros. May be y itself with the same
  *            pitch (added in place), or not overlap it; another overlap is GPTQ_EINVAL.
  *   y        device float[m x ld_y], output, ld_y >= rows. Must not overlap the other arrays.
  *   work     device workspace of at least gptq_lora_workspace_bytes(m, d, rows, adapters, rank) bytes,
  *            not shared with a concurrent call; 16-byte aligned.
  * Products of x and A are exact in fp32 (fp16 and bf16), T and all sums are fp32. Results do not depend
- * on scheduling. Two launches on `stream`; the call may be captured in a graph.
+ * on scheduling. Launches on `stream` alone; the call may be captured in a graph.
  */
 gptq_status_t gptq_lora_gemm(const void *x, int32_t dtype, int64_t m, int64_t ld_x, const void *A, const void *B,
                              const int32_t *ranks, const float *scales, int64_t adapters, int32_t rank,

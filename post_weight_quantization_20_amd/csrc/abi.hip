@@ -317,8 +317,10 @@ bool attention_ok(const gptq_attention_t* a) {
 
 }  // namespace
 
+static constexpr int64_t kMaxRows = (int64_t)1 << 24;   // gptq_lora_gemm's outputs
+
 size_t gptq_lora_workspace_bytes(int64_t m, int64_t d, int64_t rows, int64_t adapters, int32_t rank) {
-  if (m <= 0 || m > kMaxDim || d < 1 || d > kMaxDim || rows <= 0 || rows > kMaxDim || adapters <= 0 ||
+  if (m <= 0 || m > kMaxDim || d < 1 || d > kMaxDim || rows <= 0 || rows > kMaxRows || adapters <= 0 ||
       adapters > kMaxDim || rank < 1 || rank > 256)
     return 0;
   return gptq::lora_workspace_bytes(m, d, rows, adapters, rank);
@@ -328,7 +330,7 @@ gptq_status_t gptq_lora_gemm(const void* x, int32_t dtype, int64_t m, int64_t ld
                              const int32_t* ranks, const float* scales, int64_t adapters, int32_t rank,
                              const int32_t* index, int64_t rows, int64_t d, const float* base, int64_t ld_base,
                              float* y, int64_t ld_y, void* work, size_t work_bytes, void* stream) {
-  if (m < 0 || m > kMaxDim || rows < 0 || rows > kMaxDim || d < 1 || d > kMaxDim || !dtype_ok(dtype)) return GPTQ_EINVAL;
+  if (m < 0 || m > kMaxDim || rows < 0 || rows > kMaxRows || d < 1 || d > kMaxDim || !dtype_ok(dtype)) return GPTQ_EINVAL;
   if (adapters < 0 || adapters > kMaxDim || rank < 1 || rank > 256) return GPTQ_EINVAL;
   if (ld_x < d || ld_x > kMaxDim || ld_y < rows || ld_y > kMaxDim) return GPTQ_EINVAL;
   if (base && (ld_base < rows || ld_base > kMaxDim)) return GPTQ_EINVAL;

@@ -1,19 +1,33 @@
 // Low-rank adapters of many requests beside a shared projection.
 //
 // Row i of x names adapter a = index[i]:  y_i = base_i + s_a B_a (A_a x_i),  A_a [r x d], B_a [rows x r];
-// a row that names none takes base_i. Two steps: T = x A^T (shrink_kernel) and y = base + s T B^T
-// (expand_kernel). T and all sums are fp32; nothing is rounded to fewer bits.
+// a row that names none takes base_i. Two launches: T = x A^T (shrink_kernel), y = base + s T B^T
+// (expand_kernel). What the pass has to move is x, the adapters in use, base and y; at 2 r (d + rows) flops
+// a row it is bound by those bytes, or by the two launches' latency for a few rows.
+//
+// Rows stay in their order (no sort): a workgroup takes 16 or more consecutive rows, lists the distinct
+// adapters they name (its slots, in order of first row) and forms each slot's product for all its rows,
+// keeping it for the rows that name the slot. Rows of one prompt share an adapter, so a tile has one or two
+// slots; a batch of single tokens has up to 16, whose products are bound by reading the adapters and are
+// shared out over waves (expand) and workgroups (shrink).
+//
+// shrink: 16-bit products on v_mfma_f32_16x16x32 (exact products, fp32 sums), fp32 ones on
+// v_mfma_f32_16x16x4, operands straight from memory (both run along d). The d axis is split over the waves
+// of a workgroup (joined in LDS in wave order) and, while there are few workgroups, over the grid; expand
+// adds the grid's partial sums in order. expand: fp32 MFMA, so T is never rounded to 16 bits: with r <= 256
+// the product is small beside y's bytes. Nothing depends on scheduling.
 #include "common.hpp"
 
 namespace gptq {
 namespace {
+
+typedef short v8s __attribute__((ext_vector_type(8)));
 
 struct LoraArgs {
   const void* x;
   int64_t ldx;
   int64_t m, d, rows;
   const void *A, *B;
-  int dtype;
   int64_t adapters;
   int rank;
   const int32_t *ranks, *index;
@@ -22,8 +36,15 @@ struct LoraArgs {
   int64_t ldb;
   float* y;
   int64_t ldy;
-  float* T;      // m x rank
+  float* T;          // [ksplit][m][rank]
+  int ksplit;        // ranges of d over the grid
+  int64_t kper;      // columns of a range, a multiple of 4 waves x 32
+  int slot_groups;   // workgroups that share out a tile's slots (shrink)
+  int64_t tile0;     // first row tile of the launch (expand)
+  int xvec, bvec, yvec;
 };
+
+constexpr int64_t kPiece = (int64_t)1 << 19;   // rows taken at a time: the workspace holds one piece's T
 
 GPTQ_DEV int rank_of(const LoraArgs& a, int64_t ad) {
   if (!a.ranks) return a.rank;
@@ -31,60 +52,358 @@ GPTQ_DEV int rank_of(const LoraArgs& a, int64_t ad) {
   return r < 0 ? 0 : r > a.rank ? a.rank : r;
 }
 
-// One wave per (row, rank): the dot product of x_i and row k of A_a.
-__global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t items = a.m * a.rank;
-  for (int64_t it = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); it < items; it += (int64_t)gridDim.x * 4) {
-    const int64_t i = it / a.rank;
-    const int k = (int)(it - i * a.rank);
-    const int64_t ad = a.index[i];
-    if (ad < 0 || ad >= a.adapters || k >= rank_of(a, ad)) continue;
-    const int64_t xo = i * a.ldx, ao = (ad * a.rank + k) * a.d;
-    float s = 0.f;
-    for (int64_t c = lane; c < a.d; c += 64)
-      s = __builtin_fmaf(load_as_f32(a.x, a.dtype, xo + c), load_as_f32(a.A, a.dtype, ao + c), s);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
-    if (lane == 0) a.T[it] = s;
+// The adapter of row i0 + lane, or -1 (past the tile or the rows, or none).
+GPTQ_DEV int adapter_of(const LoraArgs& a, int64_t i0, int tile, int lane) {
+  if (lane >= tile || i0 + lane >= a.m) return -1;
+  const int ad = a.index[i0 + lane];
+  return ad < 0 || ad >= a.adapters ? -1 : ad;
+}
+
+// Calls f(slot, adapter, rows) for the distinct adapters of a wave's lanes in order of first lane.
+template <typename F>
+GPTQ_DEV void each_slot(int ad, F&& f) {
+  uint64_t left = __ballot(ad >= 0);
+  for (int s = 0; left; ++s) {
+    const int a = __builtin_amdgcn_readlane(ad, __builtin_ctzll(left));
+    const uint64_t mine = __ballot(ad == a);
+    f(s, a, mine);
+    left &= ~mine;
   }
 }
 
-__global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
-  const int64_t total = a.m * a.rows;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
-    const int64_t i = e / a.rows, j = e - i * a.rows;
-    const int64_t ad = a.index[i];
-    float v = a.base ? a.base[i * a.ldb + j] : 0.f;
-    if (ad >= 0 && ad < a.adapters) {
-      const int r = rank_of(a, ad);
-      const int64_t bo = (ad * a.rows + j) * a.rank;
-      float s = 0.f;
-      for (int k = 0; k < r; ++k) s = __builtin_fmaf(a.T[i * a.rank + k], load_as_f32(a.B, a.dtype, bo + k), s);
-      if (r) v += (a.scales ? a.scales[ad] : 1.0f) * s;
-    }
-    a.y[i * a.ldy + j] = v;
+// Eight (16-bit types) or four (fp32) consecutive elements from column k of a row of n columns.
+template <int DT> struct Frag;
+template <> struct Frag<F16> { typedef v8s T; static constexpr int N = 8; };
+template <> struct Frag<BF16> { typedef v8s T; static constexpr int N = 8; };
+template <> struct Frag<F32> { typedef floatx4 T; static constexpr int N = 4; };
+
+template <int DT, bool VEC>
+GPTQ_DEV typename Frag<DT>::T load_frag(const void* row, int64_t k, int64_t n, bool ok) {
+  typedef typename Frag<DT>::T V;
+  typedef typename std::conditional<DT == F32, float, short>::type E;
+  const E* p = static_cast<const E*>(row);
+  V v = {};
+  if (!ok) return v;
+  if (VEC) {
+    if (k < n) v = *reinterpret_cast<const V*>(p + k);
+  } else {
+#pragma unroll
+    for (int e = 0; e < Frag<DT>::N; ++e)
+      if (k + e < n) v[e] = p[k + e];
   }
+  return v;
+}
+
+template <int DT>
+GPTQ_DEV floatx4 dot_step(typename Frag<DT>::T a, typename Frag<DT>::T b, floatx4 c) {
+  if constexpr (DT == F16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+  } else if constexpr (DT == BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+}
+
+// T of 16 MT rows for slots blockIdx.z, blockIdx.z + slot_groups, ... and range blockIdx.y of d; 16 NR ranks
+// at a time. Lane l of the MFMA holds row l % 16 of x (and rank l % 16 of A) at 8 (or 4) columns of its
+// quarter l / 16; it gets T of rank l % 16 and rows 4 (l / 16) .. + 3.
+template <int DT, int MT, int NR, bool VEC>
+__global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
+  constexpr int KS = 4 * Frag<DT>::N;     // columns of a step
+  __shared__ floatx4 part[3][MT][NR][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t i0 = (int64_t)blockIdx.x * 16 * MT;
+  const int ad = adapter_of(a, i0, 16 * MT, lane);
+  const int esz = DT == F32 ? 4 : 2;
+  const int l16 = lane & 15, quarter = lane >> 4;
+  const char* xrow[MT];
+  bool xok[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t i = i0 + 16 * t + l16;
+    xok[t] = i < a.m;
+    xrow[t] = static_cast<const char*>(a.x) + (xok[t] ? i : 0) * a.ldx * esz;
+  }
+  const int64_t k0 = blockIdx.y * a.kper + wave * (a.kper / 4);
+  const int64_t k1 = min(a.d, k0 + a.kper / 4);
+  float* T = a.T + (int64_t)blockIdx.y * a.m * a.rank;
+  each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
+    if (slot % a.slot_groups != (int)blockIdx.z) return;
+    const int r = rank_of(a, adapter);
+    for (int n0 = 0; n0 < a.rank; n0 += 16 * NR) {
+      floatx4 acc[MT][NR];
+      const char* arow[NR];
+      bool aok[NR];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const int k = n0 + 16 * n + l16;
+        aok[n] = k < r;
+        arow[n] = static_cast<const char*>(a.A) + ((int64_t)adapter * a.rank + (aok[n] ? k : 0)) * a.d * esz;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll 4
+      for (int64_t k = k0; k < k1; k += KS) {
+        const int64_t kk = k + quarter * Frag<DT>::N;
+        typename Frag<DT>::T xf[MT], af[NR];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) xf[t] = load_frag<DT, VEC>(xrow[t], kk, k1, xok[t]);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) af[n] = load_frag<DT, VEC>(arow[n], kk, k1, aok[n]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int n = 0; n < NR; ++n) acc[t][n] = dot_step<DT>(xf[t], af[n], acc[t][n]);
+      }
+      __syncthreads();   // the last partial sums have been read
+      if (wave) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int n = 0; n < NR; ++n) part[wave - 1][t][n][lane] = acc[t][n];
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            floatx4 s = acc[t][n];
+#pragma unroll
+            for (int w = 0; w < 3; ++w) {
+              const floatx4 o = part[w][t][n][lane];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[e] += o[e];
+            }
+            const int k = n0 + 16 * n + l16;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = 16 * t + 4 * quarter + e;
+              if (k < a.rank && ((mine >> row) & 1)) T[(i0 + row) * a.rank + k] = s[e];
+            }
+          }
+      }
+    }
+  });
+}
+
+// Four consecutive elements of a row of B as floats, zeros from column r on.
+template <int DT>
+GPTQ_DEV floatx4 load_b4(const void* B, int64_t at, int k, int r, bool vec) {
+  floatx4 v = {0.f, 0.f, 0.f, 0.f};
+  typedef typename ElemOf<DT>::T T;
+  const T* p = static_cast<const T*>(B) + at + k;
+  if (vec && k + 4 <= r) {
+    typedef T V4 __attribute__((ext_vector_type(4)));
+    const V4 u = *reinterpret_cast<const V4*>(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)u[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (k + e < r) v[e] = (float)p[e];
+  }
+  return v;
+}
+
+// y of 16 MT rows. SLOTS: the four waves share 16 NJ columns and take the tile's slots in turn (each row is
+// written by the wave of its slot); otherwise each wave takes 16 NJ columns of its own and every slot. The
+// MFMA's lane l holds B row (column of y) l % 16 and T row l % 16 at ranks 4 (l / 16) .. + 3, and gets four
+// consecutive columns of y of row l % 16.
+template <int DT, int MT, int NJ, bool SLOTS>
+__global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
+  extern __shared__ __align__(16) float ts[];   // [16 MT][rank rounded up to 16, + 4]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, quarter = lane >> 4;
+  const int64_t i0 = (a.tile0 + blockIdx.y) * 16 * MT;
+  const int64_t j0 = SLOTS ? (int64_t)blockIdx.x * 16 * NJ : ((int64_t)blockIdx.x * 4 + wave) * 16 * NJ;
+  const int ad = adapter_of(a, i0, 16 * MT, lane);
+  const int rp = (a.rank + 15) / 16 * 16, pitch = rp + 4;
+  // T of the tile's rows, the ranges of d added in order
+  for (int e = threadIdx.x; e < 16 * MT * rp; e += 256) {
+    const int row = e / rp, k = e - row * rp;
+    const int ra = __shfl(ad, row, 64);   // a wave's 64 elements can span rows
+    float s = 0.f;
+    if (ra >= 0 && k < a.rank)
+      for (int p = 0; p < a.ksplit; ++p) s += a.T[((int64_t)p * a.m + i0 + row) * a.rank + k];
+    ts[row * pitch + k] = s;
+  }
+  __syncthreads();
+  if (j0 >= a.rows) return;
+
+  auto store = [&](int t, int j, const floatx4& v, float scale, int64_t i) {
+    const int64_t c = j0 + 16 * j + 4 * quarter;
+    float* yp = a.y + i * a.ldy + c;
+    const float* bp = a.base ? a.base + i * a.ldb + c : nullptr;
+    if (a.yvec && c + 4 <= a.rows) {
+      floatx4 o = {0.f, 0.f, 0.f, 0.f};
+      if (bp) o = *reinterpret_cast<const floatx4*>(bp);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(scale, v[e], o[e]);
+      *reinterpret_cast<floatx4*>(yp) = o;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.rows) yp[e] = __builtin_fmaf(scale, v[e], bp ? bp[e] : 0.f);
+    }
+  };
+
+  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+  each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
+    if (SLOTS && (slot & 3) != wave) return;
+    const int r = rank_of(a, adapter);
+    const float scale = a.scales ? a.scales[adapter] : 1.0f;
+    floatx4 acc[MT][NJ];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[t][j] = zero;
+    for (int k0 = 0; k0 < r; k0 += 16) {
+      const int k = k0 + 4 * quarter;
+      floatx4 b[NJ], t4[MT];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t jr = min(j0 + 16 * j + l16, a.rows - 1);
+        b[j] = load_b4<DT>(a.B, ((int64_t)adapter * a.rows + jr) * a.rank, k, r, a.bvec);
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) t4[t] = *reinterpret_cast<const floatx4*>(ts + (16 * t + l16) * pitch + k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j][e], t4[t][e], acc[t][j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      if ((mine >> (16 * t + l16)) & 1) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) store(t, j, acc[t][j], r ? scale : 0.f, i0 + 16 * t + l16);
+      }
+  });
+  // rows without an adapter
+  const uint64_t with = __ballot(ad >= 0);
+  if (SLOTS && wave != 0) return;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t i = i0 + 16 * t + l16;
+    if (i < a.m && !((with >> (16 * t + l16)) & 1)) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) store(t, j, zero, 0.f, i);
+    }
+  }
+}
+
+// How the call is laid out, from its sizes alone.
+struct Plan {
+  int mt_shrink, slot_groups, ksplit;
+  int64_t kper;
+};
+
+Plan plan(int64_t m, int64_t d, int64_t adapters) {
+  Plan p{};
+  // Rows of a shrink tile: an adapter is read once per tile, so long runs take 32.
+  p.mt_shrink = m >= 1024 ? 2 : 1;
+  const int64_t tile = 16 * p.mt_shrink, tiles = (m + tile - 1) / tile;
+  // Few tiles: a workgroup for each slot. Then d is split until there are about 512 workgroups, in ranges
+  // of at least 512 columns (128 a wave).
+  p.slot_groups = tiles >= 64 ? 1 : (int)std::min<int64_t>(std::min(tile, m), std::max<int64_t>(1, adapters));
+  const int64_t wgs = tiles * p.slot_groups;
+  p.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, (512 + wgs - 1) / wgs), d / 512));
+  p.kper = ((d + p.ksplit - 1) / p.ksplit + 127) / 128 * 128;
+  p.ksplit = (int)((d + p.kper - 1) / p.kper);
+  return p;
+}
+
+template <int DT, bool VEC>
+hipError_t shrink(const LoraArgs& a, const Plan& p, hipStream_t s) {
+  const int64_t tile = 16 * p.mt_shrink;
+  const dim3 grid((unsigned)((a.m + tile - 1) / tile), (unsigned)a.ksplit, (unsigned)a.slot_groups);
+  const int nr = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
+#define GPTQ_SHRINK(MT, NR) hipLaunchKernelGGL((shrink_kernel<DT, MT, NR, VEC>), grid, dim3(256), 0, s, a)
+  if (p.mt_shrink == 1) {
+    if (nr == 1) GPTQ_SHRINK(1, 1);
+    else if (nr == 2) GPTQ_SHRINK(1, 2);
+    else GPTQ_SHRINK(1, 4);
+  } else {
+    if (nr == 1) GPTQ_SHRINK(2, 1);
+    else if (nr == 2) GPTQ_SHRINK(2, 2);
+    else GPTQ_SHRINK(2, 4);
+  }
+#undef GPTQ_SHRINK
+  return hipGetLastError();
+}
+
+template <int DT, int MT, int NJ, bool SLOTS>
+hipError_t launch_expand(const LoraArgs& a, hipStream_t s) {
+  const int64_t cols = (SLOTS ? 1 : 4) * 16 * NJ;
+  const size_t lds = (size_t)16 * MT * ((a.rank + 15) / 16 * 16 + 4) * sizeof(float);
+  // a grid holds fewer than 2^32 threads: very wide outputs take their row tiles in several launches
+  const int64_t xs = (a.rows + cols - 1) / cols, tiles = (a.m + 16 * MT - 1) / (16 * MT);
+  const int64_t step = std::min<int64_t>(65535, std::max<int64_t>(1, ((int64_t)1 << 23) / xs));
+  for (int64_t t0 = 0; t0 < tiles; t0 += step) {
+    LoraArgs b = a;
+    b.tile0 = t0;
+    hipLaunchKernelGGL((expand_kernel<DT, MT, NJ, SLOTS>), dim3((unsigned)xs, (unsigned)std::min(step, tiles - t0)),
+                       dim3(256), lds, s, b);
+  }
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run(const LoraArgs& a, const Plan& p, hipStream_t s) {
+  hipError_t e = a.adapters == 0 ? hipSuccess : a.xvec ? shrink<DT, true>(a, p, s) : shrink<DT, false>(a, p, s);
+  if (e != hipSuccess) return e;
+  // Long inputs: 64 rows a tile, so that B is read once for them (32 where T of 64 rows of wide ranks would
+  // leave few workgroups a CU); few rows: 16, slots over the waves, and narrow columns while a launch of
+  // wide ones has fewer than 512 workgroups.
+  if (a.m >= 512) return a.rank <= 128 ? launch_expand<DT, 4, 4, false>(a, s) : launch_expand<DT, 2, 4, false>(a, s);
+  const int64_t wide = (a.rows + 63) / 64 * ((a.m + 15) / 16);
+  return wide >= 512 ? launch_expand<DT, 1, 4, true>(a, s) : launch_expand<DT, 1, 1, true>(a, s);
 }
 
 }  // namespace
 
-size_t lora_workspace_bytes(int64_t m, int64_t, int64_t, int64_t, int32_t rank) { return (size_t)m * rank * 4; }
+size_t lora_workspace_bytes(int64_t m, int64_t d, int64_t, int64_t adapters, int32_t rank) {
+  m = std::min(m, kPiece);
+  return (size_t)plan(m, d, adapters).ksplit * m * rank * 4;
+}
 
 hipError_t lora_gemm(const void* x, int dtype, int64_t m, int64_t ldx, const void* A, const void* B,
                      const int32_t* ranks, const float* scales, int64_t adapters, int32_t rank, const int32_t* index,
                      int64_t rows, int64_t d, const float* base, int64_t ld_base, float* y, int64_t ldy, void* work,
                      hipStream_t s) {
+  const Plan p = plan(std::min(m, kPiece), d, adapters);
   LoraArgs a{};
   a.x = x; a.ldx = ldx; a.m = m; a.d = d; a.rows = rows;
-  a.A = A; a.B = B; a.dtype = dtype; a.adapters = adapters; a.rank = rank;
+  a.A = A; a.B = B; a.adapters = adapters; a.rank = rank;
   a.ranks = ranks; a.index = index; a.scales = scales;
   a.base = base; a.ldb = ld_base; a.y = y; a.ldy = ldy;
   a.T = static_cast<float*>(work);
-  hipLaunchKernelGGL(shrink_kernel, dim3((unsigned)std::min<int64_t>((m * rank + 3) / 4, 65536)), dim3(256), 0, s, a);
-  hipLaunchKernelGGL(expand_kernel, dim3((unsigned)std::min<int64_t>((m * rows + 255) / 256, 65536)), dim3(256), 0, s,
-                     a);
-  return hipGetLastError();
+  a.ksplit = p.ksplit; a.kper = p.kper; a.slot_groups = p.slot_groups;
+  // 16-byte loads of x and A, four elements of B at a time, 16-byte accesses of base and y
+  const int64_t esz = dtype == F32 ? 4 : 2, n = 16 / esz;
+  auto at = [](const void* q, int64_t to) { return reinterpret_cast<uintptr_t>(q) % to == 0; };
+  a.xvec = d % n == 0 && ldx % n == 0 && at(x, 16) && at(A, 16);
+  a.bvec = rank % 4 == 0 && at(B, 4 * esz);
+  a.yvec = ldy % 4 == 0 && at(y, 16) && (!base || (ld_base % 4 == 0 && at(base, 16)));
+  for (int64_t i0 = 0; i0 < m; i0 += kPiece) {
+    LoraArgs b = a;
+    b.m = std::min(kPiece, m - i0);
+    b.x = static_cast<const char*>(x) + i0 * ldx * esz;
+    b.index = index + i0;
+    b.base = base ? base + i0 * ld_base : nullptr;
+    b.y = y + i0 * ldy;
+    const hipError_t e = dtype == F32 ? run<F32>(b, p, s) : dtype == F16 ? run<F16>(b, p, s) : run<BF16>(b, p, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace gptq
