@@ -193,7 +193,7 @@ __global__ __launch_bounds__(256) void attn_row_kernel(AttnArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ 16-bit types, matrix cores
+// ------------------------------------------------------------------ matrix cores
 //
 // The query heads that share a key head are rows of one tile: packed row r of a sequence is query
 // r / group and head r % group, so a key tile is read once for all of them, and a single new token still
@@ -226,11 +226,22 @@ GPTQ_DEV void dma16(i32x4 rsrc, uint32_t voff, uint32_t lds_addr) {
                : "memory");
 }
 
-// Buffer descriptor of n 16-bit elements from a wave-uniform address.
-GPTQ_DEV i32x4 descriptor(uint64_t base, int64_t n) {
+// Buffer descriptor of `bytes` bytes from a wave-uniform address.
+GPTQ_DEV i32x4 descriptor(uint64_t base, int64_t bytes) {
   const uint64_t b = uniform64(base);
-  return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), __builtin_amdgcn_readfirstlane((int)(2 * n)), 0x00020000};
+  return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
+
+// Keys of a tile and buffers, within 160 KB of LDS (two workgroups a CU where rows are shared and the
+// head is at most 128 wide).
+template <int DT, int DHP, int WM>
+struct Tile {
+  static constexpr int ESZ = DT == F32 ? 4 : 2;
+  static constexpr int KT = WM == 4 && DT != F32 ? 64 : 32;
+  static constexpr int TILEB = KT * DHP * ESZ;
+  static constexpr int NB = WM == 1 && TILEB > 8192 ? 1 : 2;
+  static constexpr int LDS = NB * 2 * TILEB * (4 / WM) + 1024 + 64;
+};
 
 template <int DT>
 GPTQ_DEV floatx16 mfma16(v8s a, v8s b, floatx16 c) {
@@ -304,18 +315,23 @@ constexpr float kShift = 7.0f, kRaise = 8.0f;
 // biased (or scaled by zero).
 template <int DT, int DHP, int WM, bool DMA, int MODE>
 __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_kernel(AttnArgs a) {
-  constexpr int KT = WM == 4 ? 64 : 32;         // keys of a tile
-  constexpr int NT = KT / 32, NF = DHP / 32, NK = DHP / 16;
-  constexpr int UN = DHP / 8;                   // 16-byte units of a row
-  constexpr int ROWB = DHP * 2, TILEB = KT * ROWB, BUFB = 2 * TILEB;
+  typedef typename ElemOf<DT>::T T;
+  typedef Tile<DT, DHP, WM> C;
+  constexpr int KT = C::KT, NB = C::NB;         // keys of a tile, buffers
+  constexpr int NT = KT / 32, NF = DHP / 32;
+  constexpr int ESZ = C::ESZ, EPU = 16 / ESZ;   // elements of a 16-byte unit
+  constexpr int NK = DHP / (2 * EPU);           // unit pairs of a row: one unit of a pair to each half wave
+  constexpr int UN = DHP / EPU;                 // units of a row
+  constexpr int ROWB = DHP * ESZ, TILEB = C::TILEB, BUFB = 2 * TILEB;
   constexpr int LOADS = KT * UN / 64 / WM;      // units a lane stages of K (and of V)
   constexpr int ROWS = 32 * WM;
+  typedef typename std::conditional<DT == F32, floatx4, v8s>::type Unit;
   extern __shared__ char smem_raw[];
   GPTQ_LDS char* smem = (GPTQ_LDS char*)smem_raw;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   // small LDS area behind the tiles: documents of a tile per wave, tile masks
-  GPTQ_LDS char* tail = smem + (WM == 4 ? 2 * BUFB : 8 * BUFB);
+  GPTQ_LDS char* tail = smem + NB * BUFB * (4 / WM);
   GPTQ_LDS int32_t* docs = (GPTQ_LDS int32_t*)tail + 64 * wave;
   GPTQ_LDS uint32_t* masks = (GPTQ_LDS uint32_t*)(tail + 1024);   // [wave]: 16 active bits, 16 whole bits
 
@@ -387,31 +403,34 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   dmin = __builtin_amdgcn_readfirstlane(dmin);
   dmax = __builtin_amdgcn_readfirstlane(dmax);
 
-  typedef typename ElemOf<DT>::T T;
-  const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sq.k0 * a.k_ld + kvh * a.k_hp;
-  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sq.k0 * a.v_ld + kvh * a.v_hp;
+  typedef typename std::conditional<DT == F32, float, short>::type E;   // an element's bits
+  const E* kp = static_cast<const E*>(a.k) + sq.k0 * a.k_ld + kvh * a.k_hp;
+  const E* vp = static_cast<const E*>(a.v) + sq.k0 * a.v_ld + kvh * a.v_hp;
 
-  // Q^T operand: row col, columns 16 ks + 8 half .. + 7; negated for a negative scale, so that the largest
-  // score is the largest product
-  v8s qf[NK];
+  // Q^T operand: row col, unit 2 ks + half of it; negated for a negative scale, so that the largest score
+  // is the largest product
+  Unit qf[NK];
   {
-    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + (sq.q0 + qi) * a.q_ld + h * a.q_hp;
-    const short flip = MODE == 0 && a.scale < 0.f ? (short)0x8000 : (short)0;
+    const E* qp = static_cast<const E*>(a.q) + (sq.q0 + qi) * a.q_ld + h * a.q_hp;
+    const bool flip = MODE == 0 && a.scale < 0.f;
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) {
-      const int c0 = 16 * ks + 8 * half;
-      v8s f = {};
+      const int c0 = EPU * (2 * ks + half);
+      Unit f = {};
       if (live) {
         if (DMA) {
-          if (c0 < a.dh) f = *reinterpret_cast<const v8s*>(qp + c0);
+          if (c0 < a.dh) f = *reinterpret_cast<const Unit*>(qp + c0);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c0 + e < a.dh) f[e] = (short)qp[c0 + e];
+          for (int e = 0; e < EPU; ++e)
+            if (c0 + e < a.dh) f[e] = qp[c0 + e];
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] ^= flip;
+      for (int e = 0; e < EPU; ++e) {
+        if constexpr (DT == F32) f[e] = flip ? -f[e] : f[e];
+        else f[e] ^= flip ? (short)0x8000 : (short)0;
+      }
       qf[ks] = f;
     }
   }
@@ -425,18 +444,18 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     const int row = unit / UN, up = unit - row * UN;
     srow[i] = row;
     ku[i] = up ^ swz_k<UN>(row);
-    vu[i] = up ^ swz_v<UN>(row);
+    vu[i] = DT == F32 ? up : up ^ swz_v<UN>(row);
   }
   constexpr uint32_t OOB = 0x80000000u;   // beyond any descriptor's range: reads as zero
   uint32_t kvo[LOADS], vvo[LOADS];
   if (DMA) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      kvo[i] = ku[i] * 8 < a.dh ? (uint32_t)((srow[i] * a.k_ld + ku[i] * 8) * 2) : OOB;
-      vvo[i] = vu[i] * 8 < a.dh ? (uint32_t)((srow[i] * a.v_ld + vu[i] * 8) * 2) : OOB;
+      kvo[i] = ku[i] * EPU < a.dh ? (uint32_t)((srow[i] * a.k_ld + ku[i] * EPU) * ESZ) : OOB;
+      vvo[i] = vu[i] * EPU < a.dh ? (uint32_t)((srow[i] * a.v_ld + vu[i] * EPU) * ESZ) : OOB;
     }
   }
-  GPTQ_LDS char* base = smem + (WM == 4 ? 0 : wave * 2 * BUFB);
+  GPTQ_LDS char* base = smem + (WM == 4 ? 0 : wave * NB * BUFB);
   auto stage = [&](int64_t j0, int buf) {
     const int64_t left = sq.lk - j0;
     const int rows = left < KT ? (int)left : KT;
@@ -444,7 +463,8 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     GPTQ_LDS char* vd = kd + TILEB;
     if (DMA) {
       const uint64_t ka = (uint64_t)(uintptr_t)(kp + j0 * a.k_ld), va = (uint64_t)(uintptr_t)(vp + j0 * a.v_ld);
-      const i32x4 kr = descriptor(ka, (rows - 1) * a.k_ld + a.dh), vr = descriptor(va, (rows - 1) * a.v_ld + a.dh);
+      const i32x4 kr = descriptor(ka, ((rows - 1) * a.k_ld + a.dh) * ESZ),
+                  vr = descriptor(va, ((rows - 1) * a.v_ld + a.dh) * ESZ);
       const uint32_t k32 = (uint32_t)(uintptr_t)kd, v32 = (uint32_t)(uintptr_t)vd;
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) dma16(kr, kvo[i], k32 + 1024 * i);
@@ -453,27 +473,27 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     } else {
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        v8s kx = {}, vx = {};
+        Unit kx = {}, vx = {};
         if (srow[i] < rows) {
-          const uint16_t* ks = kp + (j0 + srow[i]) * a.k_ld;
-          const uint16_t* vs = vp + (j0 + srow[i]) * a.v_ld;
+          const E* ks = kp + (j0 + srow[i]) * a.k_ld;
+          const E* vs = vp + (j0 + srow[i]) * a.v_ld;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (ku[i] * 8 + e < a.dh) kx[e] = (short)ks[ku[i] * 8 + e];
-            if (vu[i] * 8 + e < a.dh) vx[e] = (short)vs[vu[i] * 8 + e];
+          for (int e = 0; e < EPU; ++e) {
+            if (ku[i] * EPU + e < a.dh) kx[e] = ks[ku[i] * EPU + e];
+            if (vu[i] * EPU + e < a.dh) vx[e] = vs[vu[i] * EPU + e];
           }
         }
-        *(GPTQ_LDS v8s*)(kd + 1024 * i + 16 * lane) = kx;
-        *(GPTQ_LDS v8s*)(vd + 1024 * i + 16 * lane) = vx;
+        *(GPTQ_LDS Unit*)(kd + 1024 * i + 16 * lane) = kx;
+        *(GPTQ_LDS Unit*)(vd + 1024 * i + 16 * lane) = vx;
       }
     }
   };
 
   // operand addresses inside a tile
-  int koff[4], voff[2];
+  int koff[4], voff[2] = {4 * half * ROWB + 4 * col, 0};
 #pragma unroll
   for (int i = 0; i < 4; ++i) koff[i] = col * ROWB + (((2 * i + half) ^ swz_k<UN>(col)) << 4);
-  {
+  if constexpr (DT != F32) {
     const int s = lane & 15, trow = 4 * half + (s >> 2);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -497,8 +517,13 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       S[t] = floatx16{};
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
-        const v8s kf = *(GPTQ_LDS v8s*)(kt + 32 * t * ROWB + koff[ks & 3] + 128 * (ks >> 2));
-        S[t] = mfma16<DT>(kf, qf[ks], S[t]);
+        const Unit kf = *(GPTQ_LDS Unit*)(kt + 32 * t * ROWB + koff[ks & 3] + 128 * (ks >> 2));
+        if constexpr (DT == F32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(kf[e], qf[ks][e], S[t], 0, 0, 0);
+        } else {
+          S[t] = mfma16<DT>(kf, qf[ks], S[t]);
+        }
       }
     }
     const int32_t jb = (int32_t)j0 + 4 * half;   // the key of register i of subtile t: jb + 32 t + 8 (i / 4) + i % 4
@@ -510,8 +535,12 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
           float x = S[t][i] * a.scale;
           if (a.cap > 0.f) {
             // tanh y = 1 - 2 / (e^2y + 1)
-            const float e2 = __builtin_amdgcn_exp2f(x * inv_cap * (2.0f * kLog2e));
-            x = a.cap - 2.0f * a.cap * __builtin_amdgcn_rcpf(e2 + 1.0f);
+            if constexpr (DT == F32) {
+              x = a.cap * tanhf(x * inv_cap);
+            } else {
+              const float e2 = __builtin_amdgcn_exp2f(x * inv_cap * (2.0f * kLog2e));
+              x = a.cap - 2.0f * a.cap * __builtin_amdgcn_rcpf(e2 + 1.0f);
+            }
           }
           if (a.slopes) x -= slope * fabsf((float)(pos - (jb + 32 * t + 8 * (i / 4) + i % 4)));
           S[t][i] = x;
@@ -559,14 +588,27 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
         for (int i = 0; i < 16; ++i) acc[ft][i] *= f;
     }
     const float off = kShift - (m == -INFINITY ? 0.f : m * c);
-    float p[NT][16];
+    float p[NT][16], sum[4] = {0.f, 0.f, 0.f, 0.f};   // a tile's sum apart, so that long sums stay short chains
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         p[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[t][i], c, off));
-        l += p[t][i];
+        sum[i & 3] += p[t][i];
       }
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    if constexpr (DT == F32) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int ft = 0; ft < NF; ++ft) {
+            const float vf = *(GPTQ_LDS float*)(vt + (32 * t + 8 * (i / 4) + i % 4) * ROWB + voff[0] + 128 * ft);
+            acc[ft] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, p[t][i], acc[ft], 0, 0, 0);
+          }
+      return;
+    } else {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -580,6 +622,7 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
           acc[ft] = mfma16<DT>(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7), pf, acc[ft]);
         }
       }
+    }
   };
 
   auto ready = [&]() {   // the staged tile is in LDS, and the other buffer is no longer read
@@ -600,9 +643,10 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     const int64_t left = (ke - b0 + step - 1) / step;
     if (left < 64) active = (1ull << left) - 1;
     if (a.q_doc && WM == 4) {
-      const int64_t j0 = b0 + 16 * (int64_t)threadIdx.x;
+      constexpr int QK = KT / 4;
+      const int64_t j0 = b0 + QK * (int64_t)threadIdx.x;
       int32_t lo = 0x7fffffff, hi = (int32_t)0x80000000;
-      for (int e = 0; e < 16; ++e)
+      for (int e = 0; e < QK; ++e)
         if (j0 + e < ke) {
           const int32_t d = a.kv_doc[sq.k0 + j0 + e];
           lo = min(lo, d);
@@ -647,13 +691,17 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       const bool have = exists(t), full = (whole >> t) & 1;
       active &= active - 1;
       ready();
-      if (active) {
-        t = __builtin_ctzll(active);
-        if (exists(t)) stage(tile_of(t), buf ^ 1);
-      }
+      if (active) t = __builtin_ctzll(active);
+      if (NB == 2 && active && exists(t)) stage(tile_of(t), buf ^ 1);
       if (have && j0 < wmax) compute(j0, buf, full);
       if (!active) break;
-      buf ^= 1;
+      if (NB == 2) {
+        buf ^= 1;
+      } else {   // one buffer: the next tile is loaded when this one has been read
+        if (DMA) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        else __syncthreads();
+        if (exists(t)) stage(tile_of(t), 0);
+      }
     }
   }
   l += mirror(l);
@@ -815,8 +863,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 
 template <int DT, int DHP, int WM, bool DMA, int MODE>
 hipError_t launch_mfma(const AttnArgs& a, hipStream_t s) {
-  constexpr size_t tile = (size_t)(WM == 4 ? 64 : 32) * DHP * 2;
-  constexpr size_t lds = 2 * 2 * tile * (WM == 4 ? 1 : 4) + 1024 + 64;
+  constexpr size_t lds = Tile<DT, DHP, WM>::LDS;
   auto f = attn_mfma_kernel<DT, DHP, WM, DMA, MODE>;
   // the LDS beyond 64 KB is asked for once per device
   static std::atomic<uint64_t> asked{0};
@@ -862,7 +909,7 @@ struct Plan {
 
 Plan plan(const gptq_attention_t& t) {
   Plan p{};
-  p.mfma = t.dtype != GPTQ_F32 && t.head_dim <= 256;
+  p.mfma = t.head_dim <= 256;
   if (!p.mfma) return p;
   const int64_t group = t.q_heads / t.kv_heads;
   // sequences of at most 32 packed rows on average: the four waves split the keys instead of the rows
@@ -915,18 +962,22 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
     a.part_o = a.part_ml + (int64_t)p.nsplit * a.nq * a.hq * 2;
   }
   if (a.tiles * a.hk * a.nsplit >= ((int64_t)1 << 24)) return hipErrorNotSupported;   // a grid's 2^32 threads
-  // 16-byte units: pointers, pitches and head width multiples of 8 elements, and a tile inside 31-bit offsets
+  // 16-byte units: pointers, pitches and head width multiples of 16 bytes, and a tile inside 31-bit offsets
+  const int unit = t.dtype == F32 ? 4 : 8;
   auto al = [&](const void* ptr, int64_t ld, int64_t hp) {
-    return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0 && hp % 8 == 0;
+    return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % unit == 0 && hp % unit == 0;
   };
-  const bool dma = a.dh % 8 == 0 && al(q, a.q_ld, a.q_hp) && al(k, a.k_ld, a.k_hp) && al(v, a.v_ld, a.v_hp) &&
+  const bool dma = a.dh % unit == 0 && al(q, a.q_ld, a.q_hp) && al(k, a.k_ld, a.k_hp) && al(v, a.v_ld, a.v_hp) &&
                    std::max(a.k_ld, a.v_ld) < ((int64_t)1 << 23);
-  a.o_vec = reinterpret_cast<uintptr_t>(out) % 8 == 0 && a.o_ld % 4 == 0 && a.o_hp % 4 == 0;
+  a.o_vec = reinterpret_cast<uintptr_t>(out) % (t.dtype == F32 ? 16 : 8) == 0 && a.o_ld % 4 == 0 && a.o_hp % 4 == 0;
   const bool extra = a.cap > 0.f || a.slopes || a.scale == 0.f;
-  hipError_t e = t.dtype == F16 ? by_head<F16>(a, dma, extra, p.few, s) : by_head<BF16>(a, dma, extra, p.few, s);
+  hipError_t e = t.dtype == F32   ? by_head<F32>(a, dma, extra, p.few, s)
+                 : t.dtype == F16 ? by_head<F16>(a, dma, extra, p.few, s)
+                                  : by_head<BF16>(a, dma, extra, p.few, s);
   if (e != hipSuccess || p.nsplit <= 1) return e;
   const dim3 grid((unsigned)std::min<int64_t>((a.nq * a.hq + 3) / 4, 65536));
-  if (t.dtype == F16) hipLaunchKernelGGL(attn_join_kernel<F16>, grid, dim3(256), 0, s, a);
+  if (t.dtype == F32) hipLaunchKernelGGL(attn_join_kernel<F32>, grid, dim3(256), 0, s, a);
+  else if (t.dtype == F16) hipLaunchKernelGGL(attn_join_kernel<F16>, grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL(attn_join_kernel<BF16>, grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
