@@ -511,6 +511,49 @@ gptq_status_t gptq_quantize_block(const gptq_block_shape_t *shape, const void *X
                                   void *stream);
 
 /*
+ * The attention of a block whose model has more than gptq_quantize_block's: key heads shared by several
+ * query heads, a norm of each query and key head, a rotation by position, capped or distance-biased
+ * scores, several documents in a sequence, a prefix. Fields as in gptq_norm_rotate_t and gptq_attention_t;
+ * head_dim is hidden / heads (at most 1024), and positions, doc and prefix go by the block's tokens and
+ * sequences (n = seqs * seq_len).
+ */
+typedef struct {
+  int64_t kv_heads;          /* dividing heads; k and v are (kv_heads * head_dim) x hidden            */
+  const void *q_norm;        /* device w_dtype[head_dim] or NULL (ones); only with qk_norm            */
+  const void *k_norm;        /* the same for keys                                                     */
+  const float *inv_freq;     /* device float[rotary_dim / 2]; with rotary_dim > 0                     */
+  const int32_t *positions;  /* device int32[axes * n]; with rotary_dim > 0                           */
+  const int32_t *pair_axis;  /* device int32[rotary_dim / 2] or NULL                                  */
+  const float *slopes;       /* device float[heads] or NULL                                           */
+  const int32_t *doc;        /* device int32[n] or NULL; negative: padding                            */
+  const int32_t *prefix;     /* device int32[seqs] or NULL                                            */
+  double norm_eps;           /* epsilon of the head norm, >= 0                                        */
+  double scale;              /* score scale; 0: 1 / sqrt(head_dim)                                    */
+  double softcap;            /* 0: none                                                               */
+  int32_t qk_norm;           /* 1: each query and key head is normed                                  */
+  int32_t w_dtype;           /* of q_norm and k_norm                                                  */
+  int32_t rotary_dim;        /* 0: no rotation                                                        */
+  int32_t interleaved;
+  int32_t axes;
+  int32_t causal;
+} gptq_block_attn_t;
+
+/* Workspace bytes for gptq_quantize_block_attn; 0 for invalid arguments. */
+size_t gptq_block_attn_workspace_bytes(const gptq_block_shape_t *shape, const gptq_block_attn_t *attn,
+                                       const gptq_params_t *p);
+
+/*
+ * gptq_quantize_block with the attention `attn` describes: after the projections, q and k go through
+ * gptq_norm_rotate and then, with v, through gptq_attention, in fp32. The other arguments, the order of
+ * the solves, the waits and the errors are gptq_quantize_block's; layers k and v have
+ * kv_heads * head_dim rows. work: gptq_block_attn_workspace_bytes(shape, attn, p) bytes.
+ */
+gptq_status_t gptq_quantize_block_attn(const gptq_block_shape_t *shape, const gptq_block_attn_t *attn, const void *X,
+                                       int32_t x_dtype, const gptq_params_t *p, int32_t true_sequential,
+                                       const gptq_block_layer_t *layers, float *Y, float *const *hess, void *work,
+                                       size_t work_bytes, int64_t *info, void *stream);
+
+/*
  * Workspace bytes for a call: kind GPTQ_WS_HESSIAN (a = n_tok of the chunk), GPTQ_WS_FACTOR (a unused)
  * or GPTQ_WS_QUANTIZE (a = rows; p->block_size is read). Returns 0 for invalid arguments.
  */

@@ -85,3 +85,32 @@ def lora(x, A, B, index, scales=None, ranks=None, base=None):
             y[i] += s * (B[a][:, :ra] @ (A[a][:ra] @ x[i]))
             mag[i] += abs(s) * (np.abs(B[a][:, :ra]) @ (np.abs(A[a][:ra]) @ np.abs(x[i])))
     return y, mag
+
+
+def block_forward(X, W, hidden, heads, kv_heads, seqs, seq_len, eps=1e-6, qk_norm=False, q_norm=None, k_norm=None,
+                  norm_eps=1e-6, inv_freq=None, positions=None, pair_axis=None, interleaved=False, scale=None,
+                  softcap=0.0, slopes=None, doc=None, prefix=None, causal=True):
+    """The decoder block of gptq_quantize_block_attn: RMSNorm, q/k/v, per-head norm and rotation, attention, o,
+    residual, RMSNorm, gated MLP, residual. Returns the four stage inputs and the output."""
+    X = np.asarray(X, dtype=np.float64)
+    n, dh = seqs * seq_len, hidden // heads
+
+    def rms(x):
+        return x / np.sqrt(np.mean(x * x, axis=1, keepdims=True) + eps)
+
+    xa = rms(X)
+    q = (xa @ W[0].T).reshape(n, heads, dh)
+    k, v = ((xa @ W[i].T).reshape(n, kv_heads, dh) for i in (1, 2))
+    pos = None if positions is None else np.atleast_2d(positions)
+    if qk_norm or inv_freq is not None:
+        q, _ = norm_rotate(q, q_norm, pos, inv_freq, pair_axis, qk_norm, norm_eps, interleaved)
+        k, _ = norm_rotate(k, k_norm, pos, inv_freq, pair_axis, qk_norm, norm_eps, interleaved)
+    ranges = [(s * seq_len, (s + 1) * seq_len) * 2 for s in range(seqs)]
+    o, _, _ = attention(q, k, v, ranges, dh ** -0.5 if scale is None else scale, causal, softcap, slopes, doc, doc,
+                        prefix)
+    o = o.reshape(n, hidden)
+    h1 = X + o @ W[3].T
+    xm = rms(h1)
+    g = xm @ W[4].T
+    down = g / (1.0 + np.exp(-g)) * (xm @ W[5].T)
+    return dict(inputs=[xa, o, xm, down], out=h1 + down @ W[6].T)

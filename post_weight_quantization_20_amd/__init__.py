@@ -28,6 +28,7 @@ from .solver import (  # noqa: F401
     GPTQ_WS_FACTOR,
     GPTQ_WS_HESSIAN,
     GPTQ_WS_QUANTIZE,
+    BlockAttention,
     BlockResult,
     BlockShape,
     GPTQError,

@@ -51,6 +51,14 @@ class gptq_attention_t(ctypes.Structure):
                 [(f, c_int32) for f in ("dtype", "q_heads", "kv_heads", "head_dim", "causal")])
 
 
+class gptq_block_attn_t(ctypes.Structure):
+    _fields_ = ([("kv_heads", c_int64)] +
+                [(f, c_void_p) for f in ("q_norm", "k_norm", "inv_freq", "positions", "pair_axis", "slopes", "doc",
+                                         "prefix")] +
+                [(f, c_double) for f in ("norm_eps", "scale", "softcap")] +
+                [(f, c_int32) for f in ("qk_norm", "w_dtype", "rotary_dim", "interleaved", "axes", "causal")])
+
+
 # name -> (restype, argtypes), mirroring include/gptq.h
 SIGNATURES = {
     "gptq_hessian_accumulate": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_size_t,
@@ -86,6 +94,12 @@ SIGNATURES = {
                                       ctypes.POINTER(gptq_params_t), c_int32, ctypes.POINTER(gptq_block_layer_t),
                                       c_void_p, ctypes.POINTER(c_void_p), c_void_p, c_size_t,
                                       ctypes.POINTER(c_int64), c_void_p]),
+    "gptq_block_attn_workspace_bytes": (c_size_t, [ctypes.POINTER(gptq_block_shape_t),
+                                                   ctypes.POINTER(gptq_block_attn_t), ctypes.POINTER(gptq_params_t)]),
+    "gptq_quantize_block_attn": (c_int32, [ctypes.POINTER(gptq_block_shape_t), ctypes.POINTER(gptq_block_attn_t),
+                                           c_void_p, c_int32, ctypes.POINTER(gptq_params_t), c_int32,
+                                           ctypes.POINTER(gptq_block_layer_t), c_void_p, ctypes.POINTER(c_void_p),
+                                           c_void_p, c_size_t, ctypes.POINTER(c_int64), c_void_p]),
     "gptq_workspace_bytes": (c_size_t, [c_int32, c_int64, c_int64, ctypes.POINTER(gptq_params_t)]),
     "gptq_status_string": (ctypes.c_char_p, [c_int32]),
 }

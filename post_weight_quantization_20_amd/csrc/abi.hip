@@ -305,6 +305,16 @@ bool same(const Tensor3& a, const Tensor3& b) {
 
 int64_t elem_bytes(int32_t t) { return t == GPTQ_F32 ? 4 : 2; }
 
+bool norm_rotate_ok(const gptq_norm_rotate_t* a) {
+  if (!a || !dtype_ok(a->dtype) || !dtype_ok(a->w_dtype) || a->n < 0 || a->n >= kMaxDim) return false;
+  if (a->q_heads < 1 || a->q_heads > 65535 || a->k_heads < 0 || a->k_heads > 65535) return false;
+  if (a->head_dim < 1 || a->head_dim > 1024 || a->rotary_dim < 0 || a->rotary_dim > a->head_dim || a->rotary_dim % 2)
+    return false;
+  if ((a->interleaved != 0 && a->interleaved != 1) || (a->norm != 0 && a->norm != 1) || a->axes < 1 || a->axes > 64)
+    return false;
+  return std::isfinite(a->eps) && a->eps >= 0.0;
+}
+
 bool attention_ok(const gptq_attention_t* a) {
   if (!a || !dtype_ok(a->dtype) || a->seqs < 0 || a->seqs >= kMaxDim) return false;
   if (a->n_q < 0 || a->n_q > kMaxDim / 2 || a->n_kv < 0 || a->n_kv > kMaxDim / 2) return false;
@@ -347,13 +357,7 @@ gptq_status_t gptq_lora_gemm(const void* x, int32_t dtype, int64_t m, int64_t ld
 gptq_status_t gptq_norm_rotate(const gptq_norm_rotate_t* a, const void* q, const void* k, const void* q_weight,
                                const void* k_weight, const int32_t* positions, const float* inv_freq,
                                const int32_t* pair_axis, void* q_out, void* k_out, void* stream) {
-  if (!a || !dtype_ok(a->dtype) || !dtype_ok(a->w_dtype) || a->n < 0 || a->n >= kMaxDim) return GPTQ_EINVAL;
-  if (a->q_heads < 1 || a->q_heads > 65535 || a->k_heads < 0 || a->k_heads > 65535) return GPTQ_EINVAL;
-  if (a->head_dim < 1 || a->head_dim > 1024 || a->rotary_dim < 0 || a->rotary_dim > a->head_dim || a->rotary_dim % 2)
-    return GPTQ_EINVAL;
-  if ((a->interleaved != 0 && a->interleaved != 1) || (a->norm != 0 && a->norm != 1) || a->axes < 1 || a->axes > 64)
-    return GPTQ_EINVAL;
-  if (!std::isfinite(a->eps) || a->eps < 0.0 || (!a->norm && (q_weight || k_weight))) return GPTQ_EINVAL;
+  if (!norm_rotate_ok(a) || (!a->norm && (q_weight || k_weight))) return GPTQ_EINVAL;
   const int64_t esz = elem_bytes(a->dtype), hk = a->k_heads, dh = a->head_dim;
   const Tensor3 q3{q, a->n, a->q_heads, dh, a->q_ld, a->q_hp, esz}, k3{k, a->n, hk, dh, a->k_ld, a->k_hp, esz},
       qo{q_out, a->n, a->q_heads, dh, a->q_out_ld, a->q_out_hp, esz},
@@ -407,19 +411,20 @@ bool block_shape_ok(const gptq_block_shape_t* sh) {
   return std::isfinite(sh->eps) && sh->eps >= 0.0;
 }
 
-}  // namespace
-
-size_t gptq_block_workspace_bytes(const gptq_block_shape_t* shape, const gptq_params_t* p) {
-  if (!block_shape_ok(shape) || !p || p->block_size < 1 || p->block_size > 128) return 0;
-  return gptq::block_layout(*shape, *p).total;
+bool block_attn_ok(const gptq_block_shape_t& sh, const gptq_block_attn_t* at) {
+  if (!at || at->kv_heads < 1 || at->kv_heads > sh.heads || sh.heads % at->kv_heads != 0) return false;
+  const gptq_norm_rotate_t r = gptq::block_rotate(sh, *at);
+  const gptq_attention_t t = gptq::block_attention(sh, *at);
+  if (!norm_rotate_ok(&r) || !attention_ok(&t)) return false;
+  if (!at->qk_norm && (at->q_norm || at->k_norm)) return false;
+  return !at->rotary_dim || (at->inv_freq && at->positions);
 }
 
-gptq_status_t gptq_quantize_block(const gptq_block_shape_t* shape, const void* X, int32_t x_dtype,
-                                  const gptq_params_t* p, int32_t true_sequential, const gptq_block_layer_t* layers,
-                                  float* Y, float* const* hess, void* work, size_t work_bytes, int64_t* info,
-                                  void* stream) {
-  if (info) info[0] = -1, info[1] = 0;
-  if (!block_shape_ok(shape) || !X || !dtype_ok(x_dtype) || !layers || !Y || !work || !info) return GPTQ_EINVAL;
+// gptq_quantize_block and gptq_quantize_block_attn (attn not null)
+gptq_status_t block_call(const gptq_block_shape_t* shape, const gptq_block_attn_t* attn, const void* X, int32_t x_dtype,
+                         const gptq_params_t* p, int32_t true_sequential, const gptq_block_layer_t* layers, float* Y,
+                         float* const* hess, void* work, size_t work_bytes, int64_t* info, void* stream) {
+  if (!X || !dtype_ok(x_dtype) || !layers || !Y || !work || !info) return GPTQ_EINVAL;
   if (true_sequential != 0 && true_sequential != 1) return GPTQ_EINVAL;
   gptq_status_t st = check_params(p, std::min(shape->hidden, shape->inter), true);
   if (st != GPTQ_OK) return st;
@@ -429,9 +434,40 @@ gptq_status_t gptq_quantize_block(const gptq_block_shape_t* shape, const void* X
     if (!l.W || !l.codes || !l.scales || !l.zeros || !l.g_idx || !l.perm || !l.loss || !dtype_ok(l.w_dtype))
       return GPTQ_EINVAL;
   }
-  if (work_bytes < gptq::block_layout(*shape, *p).total) return GPTQ_ENOMEM;
-  return gptq::quantize_block(*shape, X, x_dtype, *p, true_sequential, layers, Y, hess, static_cast<char*>(work),
-                              info, static_cast<hipStream_t>(stream));
+  if (work_bytes < gptq::block_layout(*shape, attn, *p).total) return GPTQ_ENOMEM;
+  return gptq::quantize_block(*shape, attn, X, x_dtype, *p, true_sequential, layers, Y, hess,
+                              static_cast<char*>(work), info, static_cast<hipStream_t>(stream));
+}
+
+}  // namespace
+
+size_t gptq_block_workspace_bytes(const gptq_block_shape_t* shape, const gptq_params_t* p) {
+  if (!block_shape_ok(shape) || !p || p->block_size < 1 || p->block_size > 128) return 0;
+  return gptq::block_layout(*shape, nullptr, *p).total;
+}
+
+size_t gptq_block_attn_workspace_bytes(const gptq_block_shape_t* shape, const gptq_block_attn_t* attn,
+                                       const gptq_params_t* p) {
+  if (!block_shape_ok(shape) || !block_attn_ok(*shape, attn) || !p || p->block_size < 1 || p->block_size > 128) return 0;
+  return gptq::block_layout(*shape, attn, *p).total;
+}
+
+gptq_status_t gptq_quantize_block(const gptq_block_shape_t* shape, const void* X, int32_t x_dtype,
+                                  const gptq_params_t* p, int32_t true_sequential, const gptq_block_layer_t* layers,
+                                  float* Y, float* const* hess, void* work, size_t work_bytes, int64_t* info,
+                                  void* stream) {
+  if (info) info[0] = -1, info[1] = 0;
+  if (!block_shape_ok(shape)) return GPTQ_EINVAL;
+  return block_call(shape, nullptr, X, x_dtype, p, true_sequential, layers, Y, hess, work, work_bytes, info, stream);
+}
+
+gptq_status_t gptq_quantize_block_attn(const gptq_block_shape_t* shape, const gptq_block_attn_t* attn, const void* X,
+                                       int32_t x_dtype, const gptq_params_t* p, int32_t true_sequential,
+                                       const gptq_block_layer_t* layers, float* Y, float* const* hess, void* work,
+                                       size_t work_bytes, int64_t* info, void* stream) {
+  if (info) info[0] = -1, info[1] = 0;
+  if (!block_shape_ok(shape) || !block_attn_ok(*shape, attn)) return GPTQ_EINVAL;
+  return block_call(shape, attn, X, x_dtype, p, true_sequential, layers, Y, hess, work, work_bytes, info, stream);
 }
 
 }  // extern "C"

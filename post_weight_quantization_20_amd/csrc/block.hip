@@ -12,7 +12,8 @@
 //   to_f32_kernel          a fp32 copy of fp32 / fp16 / bf16 values
 // Products (x W^T, the attention scores and P V) run on gemm_f32. quantize_block (the body of
 // gptq_quantize_block) strings them together with the library's own Hessian, factor and column-loop
-// entry points.
+// entry points. gptq_quantize_block_attn takes the same way with norm_rotate (rotate.hip) and attention
+// (attention.hip) in place of the split scores, their softmax and P V.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -231,15 +232,58 @@ namespace {
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// Width of the block's keys and values.
+int64_t kv_width(const gptq_block_shape_t& sh, const gptq_block_attn_t* attn) {
+  return attn ? attn->kv_heads * (sh.hidden / sh.heads) : sh.hidden;
+}
+
 // Layer i of the block (q, k, v, o, gate, up, down): output features and input features.
-void layer_dims(const gptq_block_shape_t& sh, int i, int64_t& rows, int64_t& d) {
-  rows = (i == 4 || i == 5) ? sh.inter : sh.hidden;
+void layer_dims(const gptq_block_shape_t& sh, const gptq_block_attn_t* attn, int i, int64_t& rows, int64_t& d) {
+  rows = (i == 4 || i == 5) ? sh.inter : (i == 1 || i == 2) ? kv_width(sh, attn) : sh.hidden;
   d = i == 6 ? sh.inter : sh.hidden;
 }
 
 }  // namespace
 
-BlockLayout block_layout(const gptq_block_shape_t& sh, const gptq_params_t& p) {
+gptq_norm_rotate_t block_rotate(const gptq_block_shape_t& sh, const gptq_block_attn_t& attn) {
+  const int64_t dh = sh.hidden / sh.heads, kv = attn.kv_heads * dh;
+  gptq_norm_rotate_t r{};
+  r.n = sh.seqs * sh.seq_len;
+  r.q_ld = r.q_out_ld = sh.hidden;
+  r.k_ld = r.k_out_ld = kv;
+  r.q_hp = r.q_out_hp = r.k_hp = r.k_out_hp = dh;
+  r.eps = attn.norm_eps;
+  r.dtype = GPTQ_F32;
+  r.w_dtype = attn.w_dtype;
+  r.q_heads = (int32_t)sh.heads;
+  r.k_heads = (int32_t)attn.kv_heads;
+  r.head_dim = (int32_t)std::min<int64_t>(dh, 1 << 20);   // wider ones are refused by the limit on head_dim
+  r.rotary_dim = attn.rotary_dim;
+  r.interleaved = attn.interleaved;
+  r.axes = attn.axes;
+  r.norm = attn.qk_norm;
+  return r;
+}
+
+gptq_attention_t block_attention(const gptq_block_shape_t& sh, const gptq_block_attn_t& attn) {
+  const int64_t dh = sh.hidden / sh.heads, kv = attn.kv_heads * dh;
+  gptq_attention_t t{};
+  t.seqs = sh.seqs;
+  t.n_q = t.n_kv = sh.seqs * sh.seq_len;
+  t.q_ld = t.out_ld = sh.hidden;
+  t.k_ld = t.v_ld = kv;
+  t.q_hp = t.k_hp = t.v_hp = t.out_hp = dh;
+  t.scale = attn.scale == 0.0 ? 1.0 / std::sqrt((double)dh) : attn.scale;
+  t.softcap = attn.softcap;
+  t.dtype = GPTQ_F32;
+  t.q_heads = (int32_t)sh.heads;
+  t.kv_heads = (int32_t)attn.kv_heads;
+  t.head_dim = (int32_t)std::min<int64_t>(dh, 1 << 20);
+  t.causal = attn.causal;
+  return t;
+}
+
+BlockLayout block_layout(const gptq_block_shape_t& sh, const gptq_block_attn_t* attn, const gptq_params_t& p) {
   BlockLayout L{};
   const int64_t n = sh.seqs * sh.seq_len, hd = sh.hidden, di = sh.inter, dm = std::max(hd, di);
   size_t off = 0;
@@ -259,8 +303,13 @@ BlockLayout block_layout(const gptq_block_shape_t& sh, const gptq_params_t& p) {
   L.off_xm = take(act);
   L.off_g = take((size_t)n * di * 4);
   L.off_u = take((size_t)n * di * 4);
-  L.off_s = take((size_t)sh.heads * sh.seq_len * sh.seq_len * 4);
-  L.off_qk3 = take((size_t)2 * n * sh.heads * split3_pitch(hd / sh.heads) * 2);   // split Q and K
+  if (!attn) {   // scores of one sequence, split Q and K
+    L.off_s = take((size_t)sh.heads * sh.seq_len * sh.seq_len * 4);
+    L.off_qk3 = take((size_t)2 * n * sh.heads * split3_pitch(hd / sh.heads) * 2);
+  } else {
+    L.attn_bytes = attention_workspace_bytes(block_attention(sh, *attn));
+    L.off_aw = take(L.attn_bytes);
+  }
   L.off_wf = take((size_t)di * hd * 4);
   L.off_h = take((size_t)dm * dm * 4);
   L.off_uf = take((size_t)dm * dm * 4);
@@ -268,7 +317,7 @@ BlockLayout block_layout(const gptq_block_shape_t& sh, const gptq_params_t& p) {
   size_t w3 = 0;
   for (int i = 0; i < 7; ++i) {
     int64_t rows, d;
-    layer_dims(sh, i, rows, d);
+    layer_dims(sh, attn, i, rows, d);
     w3 = std::max(w3, (size_t)rows * split3_pitch(d) * 2);
   }
   L.off_w3 = take(w3);                                  // a weight as fp16 [hi | lo | hi | 0]
@@ -282,7 +331,7 @@ BlockLayout block_layout(const gptq_block_shape_t& sh, const gptq_params_t& p) {
   L.quant_bytes = 0;
   for (int i = 0; i < 7; ++i) {
     int64_t rows, d;
-    layer_dims(sh, i, rows, d);
+    layer_dims(sh, attn, i, rows, d);
     L.quant_bytes = std::max(L.quant_bytes, gptq_workspace_bytes(GPTQ_WS_QUANTIZE, rows, d, &p));
   }
   L.off_qw = take(L.quant_bytes);
@@ -295,10 +344,10 @@ BlockLayout block_layout(const gptq_block_shape_t& sh, const gptq_params_t& p) {
 // recomputed through the quantized o; down's input through the quantized gate and up. With
 // true_sequential = 0 every input comes from the block with its original weights. The block output
 // Y always runs through the quantized weights (the next block's input).
-int quantize_block(const gptq_block_shape_t& sh, const void* X, int x_dtype, const gptq_params_t& p,
-                   int true_sequential, const gptq_block_layer_t* layers, float* Y, float* const* hess, char* work,
-                   int64_t* info, hipStream_t s) {
-  const BlockLayout L = block_layout(sh, p);
+int quantize_block(const gptq_block_shape_t& sh, const gptq_block_attn_t* attn, const void* X, int x_dtype,
+                   const gptq_params_t& p, int true_sequential, const gptq_block_layer_t* layers, float* Y,
+                   float* const* hess, char* work, int64_t* info, hipStream_t s) {
+  const BlockLayout L = block_layout(sh, attn, p);
   const int64_t n = sh.seqs * sh.seq_len, hd = sh.hidden, di = sh.inter;
   float* xf = reinterpret_cast<float*>(work + L.off_xf);
   float* xa = reinterpret_cast<float*>(work + L.off_xa);
@@ -344,7 +393,7 @@ int quantize_block(const gptq_block_shape_t& sh, const void* X, int x_dtype, con
     }
     for (int i = first; i <= last; ++i) {
       int64_t rows, dd;
-      layer_dims(sh, i, rows, dd);
+      layer_dims(sh, attn, i, rows, dd);
       if (i != first && layers[i].perm != layers[first].perm)
         GPTQ_TRY(hipMemcpyAsync(layers[i].perm, layers[first].perm, (size_t)d * 4, hipMemcpyDeviceToDevice, s));
       st = gptq_quantize_layer(layers[i].W, layers[i].w_dtype, rows, d, d, U, layers[i].perm, &p, layers[i].codes,
@@ -357,7 +406,7 @@ int quantize_block(const gptq_block_shape_t& sh, const void* X, int x_dtype, con
   // dense fp32 weights of layer i: its quantized values or its original ones
   auto weight = [&](int i, bool quantized) -> hipError_t {
     int64_t rows, d;
-    layer_dims(sh, i, rows, d);
+    layer_dims(sh, attn, i, rows, d);
     if (!quantized) return to_f32(layers[i].W, layers[i].w_dtype, rows * d, Wf, s);
     const int64_t g = p.group_size <= 0 ? d : p.group_size;
     return dequantize(layers[i].codes, rows, d, layers[i].scales, layers[i].zeros, layers[i].g_idx, g, Wf, d, s);
@@ -371,7 +420,7 @@ int quantize_block(const gptq_block_shape_t& sh, const void* X, int x_dtype, con
   float* mx = reinterpret_cast<float*>(work + L.off_mx);
   auto project = [&](int i, bool quantized, float* out, bool accumulate) -> int {
     int64_t rows, d;
-    layer_dims(sh, i, rows, d);
+    layer_dims(sh, attn, i, rows, d);
     GPTQ_TRY(weight(i, quantized));
     GPTQ_TRY(absmax(Wf, rows * d, mx + 1, mx, s));
     float wmax = 0.0f;
@@ -399,8 +448,16 @@ int quantize_block(const gptq_block_shape_t& sh, const void* X, int x_dtype, con
     if ((st = project(0, quantized, q, false)) != GPTQ_OK) return st;
     if ((st = project(1, quantized, k, false)) != GPTQ_OK) return st;
     if ((st = project(2, quantized, v, false)) != GPTQ_OK) return st;
-    GPTQ_TRY(causal_attention(q, k, v, sh.seqs, sh.seq_len, sh.heads, hd / sh.heads, hd, at, hd, S,
-                              reinterpret_cast<_Float16*>(work + L.off_qk3), s));
+    if (!attn) {
+      GPTQ_TRY(causal_attention(q, k, v, sh.seqs, sh.seq_len, sh.heads, hd / sh.heads, hd, at, hd, S,
+                                reinterpret_cast<_Float16*>(work + L.off_qk3), s));
+    } else {
+      if (attn->qk_norm || attn->rotary_dim)
+        GPTQ_TRY(norm_rotate(block_rotate(sh, *attn), q, k, attn->q_norm, attn->k_norm, attn->positions,
+                             attn->inv_freq, attn->pair_axis, q, k, s));
+      GPTQ_TRY(attention(block_attention(sh, *attn), q, k, v, nullptr, nullptr, attn->slopes, attn->doc, attn->doc,
+                         attn->prefix, at, work + L.off_aw, L.attn_bytes, s));
+    }
     GPTQ_TRY(split_input(at, hd));
     if (quantize && (st = stage(1, hd, 3, 3)) != GPTQ_OK) return st;
     GPTQ_TRY(hipMemcpyAsync(h1, xf, (size_t)n * hd * 4, hipMemcpyDeviceToDevice, s));

@@ -255,10 +255,15 @@ hipError_t to_f32(const void* x, int dtype, int64_t n, float* y, hipStream_t s);
 // Hessian, factor and column-loop workspaces.
 struct BlockLayout {
   size_t off_xf, off_xa, off_q, off_k, off_v, off_at, off_h1, off_xm, off_g, off_u, off_s, off_wf, off_h, off_uf,
-      off_qk3, off_xs, off_w3, off_mx, off_h2, off_hw, off_fw, off_qw, hess_bytes, factor_bytes, quant_bytes, total;
+      off_qk3, off_xs, off_w3, off_mx, off_h2, off_hw, off_fw, off_qw, off_aw, hess_bytes, factor_bytes, quant_bytes,
+      attn_bytes, total;
 };
-BlockLayout block_layout(const gptq_block_shape_t& sh, const gptq_params_t& p);
-int quantize_block(const gptq_block_shape_t& sh, const void* X, int x_dtype, const gptq_params_t& p,
+// attn: the block's attention (gptq_quantize_block_attn), or null for the plain causal one.
+gptq_norm_rotate_t block_rotate(const gptq_block_shape_t& sh, const gptq_block_attn_t& attn);
+gptq_attention_t block_attention(const gptq_block_shape_t& sh, const gptq_block_attn_t& attn);
+BlockLayout block_layout(const gptq_block_shape_t& sh, const gptq_block_attn_t* attn, const gptq_params_t& p);
+int quantize_block(const gptq_block_shape_t& sh, const gptq_block_attn_t* attn, const void* X, int x_dtype,
+                   const gptq_params_t& p,
                    int true_sequential, const gptq_block_layer_t* layers, float* Y, float* const* hess, char* work,
                    int64_t* info, hipStream_t s);
 

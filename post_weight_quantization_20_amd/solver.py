@@ -392,10 +392,62 @@ class BlockShape:
         return _lib.gptq_block_shape_t(int(self.hidden), int(self.heads), int(self.inter), int(self.seqs),
                                        int(self.seq_len), float(self.eps))
 
-    def layer_dims(self, i: int) -> Tuple[int, int]:
-        """(rows, d) of layer i in BLOCK_LAYERS order."""
+    def layer_dims(self, i: int, kv_heads: Optional[int] = None) -> Tuple[int, int]:
+        """(rows, d) of layer i in BLOCK_LAYERS order; kv_heads (None: heads) sets the rows of k and v."""
         rows = self.inter if i in (4, 5) else self.hidden
+        if i in (1, 2) and kv_heads is not None:
+            rows = kv_heads * (self.hidden // self.heads)
         return rows, (self.inter if i == 6 else self.hidden)
+
+
+@dataclass
+class BlockAttention:
+    """The attention of a block (gptq_block_attn_t): shared key heads, per-head norm, rotation, masks.
+    Tensors are contiguous on the block's device; int32 except inv_freq and slopes (float32) and the norm
+    weights (fp32/fp16/bf16, [head_dim])."""
+
+    kv_heads: int
+    qk_norm: bool = False
+    q_norm: Optional[torch.Tensor] = None
+    k_norm: Optional[torch.Tensor] = None
+    norm_eps: float = 1e-6
+    inv_freq: Optional[torch.Tensor] = None    # [rotary_dim / 2]; None: no rotation
+    positions: Optional[torch.Tensor] = None   # [tokens] or [axes, tokens]
+    pair_axis: Optional[torch.Tensor] = None   # [rotary_dim / 2]
+    interleaved: bool = False
+    scale: float = 0.0                         # 0: 1 / sqrt(head_dim)
+    softcap: float = 0.0
+    slopes: Optional[torch.Tensor] = None      # [heads]
+    doc: Optional[torch.Tensor] = None         # [tokens]
+    prefix: Optional[torch.Tensor] = None      # [seqs]
+    causal: bool = True
+
+    def c(self, shape: BlockShape, device=None) -> _lib.gptq_block_attn_t:
+        """The C descriptor; checks the tensors (on `device`, when given)."""
+        n, dh = shape.seqs * shape.seq_len, shape.hidden // shape.heads
+        rd = 0 if self.inv_freq is None else 2 * self.inv_freq.numel()
+        axes = self.positions.shape[0] if self.positions is not None and self.positions.dim() == 2 else 1
+        pos = (n,) if self.positions is None or self.positions.dim() == 1 else (axes, n)
+        w_dtype = torch.float32
+        for name in ("q_norm", "k_norm"):
+            w = getattr(self, name)
+            if w is not None:
+                if w.dtype not in _DTYPE:
+                    raise ValueError(f"{name} must be fp32/fp16/bf16")
+                w_dtype = w.dtype
+        for name, sh, dt in (("q_norm", (dh,), w_dtype), ("k_norm", (dh,), w_dtype),
+                             ("inv_freq", (rd // 2,), torch.float32), ("positions", pos, torch.int32),
+                             ("pair_axis", (rd // 2,), torch.int32), ("slopes", (shape.heads,), torch.float32),
+                             ("doc", (n,), torch.int32), ("prefix", (shape.seqs,), torch.int32)):
+            t = getattr(self, name)
+            if t is not None:
+                _need_cuda(t)
+                _want(t, sh, dt, name, device)
+        ptr = [None if getattr(self, f) is None else getattr(self, f).data_ptr()
+               for f in ("q_norm", "k_norm", "inv_freq", "positions", "pair_axis", "slopes", "doc", "prefix")]
+        return _lib.gptq_block_attn_t(int(self.kv_heads), *ptr, float(self.norm_eps), float(self.scale),
+                                      float(self.softcap), int(bool(self.qk_norm)), _DTYPE[w_dtype], rd,
+                                      int(bool(self.interleaved)), axes, int(bool(self.causal)))
 
 
 @dataclass
@@ -406,15 +458,20 @@ class BlockResult:
     hessians: Optional[list]          # float32 [d, d] per stage (upper triangle), when asked for
 
 
-def gptq_block_workspace_bytes(shape: BlockShape, params: Params) -> int:
+def gptq_block_workspace_bytes(shape: BlockShape, params: Params, attn: Optional[BlockAttention] = None) -> int:
+    if attn is not None:
+        return int(_lib.lib().gptq_block_attn_workspace_bytes(ctypes.byref(shape.c()), ctypes.byref(attn.c(shape)),
+                                                              ctypes.byref(params.c())))
     return int(_lib.lib().gptq_block_workspace_bytes(ctypes.byref(shape.c()), ctypes.byref(params.c())))
 
 
 def gptq_quantize_block(X: torch.Tensor, weights, shape: BlockShape, params: Params, true_sequential: bool = True,
                         return_hessians: bool = False, work: Optional[torch.Tensor] = None,
-                        stream=None) -> BlockResult:
+                        stream=None, attn: Optional[BlockAttention] = None) -> BlockResult:
     """Quantizes the seven layers of one decoder block (weights in BLOCK_LAYERS order, each
-    contiguous [rows, d]) from its input X [seqs * seq_len, hidden], true-sequential by default."""
+    contiguous [rows, d]) from its input X [seqs * seq_len, hidden], true-sequential by default. attn: the
+    block's attention where it is not plain causal multi-head attention (k and v then have
+    attn.kv_heads * head_dim rows)."""
     _need_cuda(X, work, *weights)
     n = shape.seqs * shape.seq_len
     if len(weights) != 7:
@@ -422,10 +479,12 @@ def gptq_quantize_block(X: torch.Tensor, weights, shape: BlockShape, params: Par
     if X.dim() != 2 or tuple(X.shape) != (n, shape.hidden) or not X.is_contiguous() or X.dtype not in _DTYPE:
         raise ValueError("X must be contiguous [seqs * seq_len, hidden], fp32/fp16/bf16")
     dev = X.device
+    kv = None if attn is None else attn.kv_heads
+    attn_c = None if attn is None else attn.c(shape, dev)
     outs, perms = [], []
     arr = (_lib.gptq_block_layer_t * 7)()
     for i, W in enumerate(weights):
-        rows, d = shape.layer_dims(i)
+        rows, d = shape.layer_dims(i, kv)
         if tuple(W.shape) != (rows, d) or not W.is_contiguous() or W.dtype not in _DTYPE:
             raise ValueError(f"{BLOCK_LAYERS[i]}: weights must be contiguous [{rows}, {d}], fp32/fp16/bf16")
         ng = params.groups(d)
@@ -445,7 +504,7 @@ def gptq_quantize_block(X: torch.Tensor, weights, shape: BlockShape, params: Par
         widths = (shape.hidden, shape.hidden, shape.hidden, shape.inter)
         hess = [torch.empty((w, w), dtype=torch.float32, device=dev) for w in widths]
         hptr = (ctypes.c_void_p * 4)(*[h.data_ptr() for h in hess])
-    nb = gptq_block_workspace_bytes(shape, params)
+    nb = gptq_block_workspace_bytes(shape, params, attn)
     if nb == 0:
         raise ValueError("invalid block shape or settings")
     if work is None:
@@ -453,8 +512,11 @@ def gptq_quantize_block(X: torch.Tensor, weights, shape: BlockShape, params: Par
     else:
         _want_work(work, nb, dev)
     info = (ctypes.c_int64 * 2)()
-    st = _lib.lib().gptq_quantize_block(ctypes.byref(shape.c()), _ptr(X), _DTYPE[X.dtype], ctypes.byref(params.c()),
-                                        int(bool(true_sequential)), arr, _ptr(Y), hptr, _ptr(work), work.numel(),
-                                        info, _stream(stream))
+    args = (_ptr(X), _DTYPE[X.dtype], ctypes.byref(params.c()), int(bool(true_sequential)), arr, _ptr(Y), hptr,
+            _ptr(work), work.numel(), info, _stream(stream))
+    if attn is None:
+        st = _lib.lib().gptq_quantize_block(ctypes.byref(shape.c()), *args)
+    else:
+        st = _lib.lib().gptq_quantize_block_attn(ctypes.byref(shape.c()), ctypes.byref(attn_c), *args)
     _check(st, int(info[1]))
     return BlockResult(layers=outs, perms=perms, Y=Y, hessians=hess)

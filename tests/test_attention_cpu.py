@@ -197,3 +197,41 @@ def test_oracle_lora_by_hand():
     B = np.array([[[2.0, 7.0]]])
     y, _ = attn_ref.lora(x, A, B, [0, -1], scales=[0.5], ranks=[1], base=np.array([[10.0], [20.0]]))
     assert np.allclose(y.ravel(), [13, 20])
+
+
+# ------------------------------------------------------------------------------------ block driver
+
+def _block_attn_bytes(**kw):
+    L = _lib()
+    shape = L.gptq_block_shape_t(64, 4, 96, 2, 40, 1e-6)
+    p = L.gptq_params_t(4, 32, 32, 0, 0, 0, 0, 0.01)
+    d = dict(kv_heads=2, norm_eps=1e-6, axes=1, causal=1)
+    d.update(kw)
+    return L.lib().gptq_block_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(L.gptq_block_attn_t(**d)),
+                                                   ctypes.byref(p))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(kv_heads=0), dict(kv_heads=3), dict(kv_heads=8), dict(norm_eps=-1.0), dict(axes=0), dict(causal=2),
+    dict(softcap=-1.0), dict(scale=float("nan")), dict(rotary_dim=8), dict(rotary_dim=18), dict(q_norm=FAKE),
+    dict(w_dtype=5), dict(qk_norm=3), dict(rotary_dim=8, inv_freq=FAKE),
+], ids=str)
+def test_block_attention_rejects_settings(kw):
+    assert _block_attn_bytes(**kw) == 0
+
+
+def test_block_attention_accepts_and_rejects_a_short_workspace():
+    L = _lib()
+    n = _block_attn_bytes()
+    assert n > 0 and _block_attn_bytes(rotary_dim=8, inv_freq=FAKE, positions=FAKE, qk_norm=1, q_norm=FAKE) > 0
+    shape = L.gptq_block_shape_t(64, 4, 96, 2, 40, 1e-6)
+    p = L.gptq_params_t(4, 32, 32, 0, 0, 0, 0, 0.01)
+    at = L.gptq_block_attn_t(kv_heads=2, norm_eps=1e-6, axes=1, causal=1)
+    lay = (L.gptq_block_layer_t * 7)(*[L.gptq_block_layer_t(*[FAKE] * 7, 1) for _ in range(7)])
+    info = (ctypes.c_int64 * 2)(5, 5)
+    f = L.lib().gptq_quantize_block_attn
+    P = ctypes.c_void_p(FAKE)
+    assert f(ctypes.byref(shape), ctypes.byref(at), P, 1, ctypes.byref(p), 1, lay, P, None, P, n - 1, info, None) == ENOMEM
+    assert f(ctypes.byref(shape), None, P, 1, ctypes.byref(p), 1, lay, P, None, P, n, info, None) == EINVAL
+    assert f(None, ctypes.byref(at), P, 1, ctypes.byref(p), 1, lay, P, None, P, n, info, None) == EINVAL
+    assert list(info) == [-1, 0]
