@@ -840,19 +840,27 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     const int64_t row = it / a.hq;
     if (!in_a_sequence(a, row, lane)) continue;
     const int h = (int)(it - row * a.hq);
-    float m = -INFINITY, l = 0.f;
-    for (int z = 0; z < a.nsplit; ++z) m = fmaxf(m, a.part_ml[2 * ((int64_t)z * total + it)]);
+    // lane z holds range z's maximum and sum (at most 64 ranges)
+    const bool mine = lane < a.nsplit;
+    float mz = -INFINITY, lz = 0.f;
+    if (mine) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * ((int64_t)lane * total + it));
+      mz = ml.x;
+      lz = ml.y;
+    }
+    const float m = wave_max(mz);
+    // a range that the row does not see takes no part
+    const float f = mz == -INFINITY && lz == 0.f ? 0.f : __builtin_amdgcn_exp2f(mz - m);
+    const float l = wave_add(lz * f);
     constexpr int NC = 4;
     float acc[NC] = {};
+#pragma unroll 8
     for (int z = 0; z < a.nsplit; ++z) {
-      const int64_t pr = (int64_t)z * total + it;
-      const float mz = a.part_ml[2 * pr], lz = a.part_ml[2 * pr + 1];
-      if (mz == -INFINITY && lz == 0.f) continue;   // a range that the row does not see
-      const float f = __builtin_amdgcn_exp2f(mz - m);
-      l += lz * f;
+      const float fz = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), z));
+      const float* po = a.part_o + ((int64_t)z * total + it) * a.dh;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (64 * c + lane < a.dh) acc[c] += a.part_o[pr * a.dh + 64 * c + lane] * f;
+        if (64 * c + lane < a.dh) acc[c] = __builtin_fmaf(po[64 * c + lane], fz, acc[c]);
     }
     T* o = static_cast<T*>(a.out) + row * a.o_ld + h * a.o_hp;
 #pragma unroll
@@ -920,7 +928,8 @@ Plan plan(const gptq_attention_t& t) {
   // 256 keys (of the average sequence).
   const int64_t items = p.tiles * t.kv_heads, keys = t.n_kv / t.seqs;
   p.nsplit = 1;
-  if (items < 512) p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>((1024 + items - 1) / items, keys / 256));
+  if (items < 512)
+    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, (1024 + items - 1) / items), keys / 256));
   return p;
 }
 

@@ -146,18 +146,24 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[t][n] = floatx4{0.f, 0.f, 0.f, 0.f};
       }
-#pragma unroll 4
-      for (int64_t k = k0; k < k1; k += KS) {
-        const int64_t kk = k + quarter * Frag<DT>::N;
-        typename Frag<DT>::T xf[MT], af[NR];
+      // U steps' loads in flight at a time
+      constexpr int U = MT + NR > 4 ? 2 : 4;
+      for (int64_t k = k0; k < k1; k += U * KS) {
+        typename Frag<DT>::T xf[U][MT], af[U][NR];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) xf[t] = load_frag<DT, VEC>(xrow[t], kk, k1, xok[t]);
+        for (int u = 0; u < U; ++u) {
+          const int64_t kk = k + u * KS + quarter * Frag<DT>::N;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) af[n] = load_frag<DT, VEC>(arow[n], kk, k1, aok[n]);
+          for (int t = 0; t < MT; ++t) xf[u][t] = load_frag<DT, VEC>(xrow[t], kk, k1, xok[t]);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+          for (int n = 0; n < NR; ++n) af[u][n] = load_frag<DT, VEC>(arow[n], kk, k1, aok[n]);
+        }
 #pragma unroll
-          for (int n = 0; n < NR; ++n) acc[t][n] = dot_step<DT>(xf[t], af[n], acc[t][n]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int n = 0; n < NR; ++n) acc[t][n] = dot_step<DT>(xf[u][t], af[u][n], acc[t][n]);
       }
       __syncthreads();   // the last partial sums have been read
       if (wave) {

@@ -63,11 +63,14 @@ GPTQ_DEV float2 turn(int32_t pos, float f) {
 
 // The workgroup takes tokens_per_wg tokens and heads_per_wg of their hq + hk heads (queries first).
 // MC: chunks per lane.
-template <int DT, int V, int G, int MC>
+template <int DT, int V, int G, int MC, bool WEIGHTS>
 __global__ __launch_bounds__(256) void norm_rotate_kernel(RotArgs a) {
   typedef typename ElemOf<DT>::T T;
   typedef T Vec __attribute__((ext_vector_type(V)));
-  extern __shared__ float2 cs[];   // [tokens_per_wg][rd / 2]
+  extern __shared__ __align__(16) float smem[];
+  // the weights of a query's and a key's columns, then the angles [tokens_per_wg][rd / 2]
+  float* wl = smem;
+  float2* cs = reinterpret_cast<float2*>(smem + (WEIGHTS ? 2 * ((a.dh + 3) & ~3) : 0));
   const int half = a.rd >> 1;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_wg;
   const int nt = (int)min((int64_t)a.tokens_per_wg, a.n - t0);
@@ -77,22 +80,33 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(RotArgs a) {
     ax = ax < 0 ? 0 : ax >= a.axes ? a.axes - 1 : ax;
     cs[i] = turn(a.pos[(int64_t)ax * a.pos_ld + t0 + t], a.inv_freq[p]);
   }
+  if constexpr (WEIGHTS) {
+    const int kb = (a.dh + 3) & ~3;
+    for (int i = threadIdx.x; i < a.dh; i += 256) {
+      wl[i] = a.qw ? load_as_f32(a.qw, a.w_dtype, i) : 1.0f;
+      wl[kb + i] = a.kw ? load_as_f32(a.kw, a.w_dtype, i) : 1.0f;
+    }
+  }
   __syncthreads();
 
   const int sub = threadIdx.x % G;
   const int h0 = (int)blockIdx.y * a.heads_per_wg;
   const int nh = min(a.heads_per_wg, a.hq + a.hk - h0);
   const int items = nt * nh;
-  for (int it = threadIdx.x / G; it < items; it += 256 / G) {
-    const int t = it / nh;
-    const int h = h0 + it - t * nh;
+  int t = 0, hl = threadIdx.x / G;   // the item's token and head
+  for (int it = hl; it < items; it += 256 / G, hl += 256 / G) {
+    while (hl >= nh) {
+      hl -= nh;
+      ++t;
+    }
+    const int h = h0 + hl;
     const bool isq = h < a.hq;
     const int64_t tok = t0 + t;
     const T* x = isq ? static_cast<const T*>(a.q) + tok * a.q_ld + h * a.q_hp
                      : static_cast<const T*>(a.k) + tok * a.k_ld + (h - a.hq) * a.k_hp;
     T* o = isq ? static_cast<T*>(a.qo) + tok * a.qo_ld + h * a.qo_hp
                : static_cast<T*>(a.ko) + tok * a.ko_ld + (h - a.hq) * a.ko_hp;
-    const void* w = isq ? a.qw : a.kw;
+    const float* w = wl + (isq ? 0 : (a.dh + 3) & ~3);
     float u[MC][V], v[MC][V];   // the two sides of the lane's pairs
     int ca[MC], cb[MC];         // their first columns (cb = dh: none)
     float ss = 0.f;
@@ -130,9 +144,9 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(RotArgs a) {
         for (int e = 0; e < V; ++e) {
           u[m][e] *= r;
           v[m][e] *= r;
-          if (w) {
-            if (ca[m] < a.dh) u[m][e] *= load_as_f32(w, a.w_dtype, ca[m] + e);
-            if (cb[m] < a.dh) v[m][e] *= load_as_f32(w, a.w_dtype, cb[m] + e);
+          if constexpr (WEIGHTS) {
+            if (ca[m] < a.dh) u[m][e] *= w[ca[m] + e];
+            if (cb[m] < a.dh) v[m][e] *= w[cb[m] + e];
           }
         }
     }
@@ -176,8 +190,12 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(RotArgs a) {
 
 template <int DT, int V, int G, int MC>
 hipError_t launch(const RotArgs& a, dim3 grid, hipStream_t s) {
-  hipLaunchKernelGGL((norm_rotate_kernel<DT, V, G, MC>), grid, dim3(256),
-                     (size_t)a.tokens_per_wg * (a.rd / 2) * sizeof(float2), s, a);
+  const size_t angles = (size_t)a.tokens_per_wg * (a.rd / 2) * sizeof(float2);
+  if (a.qw || a.kw)
+    hipLaunchKernelGGL((norm_rotate_kernel<DT, V, G, MC, true>), grid, dim3(256),
+                       angles + 2 * ((a.dh + 3) & ~3) * sizeof(float), s, a);
+  else
+    hipLaunchKernelGGL((norm_rotate_kernel<DT, V, G, MC, false>), grid, dim3(256), angles, s, a);
   return hipGetLastError();
 }
 
