@@ -854,13 +854,20 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     const float l = wave_add(lz * f);
     constexpr int NC = 4;
     float acc[NC] = {};
-#pragma unroll 8
-    for (int z = 0; z < a.nsplit; ++z) {
-      const float fz = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), z));
-      const float* po = a.part_o + ((int64_t)z * total + it) * a.dh;
+    for (int z0 = 0; z0 < a.nsplit; z0 += 8) {
+      float v[8][NC];
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        if (64 * c + lane < a.dh) acc[c] = __builtin_fmaf(po[64 * c + lane], fz, acc[c]);
+      for (int e = 0; e < 8; ++e) {
+        const float* po = a.part_o + ((int64_t)(z0 + e < a.nsplit ? z0 + e : z0) * total + it) * a.dh;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) v[e][c] = 64 * c + lane < a.dh ? po[64 * c + lane] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {   // lanes past the last range hold a factor of zero
+        const float fz = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), z0 + e));
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[c] = __builtin_fmaf(v[e][c], fz, acc[c]);
+      }
     }
     T* o = static_cast<T*>(a.out) + row * a.o_ld + h * a.o_hp;
 #pragma unroll

@@ -36,7 +36,8 @@ struct LoraArgs {
   int64_t ldb;
   float* y;
   int64_t ldy;
-  float* T;          // [ksplit][m][rank]
+  float* T;          // [ksplit][m][rp]
+  int rp;            // rank rounded up to 16
   int ksplit;        // ranges of d over the grid
   int64_t kper;      // columns of a range, a multiple of 4 waves x 32
   int slot_groups;   // workgroups that share out a tile's slots (shrink)
@@ -116,7 +117,10 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
   constexpr int KS = 4 * Frag<DT>::N;     // columns of a step
   __shared__ floatx4 part[3][MT][NR][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t i0 = (int64_t)blockIdx.x * 16 * MT;
+  // neighbouring tiles, which share adapters, on one XCD (workgroups go to the eight in turn)
+  const int64_t per = gridDim.x >> 3;
+  const int64_t tile = blockIdx.x < 8 * per ? (blockIdx.x & 7) * per + (blockIdx.x >> 3) : blockIdx.x;
+  const int64_t i0 = tile * 16 * MT;
   const int ad = adapter_of(a, i0, 16 * MT, lane);
   const int esz = DT == F32 ? 4 : 2;
   const int l16 = lane & 15, quarter = lane >> 4;
@@ -130,7 +134,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
   }
   const int64_t k0 = blockIdx.y * a.kper + wave * (a.kper / 4);
   const int64_t k1 = min(a.d, k0 + a.kper / 4);
-  float* T = a.T + (int64_t)blockIdx.y * a.m * a.rank;
+  float* T = a.T + (int64_t)blockIdx.y * a.m * a.rp;
   each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
     if (slot % a.slot_groups != (int)blockIdx.z) return;
     const int r = rank_of(a, adapter);
@@ -189,7 +193,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int row = 16 * t + 4 * quarter + e;
-              if (k < a.rank && ((mine >> row) & 1)) T[(i0 + row) * a.rank + k] = s[e];
+              if (k < a.rp && ((mine >> row) & 1)) T[(i0 + row) * a.rp + k] = s[e];
             }
           }
       }
@@ -222,21 +226,59 @@ GPTQ_DEV floatx4 load_b4(const void* B, int64_t at, int k, int r, bool vec) {
 // consecutive columns of y of row l % 16.
 template <int DT, int MT, int NJ, bool SLOTS>
 __global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
-  extern __shared__ __align__(16) float ts[];   // [16 MT][rank rounded up to 16, + 4]
+  extern __shared__ __align__(16) float ts[];   // [16 MT][rp + 4]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, quarter = lane >> 4;
   const int64_t i0 = (a.tile0 + blockIdx.y) * 16 * MT;
   const int64_t j0 = SLOTS ? (int64_t)blockIdx.x * 16 * NJ : ((int64_t)blockIdx.x * 4 + wave) * 16 * NJ;
   const int ad = adapter_of(a, i0, 16 * MT, lane);
-  const int rp = (a.rank + 15) / 16 * 16, pitch = rp + 4;
-  // T of the tile's rows, the ranges of d added in order
-  for (int e = threadIdx.x; e < 16 * MT * rp; e += 256) {
-    const int row = e / rp, k = e - row * rp;
-    const int ra = __shfl(ad, row, 64);   // a wave's 64 elements can span rows
-    float s = 0.f;
-    if (ra >= 0 && k < a.rank)
-      for (int p = 0; p < a.ksplit; ++p) s += a.T[((int64_t)p * a.m + i0 + row) * a.rank + k];
-    ts[row * pitch + k] = s;
+  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+  const uint64_t with = __ballot(ad >= 0);   // rows with an adapter
+  // base of this lane's rows and columns, on its way while T is formed
+  floatx4 o[MT][NJ];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t i = i0 + 16 * t + l16;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t c = j0 + 16 * j + 4 * quarter;
+      o[t][j] = zero;
+      if (!a.base || i >= a.m) continue;
+      const float* bp = a.base + i * a.ldb + c;
+      if (a.yvec && c + 4 <= a.rows) {
+        o[t][j] = *reinterpret_cast<const floatx4*>(bp);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < a.rows) o[t][j][e] = bp[e];
+      }
+    }
+  }
+  // T of the tile's rows, the ranges of d added in order, four ranks a thread and four such pieces at a
+  // time; rows without an adapter (whose T is not written) are zero
+  const int rp = a.rp, pitch = rp + 4, q4 = rp >> 2, pieces = 16 * MT * q4;
+  for (int e0 = threadIdx.x; e0 < pieces; e0 += 4 * 256) {
+    floatx4 s[4];
+    const float* p[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + 256 * u, row = e / q4;
+      s[u] = zero;
+      p[u] = e < pieces && ((with >> row) & 1) ? a.T + (i0 + row) * rp + 4 * (e - row * q4) : nullptr;
+    }
+    for (int z = 0; z < a.ksplit; ++z)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (p[u]) {
+          const floatx4 v = *reinterpret_cast<const floatx4*>(p[u] + (int64_t)z * a.m * rp);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[u][c] += v[c];
+        }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + 256 * u, row = e / q4;
+      if (e < pieces) *reinterpret_cast<floatx4*>(ts + row * pitch + 4 * (e - row * q4)) = s[u];
+    }
   }
   __syncthreads();
   if (j0 >= a.rows) return;
@@ -244,21 +286,18 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
   auto store = [&](int t, int j, const floatx4& v, float scale, int64_t i) {
     const int64_t c = j0 + 16 * j + 4 * quarter;
     float* yp = a.y + i * a.ldy + c;
-    const float* bp = a.base ? a.base + i * a.ldb + c : nullptr;
-    if (a.yvec && c + 4 <= a.rows) {
-      floatx4 o = {0.f, 0.f, 0.f, 0.f};
-      if (bp) o = *reinterpret_cast<const floatx4*>(bp);
+    floatx4 r = o[t][j];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(scale, v[e], o[e]);
-      *reinterpret_cast<floatx4*>(yp) = o;
+    for (int e = 0; e < 4; ++e) r[e] = __builtin_fmaf(scale, v[e], r[e]);
+    if (a.yvec && c + 4 <= a.rows) {
+      *reinterpret_cast<floatx4*>(yp) = r;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c + e < a.rows) yp[e] = __builtin_fmaf(scale, v[e], bp ? bp[e] : 0.f);
+        if (c + e < a.rows) yp[e] = r[e];
     }
   };
 
-  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
   each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
     if (SLOTS && (slot & 3) != wave) return;
     const int r = rank_of(a, adapter);
@@ -294,7 +333,6 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
       }
   });
   // rows without an adapter
-  const uint64_t with = __ballot(ad >= 0);
   if (SLOTS && wave != 0) return;
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
@@ -349,7 +387,7 @@ hipError_t shrink(const LoraArgs& a, const Plan& p, hipStream_t s) {
 template <int DT, int MT, int NJ, bool SLOTS>
 hipError_t launch_expand(const LoraArgs& a, hipStream_t s) {
   const int64_t cols = (SLOTS ? 1 : 4) * 16 * NJ;
-  const size_t lds = (size_t)16 * MT * ((a.rank + 15) / 16 * 16 + 4) * sizeof(float);
+  const size_t lds = (size_t)16 * MT * (a.rp + 4) * sizeof(float);
   // a grid holds fewer than 2^32 threads: very wide outputs take their row tiles in several launches
   const int64_t xs = (a.rows + cols - 1) / cols, tiles = (a.m + 16 * MT - 1) / (16 * MT);
   const int64_t step = std::min<int64_t>(65535, std::max<int64_t>(1, ((int64_t)1 << 23) / xs));
@@ -378,7 +416,7 @@ hipError_t run(const LoraArgs& a, const Plan& p, hipStream_t s) {
 
 size_t lora_workspace_bytes(int64_t m, int64_t d, int64_t, int64_t adapters, int32_t rank) {
   m = std::min(m, kPiece);
-  return (size_t)plan(m, d, adapters).ksplit * m * rank * 4;
+  return (size_t)plan(m, d, adapters).ksplit * m * ((rank + 15) / 16 * 16) * 4;
 }
 
 hipError_t lora_gemm(const void* x, int dtype, int64_t m, int64_t ldx, const void* A, const void* B,
@@ -389,6 +427,7 @@ hipError_t lora_gemm(const void* x, int dtype, int64_t m, int64_t ldx, const voi
   LoraArgs a{};
   a.x = x; a.ldx = ldx; a.m = m; a.d = d; a.rows = rows;
   a.A = A; a.B = B; a.adapters = adapters; a.rank = rank;
+  a.rp = (rank + 15) / 16 * 16;
   a.ranks = ranks; a.index = index; a.scales = scales;
   a.base = base; a.ldb = ld_base; a.y = y; a.ldy = ldy;
   a.T = static_cast<float*>(work);
