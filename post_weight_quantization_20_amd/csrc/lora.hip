@@ -20,6 +20,7 @@
 
 namespace gptq {
 namespace {
+constexpr int EW = 4;   // waves of an expand workgroup
 
 typedef short v8s __attribute__((ext_vector_type(8)));
 
@@ -39,7 +40,7 @@ struct LoraArgs {
   float* T;          // [ksplit][m][rp]
   int rp;            // rank rounded up to 16
   int ksplit;        // ranges of d over the grid
-  int64_t kper;      // columns of a range, a multiple of 4 waves x 32
+  int64_t kper;      // columns of a range, a multiple of 32
   int slot_groups;   // workgroups that share out a tile's slots (shrink)
   int64_t tile0;     // first row tile of the launch (expand)
   int xvec, bvec, yvec;
@@ -132,8 +133,11 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
     xok[t] = i < a.m;
     xrow[t] = static_cast<const char*>(a.x) + (xok[t] ? i : 0) * a.ldx * esz;
   }
-  const int64_t k0 = blockIdx.y * a.kper + wave * (a.kper / 4);
-  const int64_t k1 = min(a.d, k0 + a.kper / 4);
+  // U steps' loads in flight at a time; the waves take such pieces of the range in turn, so that the
+  // workgroup reads each row in long runs
+  constexpr int U = 4, STEP = U * KS;
+  const int64_t k0 = blockIdx.y * a.kper + wave * STEP;
+  const int64_t k1 = min(a.d, (int64_t)(blockIdx.y + 1) * a.kper);
   float* T = a.T + (int64_t)blockIdx.y * a.m * a.rp;
   each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
     if (slot % a.slot_groups != (int)blockIdx.z) return;
@@ -150,9 +154,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[t][n] = floatx4{0.f, 0.f, 0.f, 0.f};
       }
-      // U steps' loads in flight at a time
-      constexpr int U = MT + NR > 4 ? 2 : 4;
-      for (int64_t k = k0; k < k1; k += U * KS) {
+      for (int64_t k = k0; k < k1; k += 4 * STEP) {
         typename Frag<DT>::T xf[U][MT], af[U][NR];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -201,68 +203,74 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
   });
 }
 
-// Four consecutive elements of a row of B as floats, zeros from column r on.
-template <int DT>
-GPTQ_DEV floatx4 load_b4(const void* B, int64_t at, int k, int r, bool vec) {
-  floatx4 v = {0.f, 0.f, 0.f, 0.f};
+// N consecutive elements of a row of B as floats, zeros from column r on.
+template <int DT, int N>
+GPTQ_DEV void load_b(const void* B, int64_t at, int k, int r, bool vec, float (&v)[N]) {
   typedef typename ElemOf<DT>::T T;
   const T* p = static_cast<const T*>(B) + at + k;
-  if (vec && k + 4 <= r) {
-    typedef T V4 __attribute__((ext_vector_type(4)));
-    const V4 u = *reinterpret_cast<const V4*>(p);
+  if (vec && k + N <= r) {
+    typedef T V __attribute__((ext_vector_type(N)));
+    const V u = *reinterpret_cast<const V*>(p);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)u[e];
+    for (int e = 0; e < N; ++e) v[e] = (float)u[e];
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (k + e < r) v[e] = (float)p[e];
+    for (int e = 0; e < N; ++e) v[e] = k + e < r ? (float)p[e] : 0.f;
   }
-  return v;
 }
 
 // y of 16 MT rows. SLOTS: the four waves share 16 NJ columns and take the tile's slots in turn (each row is
 // written by the wave of its slot); otherwise each wave takes 16 NJ columns of its own and every slot. The
 // MFMA's lane l holds B row (column of y) l % 16 and T row l % 16 at ranks 4 (l / 16) .. + 3, and gets four
 // consecutive columns of y of row l % 16.
-template <int DT, int MT, int NJ, bool SLOTS>
-__global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
+template <int DT, int MT, int NJ, int KN, bool SLOTS>
+__global__ __launch_bounds__(64 * EW) void expand_kernel(LoraArgs a) {
   extern __shared__ __align__(16) float ts[];   // [16 MT][rp + 4]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, quarter = lane >> 4;
   const int64_t i0 = (a.tile0 + blockIdx.y) * 16 * MT;
-  const int64_t j0 = SLOTS ? (int64_t)blockIdx.x * 16 * NJ : ((int64_t)blockIdx.x * 4 + wave) * 16 * NJ;
   const int ad = adapter_of(a, i0, 16 * MT, lane);
   const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
   const uint64_t with = __ballot(ad >= 0);   // rows with an adapter
-  // base of this lane's rows and columns, on its way while T is formed
+  // base of this lane's rows and columns
+  constexpr int64_t COLS = (SLOTS ? 1 : EW) * 16 * NJ;
+  const int64_t j0 = blockIdx.x * COLS + (SLOTS ? 0 : wave * 16 * NJ);
+  // base of the rows this wave writes, on its way while T is formed
   floatx4 o[MT][NJ];
+  {
+    int64_t owner = 0;   // the wave of this lane's row: its slot's, the first for rows without an adapter
+    if (SLOTS)
+      each_slot(ad, [&](int slot, int, uint64_t mine) {
+        if ((mine >> l16) & 1) owner = slot % EW;
+      });
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int64_t i = i0 + 16 * t + l16;
+    for (int t = 0; t < MT; ++t) {
+      const int64_t i = i0 + 16 * t + l16;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int64_t c = j0 + 16 * j + 4 * quarter;
-      o[t][j] = zero;
-      if (!a.base || i >= a.m) continue;
-      const float* bp = a.base + i * a.ldb + c;
-      if (a.yvec && c + 4 <= a.rows) {
-        o[t][j] = *reinterpret_cast<const floatx4*>(bp);
-      } else {
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t c = j0 + 16 * j + 4 * quarter;
+        o[t][j] = zero;
+        if (!a.base || i >= a.m || c >= a.rows || (SLOTS && owner != wave)) continue;
+        const float* bp = a.base + i * a.ldb + c;
+        if (a.yvec && c + 4 <= a.rows) {
+          o[t][j] = *reinterpret_cast<const floatx4*>(bp);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e < a.rows) o[t][j][e] = bp[e];
+          for (int e = 0; e < 4; ++e)
+            if (c + e < a.rows) o[t][j][e] = bp[e];
+        }
       }
     }
   }
   // T of the tile's rows, the ranges of d added in order, four ranks a thread and four such pieces at a
   // time; rows without an adapter (whose T is not written) are zero
   const int rp = a.rp, pitch = rp + 4, q4 = rp >> 2, pieces = 16 * MT * q4;
-  for (int e0 = threadIdx.x; e0 < pieces; e0 += 4 * 256) {
+  for (int e0 = threadIdx.x; e0 < pieces; e0 += 4 * 64 * EW) {
     floatx4 s[4];
     const float* p[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int e = e0 + 256 * u, row = e / q4;
+      const int e = e0 + 64 * EW * u, row = e / q4;
       s[u] = zero;
       p[u] = e < pieces && ((with >> row) & 1) ? a.T + (i0 + row) * rp + 4 * (e - row * q4) : nullptr;
     }
@@ -276,13 +284,13 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
         }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int e = e0 + 256 * u, row = e / q4;
+      const int e = e0 + 64 * EW * u, row = e / q4;
       if (e < pieces) *reinterpret_cast<floatx4*>(ts + row * pitch + 4 * (e - row * q4)) = s[u];
     }
   }
   __syncthreads();
-  if (j0 >= a.rows) return;
 
+  if (j0 >= a.rows) return;
   auto store = [&](int t, int j, const floatx4& v, float scale, int64_t i) {
     const int64_t c = j0 + 16 * j + 4 * quarter;
     float* yp = a.y + i * a.ldy + c;
@@ -299,7 +307,7 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
   };
 
   each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
-    if (SLOTS && (slot & 3) != wave) return;
+    if (SLOTS && slot % EW != wave) return;
     const int r = rank_of(a, adapter);
     const float scale = a.scales ? a.scales[adapter] : 1.0f;
     floatx4 acc[MT][NJ];
@@ -307,23 +315,27 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[t][j] = zero;
-    for (int k0 = 0; k0 < r; k0 += 16) {
-      const int k = k0 + 4 * quarter;
-      floatx4 b[NJ], t4[MT];
+    for (int k0 = 0; k0 < r; k0 += 4 * KN) {
+      const int k = k0 + KN * quarter;
+      float b[NJ][KN];
+      floatx4 t4[MT][KN / 4];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int64_t jr = min(j0 + 16 * j + l16, a.rows - 1);
-        b[j] = load_b4<DT>(a.B, ((int64_t)adapter * a.rows + jr) * a.rank, k, r, a.bvec);
+        load_b<DT, KN>(a.B, ((int64_t)adapter * a.rows + jr) * a.rank, k, r, a.bvec, b[j]);
       }
 #pragma unroll
-      for (int t = 0; t < MT; ++t) t4[t] = *reinterpret_cast<const floatx4*>(ts + (16 * t + l16) * pitch + k);
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+        for (int c = 0; c < KN / 4; ++c)
+          t4[t][c] = *reinterpret_cast<const floatx4*>(ts + (16 * t + l16) * pitch + k + 4 * c);
+#pragma unroll
+      for (int e = 0; e < KN; ++e)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
-            acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j][e], t4[t][e], acc[t][j], 0, 0, 0);
+            acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j][e], t4[t][e / 4][e % 4], acc[t][j], 0, 0, 0);
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -344,6 +356,8 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraArgs a) {
   }
 }
 
+int padded_rank(int rank) { return (rank + 15) / 16 * 16; }
+
 // How the call is laid out, from its sizes alone.
 struct Plan {
   int mt_shrink, slot_groups, ksplit;
@@ -357,8 +371,9 @@ Plan plan(int64_t m, int64_t d, int64_t adapters) {
   const int64_t tile = 16 * p.mt_shrink, tiles = (m + tile - 1) / tile;
   // Few tiles: a workgroup for each slot. Then d is split until there are about 512 workgroups, in ranges
   // of at least 512 columns (128 a wave).
-  p.slot_groups = tiles >= 64 ? 1 : (int)std::min<int64_t>(std::min(tile, m), std::max<int64_t>(1, adapters));
-  const int64_t wgs = tiles * p.slot_groups;
+  // Long inputs: workgroups for two slots of a tile, so that a tile where two prompts meet takes no longer.
+  p.slot_groups = (int)std::min<int64_t>(tiles >= 64 ? 2 : std::min(tile, m), std::max<int64_t>(1, adapters));
+  const int64_t wgs = tiles >= 64 ? tiles : tiles * p.slot_groups;
   p.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, (512 + wgs - 1) / wgs), d / 512));
   p.kper = ((d + p.ksplit - 1) / p.ksplit + 127) / 128 * 128;
   p.ksplit = (int)((d + p.kper - 1) / p.kper);
@@ -384,9 +399,9 @@ hipError_t shrink(const LoraArgs& a, const Plan& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int DT, int MT, int NJ, bool SLOTS>
-hipError_t launch_expand(const LoraArgs& a, hipStream_t s) {
-  const int64_t cols = (SLOTS ? 1 : 4) * 16 * NJ;
+template <int DT, int MT, int NJ, int KN, bool SLOTS>
+hipError_t launch_expand_k(const LoraArgs& a, hipStream_t s) {
+  const int64_t cols = (SLOTS ? 1 : EW) * 16 * NJ;
   const size_t lds = (size_t)16 * MT * (a.rp + 4) * sizeof(float);
   // a grid holds fewer than 2^32 threads: very wide outputs take their row tiles in several launches
   const int64_t xs = (a.rows + cols - 1) / cols, tiles = (a.m + 16 * MT - 1) / (16 * MT);
@@ -394,20 +409,28 @@ hipError_t launch_expand(const LoraArgs& a, hipStream_t s) {
   for (int64_t t0 = 0; t0 < tiles; t0 += step) {
     LoraArgs b = a;
     b.tile0 = t0;
-    hipLaunchKernelGGL((expand_kernel<DT, MT, NJ, SLOTS>), dim3((unsigned)xs, (unsigned)std::min(step, tiles - t0)),
-                       dim3(256), lds, s, b);
+    hipLaunchKernelGGL((expand_kernel<DT, MT, NJ, KN, SLOTS>), dim3((unsigned)xs, (unsigned)std::min(step, tiles - t0)),
+                       dim3(64 * EW), lds, s, b);
   }
   return hipGetLastError();
+}
+
+template <int DT, int MT, int NJ, bool SLOTS>
+hipError_t launch_expand(const LoraArgs& a, hipStream_t s) {
+  // B's rows 16 bytes a lane at a time where the padded rank is whole pieces of four lanes
+  if constexpr (DT != F32)
+    if (a.rp % 32 == 0) return launch_expand_k<DT, MT, NJ, 8, SLOTS>(a, s);
+  return launch_expand_k<DT, MT, NJ, 4, SLOTS>(a, s);
 }
 
 template <int DT>
 hipError_t run(const LoraArgs& a, const Plan& p, hipStream_t s) {
   hipError_t e = a.adapters == 0 ? hipSuccess : a.xvec ? shrink<DT, true>(a, p, s) : shrink<DT, false>(a, p, s);
   if (e != hipSuccess) return e;
-  // Long inputs: 64 rows a tile, so that B is read once for them (32 where T of 64 rows of wide ranks would
-  // leave few workgroups a CU); few rows: 16, slots over the waves, and narrow columns while a launch of
-  // wide ones has fewer than 512 workgroups.
-  if (a.m >= 512) return a.rank <= 128 ? launch_expand<DT, 4, 4, false>(a, s) : launch_expand<DT, 2, 4, false>(a, s);
+  // Long inputs: 32 rows and 128 columns a workgroup. 4096 x 4096 outputs of rank 64 take 55 us with them,
+  // 62 with 64 rows (half B's reads, fewer waves a CU) and 66 with 256 columns (half T's reads). Few rows:
+  // 16, slots over the waves, and narrow columns while a launch of wide ones has fewer than 512 workgroups.
+  if (a.m >= 512) return launch_expand<DT, 2, 2, false>(a, s);
   const int64_t wide = (a.rows + 63) / 64 * ((a.m + 15) / 16);
   return wide >= 512 ? launch_expand<DT, 1, 4, true>(a, s) : launch_expand<DT, 1, 1, true>(a, s);
 }
@@ -416,7 +439,7 @@ hipError_t run(const LoraArgs& a, const Plan& p, hipStream_t s) {
 
 size_t lora_workspace_bytes(int64_t m, int64_t d, int64_t, int64_t adapters, int32_t rank) {
   m = std::min(m, kPiece);
-  return (size_t)plan(m, d, adapters).ksplit * m * ((rank + 15) / 16 * 16) * 4;
+  return (size_t)plan(m, d, adapters).ksplit * m * padded_rank(rank) * 4;
 }
 
 hipError_t lora_gemm(const void* x, int dtype, int64_t m, int64_t ldx, const void* A, const void* B,
@@ -427,16 +450,17 @@ hipError_t lora_gemm(const void* x, int dtype, int64_t m, int64_t ldx, const voi
   LoraArgs a{};
   a.x = x; a.ldx = ldx; a.m = m; a.d = d; a.rows = rows;
   a.A = A; a.B = B; a.adapters = adapters; a.rank = rank;
-  a.rp = (rank + 15) / 16 * 16;
+  a.rp = padded_rank(rank);
   a.ranks = ranks; a.index = index; a.scales = scales;
   a.base = base; a.ldb = ld_base; a.y = y; a.ldy = ldy;
   a.T = static_cast<float*>(work);
   a.ksplit = p.ksplit; a.kper = p.kper; a.slot_groups = p.slot_groups;
-  // 16-byte loads of x and A, four elements of B at a time, 16-byte accesses of base and y
+  // 16-byte loads of x and A, four or eight elements of B at a time, 16-byte accesses of base and y
   const int64_t esz = dtype == F32 ? 4 : 2, n = 16 / esz;
   auto at = [](const void* q, int64_t to) { return reinterpret_cast<uintptr_t>(q) % to == 0; };
   a.xvec = d % n == 0 && ldx % n == 0 && at(x, 16) && at(A, 16);
-  a.bvec = rank % 4 == 0 && at(B, 4 * esz);
+  const int64_t kn = dtype != F32 && a.rp % 32 == 0 ? 8 : 4;
+  a.bvec = rank % kn == 0 && at(B, kn * esz);
   a.yvec = ldy % 4 == 0 && at(y, 16) && (!base || (ld_base % 4 == 0 && at(base, 16)));
   for (int64_t i0 = 0; i0 < m; i0 += kPiece) {
     LoraArgs b = a;
