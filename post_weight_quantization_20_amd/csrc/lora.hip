@@ -262,31 +262,26 @@ __global__ __launch_bounds__(64 * EW) void expand_kernel(LoraArgs a) {
       }
     }
   }
-  // T of the tile's rows, the ranges of d added in order, four ranks a thread and four such pieces at a
-  // time; rows without an adapter (whose T is not written) are zero
+  // T of the tile's rows, the ranges of d added in order, four ranks a thread and eight ranges at a time;
+  // rows without an adapter (whose T is not written) are zero
   const int rp = a.rp, pitch = rp + 4, q4 = rp >> 2, pieces = 16 * MT * q4;
-  for (int e0 = threadIdx.x; e0 < pieces; e0 += 4 * 64 * EW) {
-    floatx4 s[4];
-    const float* p[4];
+  for (int e = threadIdx.x; e < pieces; e += 64 * EW) {
+    const int row = e / q4, k = 4 * (e - row * q4);
+    floatx4 s = zero;
+    if ((with >> row) & 1) {
+      const float* p = a.T + (i0 + row) * rp + k;
+      for (int z0 = 0; z0 < a.ksplit; z0 += 8) {
+        floatx4 v[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = e0 + 64 * EW * u, row = e / q4;
-      s[u] = zero;
-      p[u] = e < pieces && ((with >> row) & 1) ? a.T + (i0 + row) * rp + 4 * (e - row * q4) : nullptr;
+        for (int z = 0; z < 8; ++z)
+          v[z] = z0 + z < a.ksplit ? *reinterpret_cast<const floatx4*>(p + (int64_t)(z0 + z) * a.m * rp) : zero;
+#pragma unroll
+        for (int z = 0; z < 8; ++z)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[c] += v[z][c];
+      }
     }
-    for (int z = 0; z < a.ksplit; ++z)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (p[u]) {
-          const floatx4 v = *reinterpret_cast<const floatx4*>(p[u] + (int64_t)z * a.m * rp);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[u][c] += v[c];
-        }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = e0 + 64 * EW * u, row = e / q4;
-      if (e < pieces) *reinterpret_cast<floatx4*>(ts + row * pitch + 4 * (e - row * q4)) = s[u];
-    }
+    *reinterpret_cast<floatx4*>(ts + row * pitch + k) = s;
   }
   __syncthreads();
 
