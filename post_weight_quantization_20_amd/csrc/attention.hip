@@ -27,7 +27,9 @@ struct AttnArgs {
   float scale, cap;
   const int32_t *q_start, *kv_start, *q_doc, *kv_doc, *prefix;
   const float* slopes;
-  int o_vec;                   // out takes 8-byte stores
+  int o_vec;                   // out takes stores of four elements
+  int64_t lq_even, lk_even;    // sequence lengths without offsets
+  uint32_t seq_tiles;          // and their row tiles
   int64_t tiles;               // row tiles of one key head, over all sequences (an upper bound)
   int nsplit;                  // ranges that a sequence's keys are split into
   float *part_ml, *part_o;     // nsplit > 1: [nsplit][nq][hq][2] and [nsplit][nq][hq][dh]
@@ -47,14 +49,14 @@ GPTQ_DEV Seq sequence(const AttnArgs& a, int64_t s) {
     r.q0 = clamp64(a.q_start[s], 0, a.nq);
     r.lq = clamp64(a.q_start[s + 1], r.q0, a.nq) - r.q0;
   } else {
-    r.lq = a.nq / a.seqs;
+    r.lq = a.lq_even;
     r.q0 = s * r.lq;
   }
   if (a.kv_start) {
     r.k0 = clamp64(a.kv_start[s], 0, a.nk);
     r.lk = clamp64(a.kv_start[s + 1], r.k0, a.nk) - r.k0;
   } else {
-    r.lk = a.nk / a.seqs;
+    r.lk = a.lk_even;
     r.k0 = s * r.lk;
   }
   return r;
@@ -267,8 +269,24 @@ GPTQ_DEV v8s round8(const float* p) {
   }
 }
 
-// The value of the lane 32 away.
-GPTQ_DEV float mirror(float v) { return __shfl_xor(v, 32, 64); }
+// The maximum and the sum with the lane 32 away: the swap of two copies leaves the lower half's values in
+// both halves of one and the upper half's in the other. Written out with the wait states that a just
+// written operand needs: the builtin with one value for both operands gives its first result twice.
+GPTQ_DEV void mirror(float v, float& lo, float& hi) {
+  lo = v;
+  hi = v;
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\ts_nop 1" : "+v"(lo), "+v"(hi));
+}
+GPTQ_DEV float mirror_max(float v) {
+  float lo, hi;
+  mirror(v, lo, hi);
+  return fmaxf(lo, hi);
+}
+GPTQ_DEV float mirror_sum(float v) {
+  float lo, hi;
+  mirror(v, lo, hi);
+  return lo + hi;
+}
 
 // Row tile t of a key head: its sequence and the tile's place in it (seq = -1: past the last tile).
 struct TileAt {
@@ -278,8 +296,8 @@ struct TileAt {
 GPTQ_DEV TileAt find_tile(const AttnArgs& a, int64_t t, int rows, int lane) {
   TileAt r{-1, 0};
   if (!a.q_start) {
-    const int64_t per = (a.nq / a.seqs * a.group + rows - 1) / rows;
-    if (per > 0 && t < per * a.seqs) r = {t / per, t % per};
+    const uint32_t per = a.seq_tiles, u = (uint32_t)t;   // a grid holds fewer than 2^24 tiles
+    if (per > 0 && u / per < a.seqs) r = {u / per, u % per};
     return r;
   }
   int64_t before = 0;
@@ -311,8 +329,8 @@ GPTQ_DEV TileAt find_tile(const AttnArgs& a, int64_t t, int rows, int lane) {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kShift = 7.0f, kRaise = 8.0f;
 
-// DHP: head width padded to 32. DMA: 16-byte aligned tensors. MODE 0: scores only scaled, 1: also capped,
-// biased (or scaled by zero).
+// DHP: head width padded to 32. DMA: 16-byte aligned tensors. MODE 0: scores only scaled, 1: capped, 2: any
+// (a bias, both, scaled by zero; caps in fp32).
 template <int DT, int DHP, int WM, bool DMA, int MODE>
 __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_kernel(AttnArgs a) {
   typedef typename ElemOf<DT>::T T;
@@ -336,17 +354,17 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   GPTQ_LDS uint32_t* masks = (GPTQ_LDS uint32_t*)(tail + 1024);   // [wave]: 16 active bits, 16 whole bits
 
   // the workgroup's key head, tile of rows and range of keys
-  const int64_t per_head = a.tiles * a.nsplit, nb = per_head * a.hk;
-  int64_t kvh, rem;
+  const uint32_t per_head = (uint32_t)a.tiles * a.nsplit;
+  uint32_t kvh, rem;
   if (a.hk % 8 == 0) {   // workgroups go to the 8 XCDs in turn: each takes whole heads, which its L2 keeps
-    const int64_t idx = (int64_t)(blockIdx.x & 7) * (nb >> 3) + (blockIdx.x >> 3);
+    const uint32_t idx = (blockIdx.x & 7) * (per_head * (uint32_t)a.hk >> 3) + (blockIdx.x >> 3);
     kvh = idx / per_head;
     rem = idx - kvh * per_head;
   } else {
-    rem = blockIdx.x / a.hk;
+    rem = blockIdx.x / (uint32_t)a.hk;
     kvh = blockIdx.x - rem * a.hk;
   }
-  const int64_t tord = rem / a.nsplit;
+  const uint32_t tord = rem / (uint32_t)a.nsplit;
   const int z = (int)(rem - tord * a.nsplit);
   TileAt at = find_tile(a, a.tiles - 1 - tord, ROWS, lane);   // long (late) tiles first
   at.seq = (int64_t)uniform64((uint64_t)at.seq);
@@ -358,23 +376,24 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   // this lane's row
   const int64_t r = row0 + (WM == 4 ? 32 * wave : 0) + col;
   const bool live = r < nrows;
-  const int64_t qi = live ? r / a.group : 0;
-  const int g = live ? (int)(r - qi * a.group) : 0;
+  // packed rows of one sequence stay below 2^24 tiles of at most 128
+  const int64_t qi = live ? (uint32_t)r / (uint32_t)a.group : 0;
+  const int g = live ? (int)((uint32_t)r - (uint32_t)qi * a.group) : 0;
   const int h = (int)kvh * a.group + g;
   const int32_t lim = live ? (int32_t)key_limit(a, sq, at.seq, qi) : 0;
   const int32_t qdoc = live && a.q_doc ? a.q_doc[sq.q0 + qi] : 0;
   const int32_t pos = (int32_t)(qi + sq.lk - sq.lq);
   float slope = 0.f;
-  if (MODE == 1 && a.slopes) slope = a.slopes[h];
+  if (MODE == 2 && a.slopes) slope = a.slopes[h];
 
   // keys: the workgroup's range [kb, ke) and, per wave, where masking starts and ends
   const int64_t last_row = (row0 + ROWS < nrows ? row0 + ROWS : nrows) - 1;
-  int64_t ke = key_limit_nodoc(a, sq, at.seq, last_row / a.group);
+  int64_t ke = key_limit_nodoc(a, sq, at.seq, (uint32_t)last_row / (uint32_t)a.group);
   int64_t kb = 0;
   if (a.nsplit > 1) {
-    const int64_t nt = (ke + KT - 1) / KT, per = (nt + a.nsplit - 1) / a.nsplit;
-    kb = z * per * KT;
-    if (ke > kb + per * KT) ke = kb + per * KT;
+    const uint32_t nt = (uint32_t)((ke + KT - 1) / KT), per = (nt + a.nsplit - 1) / (uint32_t)a.nsplit;
+    kb = (int64_t)z * per * KT;
+    if (ke > kb + (int64_t)per * KT) ke = kb + (int64_t)per * KT;
   }
   int32_t wmin = live ? lim : 0x7fffffff, wmax = lim, dmin = live && lim > 0 ? qdoc : 0x7fffffff,
           dmax = live && lim > 0 ? qdoc : -1;
@@ -504,9 +523,12 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
 #pragma unroll
   for (int f = 0; f < NF; ++f) acc[f] = floatx16{};
   float m = -INFINITY, l = 0.f;
-  const float c = MODE == 0 ? fabsf(a.scale) * kLog2e : kLog2e;
+  // a key's weight is 2^(c S): S is the product (MODE 0), -1 / (e^2y + 1) with y = scale q.k / cap, which
+  // is (tanh y - 1) / 2 (MODE 1), or the finished score (MODE 2)
+  const float c = MODE == 0 ? fabsf(a.scale) * kLog2e : MODE == 1 ? 2.0f * a.cap * kLog2e : kLog2e;
   const float raise = kRaise / c;
   const float inv_cap = a.cap > 0.f ? 1.0f / a.cap : 0.f;
+  const float to_cap = 2.0f * kLog2e * inv_cap;
 
   auto compute = [&](int64_t j0, int buf, bool whole) {
     GPTQ_LDS char* kt = base + buf * BUFB;
@@ -527,24 +549,38 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       }
     }
     const int32_t jb = (int32_t)j0 + 4 * half;   // the key of register i of subtile t: jb + 32 t + 8 (i / 4) + i % 4
-    if (MODE == 1) {
+    if constexpr (MODE == 1) {
+      const float k = a.scale * to_cap;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x = S[t][i] * a.scale;
-          if (a.cap > 0.f) {
-            // tanh y = 1 - 2 / (e^2y + 1)
-            if constexpr (DT == F32) {
-              x = a.cap * tanhf(x * inv_cap);
-            } else {
-              const float e2 = __builtin_amdgcn_exp2f(x * inv_cap * (2.0f * kLog2e));
-              x = a.cap - 2.0f * a.cap * __builtin_amdgcn_rcpf(e2 + 1.0f);
-            }
+        for (int i = 0; i < 16; ++i)
+          S[t][i] = -__builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(S[t][i] * k) + 1.0f);
+    }
+    if constexpr (MODE == 2) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[t][i] *= a.scale;
+      if (a.cap > 0.f) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if constexpr (DT == F32)
+              S[t][i] = a.cap * tanhf(S[t][i] * inv_cap);
+            else   // tanh y = 1 - 2 / (e^2y + 1)
+              S[t][i] = a.cap - 2.0f * a.cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(S[t][i] * to_cap) + 1.0f);
           }
-          if (a.slopes) x -= slope * fabsf((float)(pos - (jb + 32 * t + 8 * (i / 4) + i % 4)));
-          S[t][i] = x;
-        }
+      }
+      if (a.slopes) {
+        const float d0 = (float)(pos - jb);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            S[t][i] = __builtin_fmaf(-slope, fabsf(d0 - (float)(32 * t + 8 * (i / 4) + i % 4)), S[t][i]);
+      }
     }
     const bool doc_mask = a.q_doc && !(whole && one_doc);
     if (j0 + KT > wmin || doc_mask) {
@@ -565,18 +601,18 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
               if (kd[e] != qdoc) S[t][4 * b + e] = -INFINITY;
           }
       }
+      const int32_t rel = lim - jb;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (jb + 32 * t + 8 * (i / 4) + i % 4 >= lim) S[t][i] = -INFINITY;
+        for (int i = 0; i < 16; ++i) S[t][i] = rel > 32 * t + 8 * (i / 4) + i % 4 ? S[t][i] : -INFINITY;
     }
     float mx = -INFINITY;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, S[t][i]);
-    mx = fmaxf(mx, mirror(mx));
+    mx = mirror_max(mx);
     if (__ballot(!(mx <= m + raise))) {
       const float m2 = fmaxf(m, mx);
       const float f = m2 == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - m2) * c);
@@ -646,12 +682,24 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       constexpr int QK = KT / 4;
       const int64_t j0 = b0 + QK * (int64_t)threadIdx.x;
       int32_t lo = 0x7fffffff, hi = (int32_t)0x80000000;
-      for (int e = 0; e < QK; ++e)
-        if (j0 + e < ke) {
-          const int32_t d = a.kv_doc[sq.k0 + j0 + e];
-          lo = min(lo, d);
-          hi = max(hi, d);
+      const int32_t* dp = a.kv_doc + sq.k0 + j0;
+      if (j0 + QK <= ke) {
+        typedef int32_t I4 __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+        for (int e = 0; e < QK / 4; ++e) {
+          const I4 d = *reinterpret_cast<const I4*>(dp + 4 * e);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            lo = min(lo, d[b]);
+            hi = max(hi, d[b]);
+          }
         }
+      } else {
+        for (int e = 0; j0 + e < ke; ++e) {
+          lo = min(lo, dp[e]);
+          hi = max(hi, dp[e]);
+        }
+      }
       lo = min(lo, __shfl_xor(lo, 1, 64));
       hi = max(hi, __shfl_xor(hi, 1, 64));
       lo = min(lo, __shfl_xor(lo, 2, 64));
@@ -704,7 +752,7 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       }
     }
   }
-  l += mirror(l);
+  l = mirror_sum(l);
 
   if (WM == 1) {
     // join the waves' partial results in wave order; the tiles' area is free now
@@ -764,7 +812,8 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     const uint64_t o = __ballot(odd && live);
     redo = (uint32_t)o | (uint32_t)(o >> 32);
   }
-  const float mexp = m == -INFINITY ? -INFINITY : m * c - kShift;   // O and l are in units of 2^mexp
+  // O and l are in units of 2^mexp
+  const float mexp = m == -INFINITY ? -INFINITY : m * c + (MODE == 1 ? a.cap * kLog2e : 0.f) - kShift;
   if (live && !((redo >> col) & 1)) {
     const int64_t row = sq.q0 + qi;
     if (a.nsplit > 1) {
@@ -896,23 +945,26 @@ hipError_t launch_mfma(const AttnArgs& a, hipStream_t s) {
 }
 
 template <int DT, int DHP, int WM>
-hipError_t by_mode(const AttnArgs& a, bool dma, bool extra, hipStream_t s) {
-  if (dma) return extra ? launch_mfma<DT, DHP, WM, true, 1>(a, s) : launch_mfma<DT, DHP, WM, true, 0>(a, s);
-  return launch_mfma<DT, DHP, WM, false, 1>(a, s);
+hipError_t by_mode(const AttnArgs& a, bool dma, hipStream_t s) {
+  if (!dma) return launch_mfma<DT, DHP, WM, false, 2>(a, s);
+  if (a.slopes || a.scale == 0.f) return launch_mfma<DT, DHP, WM, true, 2>(a, s);
+  if (a.cap == 0.f) return launch_mfma<DT, DHP, WM, true, 0>(a, s);
+  if constexpr (DT == F32) return launch_mfma<DT, DHP, WM, true, 2>(a, s);
+  else return launch_mfma<DT, DHP, WM, true, 1>(a, s);
 }
 
 template <int DT>
-hipError_t by_head(const AttnArgs& a, bool dma, bool extra, bool few, hipStream_t s) {
+hipError_t by_head(const AttnArgs& a, bool dma, bool few, hipStream_t s) {
   // few rows: each wave needs its own double buffer, which 160 KB of LDS holds up to 128-wide heads
   if (few) {
-    if (a.dh <= 64) return by_mode<DT, 64, 1>(a, dma, extra, s);
-    if (a.dh <= 96) return by_mode<DT, 96, 1>(a, dma, extra, s);
-    return by_mode<DT, 128, 1>(a, dma, extra, s);
+    if (a.dh <= 64) return by_mode<DT, 64, 1>(a, dma, s);
+    if (a.dh <= 96) return by_mode<DT, 96, 1>(a, dma, s);
+    return by_mode<DT, 128, 1>(a, dma, s);
   }
-  if (a.dh <= 64) return by_mode<DT, 64, 4>(a, dma, extra, s);
-  if (a.dh <= 96) return by_mode<DT, 96, 4>(a, dma, extra, s);
-  if (a.dh <= 128) return by_mode<DT, 128, 4>(a, dma, extra, s);
-  return by_mode<DT, 256, 4>(a, dma, extra, s);
+  if (a.dh <= 64) return by_mode<DT, 64, 4>(a, dma, s);
+  if (a.dh <= 96) return by_mode<DT, 96, 4>(a, dma, s);
+  if (a.dh <= 128) return by_mode<DT, 128, 4>(a, dma, s);
+  return by_mode<DT, 256, 4>(a, dma, s);
 }
 
 // The launch's plan: rows a tile holds, tiles, ranges that keys are split into.
@@ -960,6 +1012,8 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
   a.causal = t.causal; a.scale = (float)t.scale; a.cap = (float)t.softcap;
   a.q_start = q_start; a.kv_start = kv_start; a.q_doc = q_doc; a.kv_doc = kv_doc; a.prefix = prefix;
   a.slopes = slopes;
+  a.lq_even = a.nq / a.seqs;
+  a.lk_even = a.nk / a.seqs;
   Plan p = plan(t);
   if (!p.mfma) {
     const int64_t waves = a.nq * a.hq;
@@ -973,6 +1027,8 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
   if (!work || work_bytes < need) p.nsplit = 1;
   a.tiles = p.tiles;
   a.nsplit = p.nsplit;
+  const int64_t rows = p.few ? 32 : 128;
+  a.seq_tiles = (uint32_t)std::min<int64_t>(1 << 24, (a.lq_even * a.group + rows - 1) / rows);
   if (p.nsplit > 1) {
     a.part_ml = static_cast<float*>(work);
     a.part_o = a.part_ml + (int64_t)p.nsplit * a.nq * a.hq * 2;
@@ -986,10 +1042,9 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
   const bool dma = a.dh % unit == 0 && al(q, a.q_ld, a.q_hp) && al(k, a.k_ld, a.k_hp) && al(v, a.v_ld, a.v_hp) &&
                    std::max(a.k_ld, a.v_ld) < ((int64_t)1 << 23);
   a.o_vec = reinterpret_cast<uintptr_t>(out) % (t.dtype == F32 ? 16 : 8) == 0 && a.o_ld % 4 == 0 && a.o_hp % 4 == 0;
-  const bool extra = a.cap > 0.f || a.slopes || a.scale == 0.f;
-  hipError_t e = t.dtype == F32   ? by_head<F32>(a, dma, extra, p.few, s)
-                 : t.dtype == F16 ? by_head<F16>(a, dma, extra, p.few, s)
-                                  : by_head<BF16>(a, dma, extra, p.few, s);
+  hipError_t e = t.dtype == F32   ? by_head<F32>(a, dma, p.few, s)
+                 : t.dtype == F16 ? by_head<F16>(a, dma, p.few, s)
+                                  : by_head<BF16>(a, dma, p.few, s);
   if (e != hipSuccess || p.nsplit <= 1) return e;
   const dim3 grid((unsigned)std::min<int64_t>((a.nq * a.hq + 3) / 4, 65536));
   if (t.dtype == F32) hipLaunchKernelGGL(attn_join_kernel<F32>, grid, dim3(256), 0, s, a);
