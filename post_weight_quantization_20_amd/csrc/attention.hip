@@ -76,15 +76,15 @@ GPTQ_DEV float wave_add(float v) {
 
 // The keys a query may see end at this index: its own position or the prefix, whichever is later, and
 // nothing for a padding document.
-GPTQ_DEV int64_t key_limit_nodoc(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i) {
-  if (!a.causal) return sq.lk;
-  const int64_t p = i + sq.lk - sq.lq + 1, pre = a.prefix ? (int64_t)a.prefix[s] : 0;
-  return clamp64(p > pre ? p : pre, 0, sq.lk);
+GPTQ_DEV int32_t key_limit_nodoc(const AttnArgs& a, const Seq& sq, int32_t prefix, int64_t i) {
+  if (!a.causal) return (int32_t)sq.lk;
+  const int64_t p = i + sq.lk - sq.lq + 1;
+  return (int32_t)clamp64(p > prefix ? p : prefix, 0, sq.lk);
 }
 
 GPTQ_DEV int64_t key_limit(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i) {
   if (a.q_doc && a.q_doc[sq.q0 + i] < 0) return 0;
-  return key_limit_nodoc(a, sq, s, i);
+  return key_limit_nodoc(a, sq, a.prefix ? a.prefix[s] : 0, i);
 }
 
 // Whether a sequence holds this row of q.
@@ -242,7 +242,7 @@ struct Tile {
   static constexpr int KT = WM == 4 && DT != F32 ? 64 : 32;
   static constexpr int TILEB = KT * DHP * ESZ;
   static constexpr int NB = WM == 1 && TILEB > 8192 ? 1 : 2;
-  static constexpr int LDS = NB * 2 * TILEB * (4 / WM) + 1024 + 64;
+  static constexpr int LDS = NB * 2 * TILEB * (4 / WM) + 1024 + 128;
 };
 
 template <int DT>
@@ -288,40 +288,58 @@ GPTQ_DEV float mirror_sum(float v) {
   return lo + hi;
 }
 
-// Row tile t of a key head: its sequence and the tile's place in it (seq = -1: past the last tile).
+// Row tile t of a key head: its sequence, the tile's place in it (seq = -1: past the last tile) and the
+// sequence's ranges and prefix, uniform over the wave.
 struct TileAt {
-  int64_t seq, tile;
+  int64_t seq;
+  uint32_t tile;
+  Seq sq;
+  int32_t prefix;
 };
 
+GPTQ_DEV int32_t lane_value(int32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
 GPTQ_DEV TileAt find_tile(const AttnArgs& a, int64_t t, int rows, int lane) {
-  TileAt r{-1, 0};
+  TileAt r{-1, 0, {}, 0};
   if (!a.q_start) {
     const uint32_t per = a.seq_tiles, u = (uint32_t)t;   // a grid holds fewer than 2^24 tiles
-    if (per > 0 && u / per < a.seqs) r = {u / per, u % per};
+    if (per > 0 && u / per < a.seqs) {
+      r.seq = u / per;
+      r.tile = u % per;
+      r.sq = sequence(a, r.seq);
+      if (a.prefix) r.prefix = a.prefix[r.seq];
+    }
     return r;
   }
+  // a lane takes a sequence; the counts of one group of 64 stay below 2^30 tiles and are summed in 64 bits
   int64_t before = 0;
   for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
     const int64_t s = s0 + lane;
-    int64_t n = 0;
+    Seq q{};
+    int32_t pre = 0, n = 0;
     if (s < a.seqs) {
-      const int64_t q0 = clamp64(a.q_start[s], 0, a.nq), q1 = clamp64(a.q_start[s + 1], q0, a.nq);
-      n = ((q1 - q0) * a.group + rows - 1) / rows;
+      q = sequence(a, s);
+      if (a.prefix) pre = a.prefix[s];
+      // at most 2^30 rows of q: a sequence with more tiles than a grid has is never reached
+      n = (int32_t)min((q.lq * a.group + rows - 1) >> (rows == 32 ? 5 : 7), (int64_t)1 << 24);
     }
-    int64_t sum = n;   // inclusive prefix sum over the lanes
+    int32_t sum = n;   // inclusive prefix sum over the lanes
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int64_t v = __shfl_up(sum, o, 64);
+      const int32_t v = __shfl_up(sum, o, 64);
       if (lane >= o) sum += v;
     }
     const uint64_t past = __ballot(before + sum > t);
     if (past) {
       const int at = __builtin_ctzll(past);
       r.seq = s0 + at;
-      r.tile = t - (before + __shfl(sum, at, 64) - __shfl(n, at, 64));
+      r.tile = (uint32_t)(t - before - lane_value(sum, at) + lane_value(n, at));
+      r.sq = Seq{lane_value((int32_t)q.q0, at), lane_value((int32_t)q.k0, at), lane_value((int32_t)q.lq, at),
+                 lane_value((int32_t)q.lk, at)};
+      r.prefix = lane_value(pre, at);
       return r;
     }
-    before += __shfl(sum, 63, 64);
+    before += lane_value(sum, 63);
   }
   return r;
 }
@@ -348,10 +366,9 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   GPTQ_LDS char* smem = (GPTQ_LDS char*)smem_raw;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
-  // small LDS area behind the tiles: documents of a tile per wave, tile masks
+  // small LDS area behind the tiles: documents of a tile per wave, what the tiles of a block hold
   GPTQ_LDS char* tail = smem + NB * BUFB * (4 / WM);
   GPTQ_LDS int32_t* docs = (GPTQ_LDS int32_t*)tail + 64 * wave;
-  GPTQ_LDS uint32_t* masks = (GPTQ_LDS uint32_t*)(tail + 1024);   // [wave]: 16 active bits, 16 whole bits
 
   // the workgroup's key head, tile of rows and range of keys
   const uint32_t per_head = (uint32_t)a.tiles * a.nsplit;
@@ -366,12 +383,10 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   }
   const uint32_t tord = rem / (uint32_t)a.nsplit;
   const int z = (int)(rem - tord * a.nsplit);
-  TileAt at = find_tile(a, a.tiles - 1 - tord, ROWS, lane);   // long (late) tiles first
-  at.seq = (int64_t)uniform64((uint64_t)at.seq);
-  at.tile = (int64_t)uniform64((uint64_t)at.tile);
+  const TileAt at = find_tile(a, a.tiles - 1 - tord, ROWS, lane);   // long (late) tiles first
   if (at.seq < 0) return;
-  const Seq sq = sequence(a, at.seq);
-  const int64_t nrows = sq.lq * a.group, row0 = at.tile * ROWS;
+  const Seq sq = at.sq;
+  const int64_t nrows = sq.lq * a.group, row0 = (int64_t)at.tile * ROWS;
 
   // this lane's row
   const int64_t r = row0 + (WM == 4 ? 32 * wave : 0) + col;
@@ -380,33 +395,63 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   const int64_t qi = live ? (uint32_t)r / (uint32_t)a.group : 0;
   const int g = live ? (int)((uint32_t)r - (uint32_t)qi * a.group) : 0;
   const int h = (int)kvh * a.group + g;
-  const int32_t lim = live ? (int32_t)key_limit(a, sq, at.seq, qi) : 0;
+  // Q^T operand: row col, unit 2 ks + half of it (on its way while the ranges are found)
+  typedef typename std::conditional<DT == F32, float, short>::type E;   // an element's bits
+  Unit qf[NK];
+  {
+    const E* qp = static_cast<const E*>(a.q) + (sq.q0 + qi) * a.q_ld + h * a.q_hp;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      const int c0 = EPU * (2 * ks + half);
+      Unit f = {};
+      if (live) {
+        if (DMA) {
+          if (c0 < a.dh) f = *reinterpret_cast<const Unit*>(qp + c0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < EPU; ++e)
+            if (c0 + e < a.dh) f[e] = qp[c0 + e];
+        }
+      }
+      qf[ks] = f;
+    }
+  }
   const int32_t qdoc = live && a.q_doc ? a.q_doc[sq.q0 + qi] : 0;
+  const int32_t lim = live && qdoc >= 0 ? key_limit_nodoc(a, sq, at.prefix, qi) : 0;
   const int32_t pos = (int32_t)(qi + sq.lk - sq.lq);
   float slope = 0.f;
   if (MODE == 2 && a.slopes) slope = a.slopes[h];
 
   // keys: the workgroup's range [kb, ke) and, per wave, where masking starts and ends
   const int64_t last_row = (row0 + ROWS < nrows ? row0 + ROWS : nrows) - 1;
-  int64_t ke = key_limit_nodoc(a, sq, at.seq, (uint32_t)last_row / (uint32_t)a.group);
+  int64_t ke = key_limit_nodoc(a, sq, at.prefix, (uint32_t)last_row / (uint32_t)a.group);
   int64_t kb = 0;
   if (a.nsplit > 1) {
     const uint32_t nt = (uint32_t)((ke + KT - 1) / KT), per = (nt + a.nsplit - 1) / (uint32_t)a.nsplit;
     kb = (int64_t)z * per * KT;
     if (ke > kb + (int64_t)per * KT) ke = kb + (int64_t)per * KT;
   }
-  int32_t wmin = live ? lim : 0x7fffffff, wmax = lim, dmin = live && lim > 0 ? qdoc : 0x7fffffff,
-          dmax = live && lim > 0 ? qdoc : -1;
+  // limits rise with the row (padding aside, which sees nothing): the first row's and the last one's
+  const uint32_t seeing = (uint32_t)__ballot(live && qdoc >= 0);
+  const bool all_see = seeing == (uint32_t)__ballot(live);
+  const int32_t wmin = seeing && all_see ? lane_value(lim, 0) : 0;
+  const int32_t wmax = seeing ? lane_value(lim, 31 - __builtin_clz(seeing)) : 0;
+  // the documents of the wave's rows: mostly one
+  int32_t dmin = 0x7fffffff, dmax = -1;
+  bool one_doc = true;
+  if (a.q_doc && seeing) {
+    dmin = dmax = lane_value(qdoc, __builtin_ctz(seeing));
+    one_doc = __ballot(live && qdoc >= 0 && qdoc != dmin) == 0;
+    if (!one_doc) {
+      dmin = live && qdoc >= 0 ? qdoc : 0x7fffffff;
+      dmax = live ? qdoc : -1;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    wmin = min(wmin, __shfl_xor(wmin, o, 64));
-    wmax = max(wmax, __shfl_xor(wmax, o, 64));
-    dmin = min(dmin, __shfl_xor(dmin, o, 64));
-    dmax = max(dmax, __shfl_xor(dmax, o, 64));
+      for (int o = 1; o < 32; o <<= 1) {
+        dmin = min(dmin, __shfl_xor(dmin, o, 64));
+        dmax = max(dmax, __shfl_xor(dmax, o, 64));
+      }
+    }
   }
-  wmin = __builtin_amdgcn_readfirstlane(wmin);
-  wmax = __builtin_amdgcn_readfirstlane(wmax);
-  const bool one_doc = __builtin_amdgcn_readfirstlane(dmin == dmax);   // every live row of the wave
   if (a.q_doc && WM == 4) {   // the workgroup's range of documents
     if (lane == 0) {
       docs[0] = dmin;
@@ -422,36 +467,16 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   dmin = __builtin_amdgcn_readfirstlane(dmin);
   dmax = __builtin_amdgcn_readfirstlane(dmax);
 
-  typedef typename std::conditional<DT == F32, float, short>::type E;   // an element's bits
   const E* kp = static_cast<const E*>(a.k) + sq.k0 * a.k_ld + kvh * a.k_hp;
   const E* vp = static_cast<const E*>(a.v) + sq.k0 * a.v_ld + kvh * a.v_hp;
-
-  // Q^T operand: row col, unit 2 ks + half of it; negated for a negative scale, so that the largest score
-  // is the largest product
-  Unit qf[NK];
-  {
-    const E* qp = static_cast<const E*>(a.q) + (sq.q0 + qi) * a.q_ld + h * a.q_hp;
-    const bool flip = MODE == 0 && a.scale < 0.f;
+  if (MODE == 0 && a.scale < 0.f) {   // the largest score is the largest product of -q
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      const int c0 = EPU * (2 * ks + half);
-      Unit f = {};
-      if (live) {
-        if (DMA) {
-          if (c0 < a.dh) f = *reinterpret_cast<const Unit*>(qp + c0);
-        } else {
-#pragma unroll
-          for (int e = 0; e < EPU; ++e)
-            if (c0 + e < a.dh) f[e] = qp[c0 + e];
-        }
-      }
+    for (int ks = 0; ks < NK; ++ks)
 #pragma unroll
       for (int e = 0; e < EPU; ++e) {
-        if constexpr (DT == F32) f[e] = flip ? -f[e] : f[e];
-        else f[e] ^= flip ? (short)0x8000 : (short)0;
+        if constexpr (DT == F32) qf[ks][e] = -qf[ks][e];
+        else qf[ks][e] ^= (short)0x8000;
       }
-      qf[ks] = f;
-    }
   }
 
   // staging: load q of this wave fills 16-byte units 64 (q + LOADS wave') + lane of a tile
@@ -674,6 +699,7 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   // rows' range are found first, a quarter tile a thread. `ready` in the unaligned WM = 1 form is a workgroup
   // barrier, so there every wave takes the same number of steps.
   const int64_t step = WM == 4 ? KT : 4 * KT;
+  int parity = 0;
   for (int64_t b0 = kb; b0 < ke; b0 += 64 * step) {
     uint64_t active = ~0ull, whole = 0;
     const int64_t left = (ke - b0 + step - 1) / step;
@@ -704,24 +730,16 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       hi = max(hi, __shfl_xor(hi, 1, 64));
       lo = min(lo, __shfl_xor(lo, 2, 64));
       hi = max(hi, __shfl_xor(hi, 2, 64));
-      uint64_t on = __ballot(lo <= dmax && hi >= dmin), full = __ballot(lo == hi && lo == dmin && dmin == dmax);
-      // one bit of each four
-      uint32_t b_on = 0, b_full = 0;
-      for (int e = 0; e < 16; ++e) {
-        b_on |= (uint32_t)((on >> (4 * e)) & 1) << e;
-        b_full |= (uint32_t)((full >> (4 * e)) & 1) << e;
-      }
+      // bit 0: holds a document of the range, bit 1: nothing but the one document of all rows. Two areas in
+      // turn: a wave may still read the last block's.
+      GPTQ_LDS uint8_t* state = (GPTQ_LDS uint8_t*)(tail + 1024) + 64 * parity;
+      parity ^= 1;
+      if ((lane & 3) == 0)
+        state[threadIdx.x >> 2] = (lo <= dmax && hi >= dmin ? 1 : 0) | (lo == hi && lo == dmin && dmin == dmax ? 2 : 0);
       __syncthreads();
-      if (lane == 0) masks[wave] = b_on | (b_full << 16);
-      __syncthreads();
-      uint64_t m_on = 0, m_full = 0;
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t v = masks[w];
-        m_on |= (uint64_t)(v & 0xffffu) << (16 * w);
-        m_full |= (uint64_t)(v >> 16) << (16 * w);
-      }
-      active &= m_on;
-      whole = m_full;
+      const uint32_t st = state[lane];
+      active &= __ballot(st & 1);
+      whole = __ballot(st & 2);
     }
     active = uniform64(active);
     whole = uniform64(whole);
@@ -802,11 +820,12 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   }
 
   // rows whose sum is not finite: computed again without the keys they do not see
-  bool odd = !(fabsf(l) < INFINITY);
+  float nothing = l * 0.f;   // zero, unless a value is not finite
 #pragma unroll
   for (int ft = 0; ft < NF; ++ft)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) odd |= !(fabsf(acc[ft][i]) < INFINITY);
+    for (int i = 0; i < 16; ++i) nothing = __builtin_fmaf(acc[ft][i], 0.f, nothing);
+  const bool odd = !(nothing == 0.f);
   uint32_t redo = 0;
   {
     const uint64_t o = __ballot(odd && live);
