@@ -228,21 +228,28 @@ GPTQ_DEV void dma16(i32x4 rsrc, uint32_t voff, uint32_t lds_addr) {
                : "memory");
 }
 
+GPTQ_DEV void dma4(i32x4 rsrc, uint32_t voff, uint32_t lds_addr) {
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds_addr)
+               : "memory");
+}
+
 // Buffer descriptor of `bytes` bytes from a wave-uniform address.
 GPTQ_DEV i32x4 descriptor(uint64_t base, int64_t bytes) {
   const uint64_t b = uniform64(base);
   return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
-// Keys of a tile and buffers, within 160 KB of LDS (two workgroups a CU where rows are shared and the
-// head is at most 128 wide).
+// Keys of a tile and buffers, within 160 KB of LDS: two workgroups a CU up to 128-wide heads (16-bit types).
+// WM = 1 waves have one buffer each: a wave's wait is covered by the seven others of its CU, and two
+// workgroups a CU with one buffer beat one with two (16 tokens against 4915 keys each, 32 / 8 heads of 128:
+// 67 against 71 us, one token against 16384: 21 against 28).
 template <int DT, int DHP, int WM>
 struct Tile {
   static constexpr int ESZ = DT == F32 ? 4 : 2;
   static constexpr int KT = WM == 4 && DT != F32 ? 64 : 32;
   static constexpr int TILEB = KT * DHP * ESZ;
-  static constexpr int NB = WM == 1 && TILEB > 8192 ? 1 : 2;
-  static constexpr int LDS = NB * 2 * TILEB * (4 / WM) + 1024 + 128;
+  static constexpr int NB = WM == 1 ? 1 : 2;
+  static constexpr int LDS = NB * 2 * TILEB * (4 / WM) + 2048 + 128;
 };
 
 template <int DT>
@@ -350,7 +357,7 @@ constexpr float kShift = 7.0f, kRaise = 8.0f;
 // DHP: head width padded to 32. DMA: 16-byte aligned tensors. MODE 0: scores only scaled, 1: capped, 2: any
 // (a bias, both, scaled by zero; caps in fp32).
 template <int DT, int DHP, int WM, bool DMA, int MODE>
-__global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(AttnArgs a) {
   typedef typename ElemOf<DT>::T T;
   typedef Tile<DT, DHP, WM> C;
   constexpr int KT = C::KT, NB = C::NB;         // keys of a tile, buffers
@@ -368,15 +375,16 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
   const int col = lane & 31, half = lane >> 5;
   // small LDS area behind the tiles: documents of a tile per wave, what the tiles of a block hold
   GPTQ_LDS char* tail = smem + NB * BUFB * (4 / WM);
-  GPTQ_LDS int32_t* docs = (GPTQ_LDS int32_t*)tail + 64 * wave;
+  GPTQ_LDS int32_t* docs = (GPTQ_LDS int32_t*)tail + 128 * wave;   // two tiles' worth
 
   // the workgroup's key head, tile of rows and range of keys
-  const uint32_t per_head = (uint32_t)a.tiles * a.nsplit;
   uint32_t kvh, rem;
-  if (a.hk % 8 == 0) {   // workgroups go to the 8 XCDs in turn: each takes whole heads, which its L2 keeps
-    const uint32_t idx = (blockIdx.x & 7) * (per_head * (uint32_t)a.hk >> 3) + (blockIdx.x >> 3);
-    kvh = idx / per_head;
-    rem = idx - kvh * per_head;
+  if (a.hk % 8 == 0) {
+    // Workgroups go to the 8 XCDs in turn: each takes an eighth of the heads, which its L2 keeps, tile by
+    // tile (head by head, an XCD's last head would run alone: 4 x 2048 fp32 tokens took a fifth longer).
+    const uint32_t mine = (uint32_t)a.hk >> 3, at = blockIdx.x >> 3;
+    rem = at / mine;
+    kvh = (blockIdx.x & 7) * mine + (at - rem * mine);
   } else {
     rem = blockIdx.x / (uint32_t)a.hk;
     kvh = blockIdx.x - rem * a.hk;
@@ -459,8 +467,8 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     }
     __syncthreads();
     for (int w = 0; w < 4; ++w) {
-      dmin = min(dmin, ((GPTQ_LDS int32_t*)tail)[64 * w]);
-      dmax = max(dmax, ((GPTQ_LDS int32_t*)tail)[64 * w + 1]);
+      dmin = min(dmin, ((GPTQ_LDS int32_t*)tail)[128 * w]);
+      dmax = max(dmax, ((GPTQ_LDS int32_t*)tail)[128 * w + 1]);
     }
     __syncthreads();
   }
@@ -500,7 +508,8 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     }
   }
   GPTQ_LDS char* base = smem + (WM == 4 ? 0 : wave * NB * BUFB);
-  auto stage = [&](int64_t j0, int buf) {
+  // whole: every key of the tile has the document of all rows, so their documents are not needed
+  auto stage = [&](int64_t j0, int buf, bool whole) {
     const int64_t left = sq.lk - j0;
     const int rows = left < KT ? (int)left : KT;
     GPTQ_LDS char* kd = base + buf * BUFB + LOADS * sub * 1024;
@@ -514,7 +523,11 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       for (int i = 0; i < LOADS; ++i) dma16(kr, kvo[i], k32 + 1024 * i);
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) dma16(vr, vvo[i], v32 + 1024 * i);
+      if (a.q_doc && !(whole && one_doc))   // keys past the last one read as document 0 and are past every limit
+        dma4(descriptor((uint64_t)(uintptr_t)(a.kv_doc + sq.k0 + j0), 4 * rows), 4 * lane,
+             (uint32_t)(uintptr_t)(docs + 64 * buf));
     } else {
+      if (a.q_doc) docs[64 * buf + lane] = lane < rows ? a.kv_doc[sq.k0 + j0 + lane] : -1;
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
         Unit kx = {}, vx = {};
@@ -611,16 +624,10 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     if (j0 + KT > wmin || doc_mask) {
       if (doc_mask) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int64_t j = j0 + 32 * t + col;
-          if (half == 0) docs[32 * t + col] = j < sq.lk ? a.kv_doc[sq.k0 + j] : -1;
-        }
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const i32x4 kd = *(GPTQ_LDS i32x4*)(docs + 32 * t + 8 * b + 4 * half);
+            const i32x4 kd = *(GPTQ_LDS i32x4*)(docs + 64 * buf + 32 * t + 8 * b + 4 * half);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (kd[e] != qdoc) S[t][4 * b + e] = -INFINITY;
@@ -732,7 +739,7 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       hi = max(hi, __shfl_xor(hi, 2, 64));
       // bit 0: holds a document of the range, bit 1: nothing but the one document of all rows. Two areas in
       // turn: a wave may still read the last block's.
-      GPTQ_LDS uint8_t* state = (GPTQ_LDS uint8_t*)(tail + 1024) + 64 * parity;
+      GPTQ_LDS uint8_t* state = (GPTQ_LDS uint8_t*)(tail + 2048) + 64 * parity;
       parity ^= 1;
       if ((lane & 3) == 0)
         state[threadIdx.x >> 2] = (lo <= dmax && hi >= dmin ? 1 : 0) | (lo == hi && lo == dmin && dmin == dmax ? 2 : 0);
@@ -751,14 +758,14 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     // every wave is done with both buffers (of the block before)
     if (WM == 4 || !DMA) __syncthreads();
     else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (exists(t)) stage(tile_of(t), 0);
+    if (exists(t)) stage(tile_of(t), 0, (whole >> t) & 1);
     while (true) {
       const int64_t j0 = tile_of(t);
       const bool have = exists(t), full = (whole >> t) & 1;
       active &= active - 1;
       ready();
       if (active) t = __builtin_ctzll(active);
-      if (NB == 2 && active && exists(t)) stage(tile_of(t), buf ^ 1);
+      if (NB == 2 && active && exists(t)) stage(tile_of(t), buf ^ 1, (whole >> t) & 1);
       if (have && j0 < wmax) compute(j0, buf, full);
       if (!active) break;
       if (NB == 2) {
@@ -766,7 +773,7 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
       } else {   // one buffer: the next tile is loaded when this one has been read
         if (DMA) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         else __syncthreads();
-        if (exists(t)) stage(tile_of(t), 0);
+        if (exists(t)) stage(tile_of(t), 0, (whole >> t) & 1);
       }
     }
   }
@@ -778,7 +785,7 @@ __global__ __launch_bounds__(256, WM == 4 && DHP <= 128 ? 2 : 1) void attn_mfma_
     GPTQ_LDS float* sh = (GPTQ_LDS float*)smem;
     constexpr int PITCH = 64 * (16 * NF + 1);
     GPTQ_LDS float* mine = sh + (wave & 1) * PITCH;
-    GPTQ_LDS float* ml = (GPTQ_LDS float*)tail;
+    GPTQ_LDS float* ml = (GPTQ_LDS float*)tail;   // the documents' area, read no more
     if (half == 0) {
       ml[64 * wave + col] = m;
       ml[64 * wave + 32 + col] = l;
@@ -1002,12 +1009,13 @@ Plan plan(const gptq_attention_t& t) {
   p.few = t.head_dim <= 128 && t.n_q * group <= 32 * t.seqs;
   const int64_t rows = p.few ? 32 : 128;
   p.tiles = t.n_q * group / rows + t.seqs;
-  // Fewer than two workgroups a CU: split the keys until there are about four, in ranges of at least
-  // 256 keys (of the average sequence).
+  // Fewer than two workgroups a CU: split the keys until there are two, in ranges of at least 256 keys (of
+  // the average sequence). More ranges cost more than they fill: 16 tokens against 4915 keys each take 67 us
+  // with 512 workgroups and 71 with 768.
   const int64_t items = p.tiles * t.kv_heads, keys = t.n_kv / t.seqs;
   p.nsplit = 1;
   if (items < 512)
-    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, (1024 + items - 1) / items), keys / 256));
+    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, (512 + items - 1) / items), keys / 256));
   return p;
 }
 
