@@ -7,7 +7,6 @@ device's current stream; outputs and workspaces it makes itself are allocated on
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional, Tuple
@@ -15,26 +14,35 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from .solver import _DTYPE, GPTQ_F32, _check, _ptr
+from .solver import _DTYPE, GPTQ_F32, _check
 
 
-@contextlib.contextmanager
-def _other_stream(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device)
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+class _Here:
+    """Nothing to enter: the call's device is current and so is its stream."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
 
 
-def _on(device, stream):
-    """The call's device made current, and the stream it runs on (allocations follow it)."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream must be on {device}")
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(torch.cuda.current_stream(device))
-    return _other_stream(device, stream)
+_HERE = _Here()
+
+
+def _place(device, stream):
+    """(hipStream_t of the call, a context that makes its device and stream current, so that allocations
+    follow them). A call on the current stream of the current device pays for neither."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device}")
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    here = _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return torch._C._cuda_getCurrentRawStream(device.index), here
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _device(first: torch.Tensor, **others) -> torch.device:
@@ -118,7 +126,8 @@ def gptq_norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor] = None, position
         _vector(pair_axis, (rd // 2,), torch.int32, "pair_axis")
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need inv_freq")
-    with _on(dev, stream) as s:
+    s, here = _place(dev, stream)
+    with here:
         if q_out is None:
             q_out = torch.empty((n, hq, dh), dtype=q.dtype, device=dev)
         if k is not None and k_out is None:
@@ -135,7 +144,7 @@ def gptq_norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor] = None, position
                                     int(bool(norm)))
         _check(_lib.lib().gptq_norm_rotate(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
                                            _ptr(positions), _ptr(inv_freq), _ptr(pair_axis), _ptr(q_out), _ptr(k_out),
-                                           ctypes.c_void_p(s.cuda_stream)))
+                                           s))
     return q_out, k_out
 
 
@@ -188,7 +197,8 @@ def gptq_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Opt
     _vector(prefix, (seqs,), torch.int32, "prefix")
     if (q_doc is None) != (kv_doc is None):
         raise ValueError("q_doc and kv_doc go together")
-    with _on(dev, stream) as s:
+    s, here = _place(dev, stream)
+    with here:
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=dev)
         a = _attention_args(q, k, v, seqs, scale, causal, softcap, out)
@@ -199,7 +209,7 @@ def gptq_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Opt
         work = _scratch(work, 0 if work is not None else int(L.gptq_attention_workspace_bytes(ctypes.byref(a))), dev)
         _check(L.gptq_attention(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(q_start), _ptr(kv_start),
                                 _ptr(slopes), _ptr(q_doc), _ptr(kv_doc), _ptr(prefix), _ptr(out), _ptr(work),
-                                work.numel(), ctypes.c_void_p(s.cuda_stream)))
+                                work.numel(), s))
     return out
 
 
@@ -227,7 +237,8 @@ def gptq_lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, index: tor
     _vector(index, (m,), torch.int32, "index")
     _vector(scales, (na,), torch.float32, "scales")
     _vector(ranks, (na,), torch.int32, "ranks")
-    with _on(dev, stream) as s:
+    s, here = _place(dev, stream)
+    with here:
         if y is None:
             y = torch.empty((m, rows), dtype=torch.float32, device=dev)
         for name, t in (("base", base), ("y", y)):
@@ -240,5 +251,5 @@ def gptq_lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, index: tor
                                 _ptr(scales), na, r, _ptr(index), rows, d, _ptr(base),
                                 0 if base is None else base.stride(0) if m > 1 else rows, _ptr(y),
                                 y.stride(0) if m > 1 else rows, _ptr(work), work.numel(),
-                                ctypes.c_void_p(s.cuda_stream)))
+                                s))
     return y
