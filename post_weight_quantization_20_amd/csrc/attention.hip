@@ -27,7 +27,7 @@ struct AttnArgs {
   float scale, cap;
   const int32_t *q_start, *kv_start, *q_doc, *kv_doc, *prefix;
   const float* slopes;
-  int o_vec;                   // out takes stores of four elements
+  int o_vec, o_rows;           // out takes stores of four elements; of 16 bytes
   int64_t lq_even, lk_even;    // sequence lengths without offsets
   uint32_t seq_tiles;          // and their row tiles
   int64_t tiles;               // row tiles of one key head, over all sequences (an upper bound)
@@ -403,34 +403,9 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
   const int64_t qi = live ? (uint32_t)r / (uint32_t)a.group : 0;
   const int g = live ? (int)((uint32_t)r - (uint32_t)qi * a.group) : 0;
   const int h = (int)kvh * a.group + g;
-  // Q^T operand: row col, unit 2 ks + half of it (on its way while the ranges are found)
-  typedef typename std::conditional<DT == F32, float, short>::type E;   // an element's bits
-  Unit qf[NK];
-  {
-    const E* qp = static_cast<const E*>(a.q) + (sq.q0 + qi) * a.q_ld + h * a.q_hp;
-#pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      const int c0 = EPU * (2 * ks + half);
-      Unit f = {};
-      if (live) {
-        if (DMA) {
-          if (c0 < a.dh) f = *reinterpret_cast<const Unit*>(qp + c0);
-        } else {
-#pragma unroll
-          for (int e = 0; e < EPU; ++e)
-            if (c0 + e < a.dh) f[e] = qp[c0 + e];
-        }
-      }
-      qf[ks] = f;
-    }
-  }
   const int32_t qdoc = live && a.q_doc ? a.q_doc[sq.q0 + qi] : 0;
-  const int32_t lim = live && qdoc >= 0 ? key_limit_nodoc(a, sq, at.prefix, qi) : 0;
-  const int32_t pos = (int32_t)(qi + sq.lk - sq.lq);
-  float slope = 0.f;
-  if (MODE == 2 && a.slopes) slope = a.slopes[h];
 
-  // keys: the workgroup's range [kb, ke) and, per wave, where masking starts and ends
+  // keys: the workgroup's range [kb, ke)
   const int64_t last_row = (row0 + ROWS < nrows ? row0 + ROWS : nrows) - 1;
   int64_t ke = key_limit_nodoc(a, sq, at.prefix, (uint32_t)last_row / (uint32_t)a.group);
   int64_t kb = 0;
@@ -439,7 +414,66 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
     kb = (int64_t)z * per * KT;
     if (ke > kb + (int64_t)per * KT) ke = kb + (int64_t)per * KT;
   }
-  // limits rise with the row (padding aside, which sees nothing): the first row's and the last one's
+  // the documents of a block of 64 tiles, a quarter tile a thread, loaded ahead of their use
+  constexpr int QK = KT / 4;
+  typedef int32_t I4 __attribute__((ext_vector_type(4), aligned(4)));
+  I4 bd[QK / 4];
+  auto fetch_docs = [&](int64_t b0) {
+    const int64_t j0 = b0 + QK * (int64_t)threadIdx.x;
+    const int32_t* dp = a.kv_doc + sq.k0 + j0;
+    if (j0 + QK <= ke) {
+#pragma unroll
+      for (int e = 0; e < QK / 4; ++e) bd[e] = *reinterpret_cast<const I4*>(dp + 4 * e);
+    } else {
+#pragma unroll
+      for (int e = 0; e < QK; ++e) bd[e / 4][e % 4] = j0 + e < ke ? dp[e] : 0;
+    }
+  };
+  if (a.q_doc && WM == 4 && kb < ke) fetch_docs(kb);
+
+  // Q^T operand: row col, unit 2 ks + half of it (on its way while the ranges are found). Loaded like that, a
+  // row at a time, the 32 bytes of a row that an instruction reads come from L2 over and over: 16-bit tiles go
+  // through the second buffer in whole rows.
+  typedef typename std::conditional<DT == F32, float, short>::type E;   // an element's bits
+  constexpr bool QLDS = DMA && WM == 4 && DT != F32;
+  Unit qf[NK];
+  GPTQ_LDS char* qarea = smem + BUFB + wave * 32 * ROWB;
+  if constexpr (QLDS) {
+    const int64_t q0 = (uint32_t)row0 / (uint32_t)a.group;
+    const uint32_t span = (uint32_t)(((ROWS + a.group - 1) / a.group + 1) * a.q_ld + a.group * a.q_hp + a.dh) * ESZ;
+    const i32x4 qr = descriptor((uint64_t)(uintptr_t)(static_cast<const E*>(a.q) + (sq.q0 + q0) * a.q_ld +
+                                                      kvh * a.group * a.q_hp), span);
+    const uint32_t mine = live ? (uint32_t)(((qi - q0) * a.q_ld + g * a.q_hp) * ESZ) : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < UN / 2; ++i) {
+      const int unit = 64 * i + lane, row = unit / UN, u = (unit - row * UN) ^ swz_k<UN>(row);
+      const uint32_t off = (uint32_t)__shfl((int)mine, row, 64);
+      dma16(qr, u * EPU < a.dh ? off + 16 * u : 0x80000000u, (uint32_t)(uintptr_t)(qarea + 1024 * i));
+    }
+  } else {
+    const E* qp = static_cast<const E*>(a.q) + (sq.q0 + qi) * a.q_ld + h * a.q_hp;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      const int c0 = EPU * (2 * ks + half);
+      Unit f = {};
+      if (DMA) {
+        // Past the head K is zero and any finite value will do (a row that holds others is computed again);
+        // lanes past the last row hold the sequence's first.
+        f = *reinterpret_cast<const Unit*>(qp + (c0 < a.dh ? c0 : 0));
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPU; ++e)
+          if (c0 + e < a.dh) f[e] = qp[c0 + e];
+      }
+      qf[ks] = f;
+    }
+  }
+  const int32_t lim = live && qdoc >= 0 ? key_limit_nodoc(a, sq, at.prefix, qi) : 0;
+  const int32_t pos = (int32_t)(qi + sq.lk - sq.lq);
+  float slope = 0.f;
+  if (MODE == 2 && a.slopes) slope = a.slopes[h];
+
+  // Where masking starts and ends for the wave. Limits rise with the row (padding aside, which sees nothing): the first row's and the last one's
   const uint32_t seeing = (uint32_t)__ballot(live && qdoc >= 0);
   const bool all_see = seeing == (uint32_t)__ballot(live);
   const int32_t wmin = seeing && all_see ? lane_value(lim, 0) : 0;
@@ -477,15 +511,19 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
 
   const E* kp = static_cast<const E*>(a.k) + sq.k0 * a.k_ld + kvh * a.k_hp;
   const E* vp = static_cast<const E*>(a.v) + sq.k0 * a.v_ld + kvh * a.v_hp;
-  if (MODE == 0 && a.scale < 0.f) {   // the largest score is the largest product of -q
+  auto negate_q = [&]() {   // for a negative scale: the largest score is the largest product of -q
+    if (MODE == 0 && a.scale < 0.f) {
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks)
+      for (int ks = 0; ks < NK; ++ks)
 #pragma unroll
-      for (int e = 0; e < EPU; ++e) {
-        if constexpr (DT == F32) qf[ks][e] = -qf[ks][e];
-        else qf[ks][e] ^= (short)0x8000;
-      }
-  }
+        for (int e = 0; e < EPU; ++e) {
+          if constexpr (DT == F32) qf[ks][e] = -qf[ks][e];
+          else qf[ks][e] ^= (short)0x8000;
+        }
+    }
+  };
+  bool have_q = !QLDS;
+  if (!QLDS) negate_q();
 
   // staging: load q of this wave fills 16-byte units 64 (q + LOADS wave') + lane of a tile
   const int sub = WM == 4 ? wave : 0;
@@ -712,27 +750,15 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
     const int64_t left = (ke - b0 + step - 1) / step;
     if (left < 64) active = (1ull << left) - 1;
     if (a.q_doc && WM == 4) {
-      constexpr int QK = KT / 4;
       const int64_t j0 = b0 + QK * (int64_t)threadIdx.x;
       int32_t lo = 0x7fffffff, hi = (int32_t)0x80000000;
-      const int32_t* dp = a.kv_doc + sq.k0 + j0;
-      if (j0 + QK <= ke) {
-        typedef int32_t I4 __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
-        for (int e = 0; e < QK / 4; ++e) {
-          const I4 d = *reinterpret_cast<const I4*>(dp + 4 * e);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            lo = min(lo, d[b]);
-            hi = max(hi, d[b]);
-          }
+      for (int e = 0; e < QK; ++e)
+        if (j0 + e < ke) {
+          lo = min(lo, bd[e / 4][e % 4]);
+          hi = max(hi, bd[e / 4][e % 4]);
         }
-      } else {
-        for (int e = 0; j0 + e < ke; ++e) {
-          lo = min(lo, dp[e]);
-          hi = max(hi, dp[e]);
-        }
-      }
+      if (b0 + 64 * step < ke) fetch_docs(b0 + 64 * step);
       lo = min(lo, __shfl_xor(lo, 1, 64));
       hi = max(hi, __shfl_xor(hi, 1, 64));
       lo = min(lo, __shfl_xor(lo, 2, 64));
@@ -764,6 +790,13 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
       const bool have = exists(t), full = (whole >> t) & 1;
       active &= active - 1;
       ready();
+      if (QLDS && !have_q) {
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks) qf[ks] = *(GPTQ_LDS Unit*)(qarea + koff[ks & 3] + 128 * (ks >> 2));
+        negate_q();
+        have_q = true;
+        __syncthreads();   // the second buffer is free
+      }
       if (active) t = __builtin_ctzll(active);
       if (NB == 2 && active && exists(t)) stage(tile_of(t), buf ^ 1, (whole >> t) & 1);
       if (have && j0 < wmax) compute(j0, buf, full);
@@ -777,6 +810,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
       }
     }
   }
+  if (QLDS) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // also where no tile was active
   l = mirror_sum(l);
 
   if (WM == 1) {
@@ -839,6 +873,34 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
     redo = (uint32_t)o | (uint32_t)(o >> 32);
   }
   // O and l are in units of 2^mexp
+  if (WM == 4 && DMA && a.nsplit == 1 && a.o_rows) {
+    // Rows leave through LDS, 16 bytes a lane along each (a lane's own pieces are 8 bytes of every 16): the
+    // tiles' area is free when every wave is here.
+    __syncthreads();
+    GPTQ_LDS char* area = smem + wave * 32 * ROWB;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int ft = 0; ft < NF; ++ft)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        T4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (T)(acc[ft][4 * b + e] * inv);
+        const int at16 = (32 * ft + 8 * b + 4 * half) * ESZ;
+        *(GPTQ_LDS T4*)(area + col * ROWB + (((at16 >> 4) ^ swz_k<UN>(col)) << 4) + (at16 & 15)) = o;
+      }
+    __builtin_amdgcn_wave_barrier();
+    const int64_t to = live && !((redo >> col) & 1) ? (sq.q0 + qi) * a.o_ld + h * a.o_hp : -1;
+#pragma unroll
+    for (int i = 0; i < UN / 2; ++i) {
+      const int unit = 64 * i + lane, row = unit / UN, u = (unit - row * UN) ^ swz_k<UN>(row);
+      const int64_t row_to = __shfl(to, row, 64);
+      const Unit v = *(GPTQ_LDS Unit*)(area + 1024 * i + 16 * lane);
+      if (row_to >= 0 && u * EPU < a.dh)
+        *reinterpret_cast<Unit*>(static_cast<E*>(a.out) + row_to + u * EPU) = v;
+    }
+  } else {
   const float mexp = m == -INFINITY ? -INFINITY : m * c + (MODE == 1 ? a.cap * kLog2e : 0.f) - kShift;
   if (live && !((redo >> col) & 1)) {
     const int64_t row = sq.q0 + qi;
@@ -880,6 +942,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
           }
         }
     }
+  }
   }
   while (redo) {
     const int rr = __builtin_ctz(redo);
@@ -1067,7 +1130,9 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
     return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % unit == 0 && hp % unit == 0;
   };
   const bool dma = a.dh % unit == 0 && al(q, a.q_ld, a.q_hp) && al(k, a.k_ld, a.k_hp) && al(v, a.v_ld, a.v_hp) &&
-                   std::max(a.k_ld, a.v_ld) < ((int64_t)1 << 23);
+                   std::max(a.k_ld, a.v_ld) < ((int64_t)1 << 23) &&
+                   (128 / a.group + 2) * a.q_ld + a.group * a.q_hp < ((int64_t)1 << 28);
+  a.o_rows = reinterpret_cast<uintptr_t>(out) % 16 == 0 && a.o_ld % unit == 0 && a.o_hp % unit == 0;
   a.o_vec = reinterpret_cast<uintptr_t>(out) % (t.dtype == F32 ? 16 : 8) == 0 && a.o_ld % 4 == 0 && a.o_hp % 4 == 0;
   hipError_t e = t.dtype == F32   ? by_head<F32>(a, dma, p.few, s)
                  : t.dtype == F16 ? by_head<F16>(a, dma, p.few, s)
