@@ -397,8 +397,8 @@ typedef struct {
   int64_t seqs;       /* sequences, >= 0 (0: nothing is queued)                                   */
   int64_t n_q, n_kv;  /* rows of q and out, rows of k and v; 0..2^30                              */
   int64_t q_ld, q_hp, k_ld, k_hp, v_ld, v_hp, out_ld, out_hp;
-  double scale;       /* score scale, finite (1 / sqrt(head_dim) as a rule)                       */
-  double softcap;     /* c > 0: scores become c tanh(score / c); 0: no cap                        */
+  double scale;       /* score scale, finite in fp32 (1 / sqrt(head_dim) as a rule)               */
+  double softcap;     /* c >= 1e-37: scores become c tanh(score / c); 0: no cap                   */
   int32_t dtype;      /* of q, k, v and out: GPTQ_F32, GPTQ_F16 or GPTQ_BF16                      */
   int32_t q_heads;    /* 1..65535                                                                 */
   int32_t kv_heads;   /* 1..65535, dividing q_heads: query head h reads head h / (q_heads / kv_heads) */

@@ -322,7 +322,9 @@ bool attention_ok(const gptq_attention_t* a) {
       a->q_heads % a->kv_heads != 0 || a->head_dim < 1 || a->head_dim > 1024)
     return false;
   if (a->causal != 0 && a->causal != 1) return false;
-  return std::isfinite(a->scale) && std::isfinite(a->softcap) && a->softcap >= 0.0;
+  // both as fp32: finite, and a cap not lost to zero
+  const float scale = (float)a->scale, cap = (float)a->softcap;
+  return std::isfinite(scale) && std::isfinite(cap) && a->softcap >= 0.0 && (a->softcap == 0.0 || cap >= 1e-37f);
 }
 
 }  // namespace

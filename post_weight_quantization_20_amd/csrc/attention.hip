@@ -353,9 +353,12 @@ GPTQ_DEV TileAt find_tile(const AttnArgs& a, int64_t t, int rows, int lane) {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kShift = 7.0f, kRaise = 8.0f;
+// Caps up to this are formed from 1 / (e^2y + 1), whose 2^-24 the cap multiplies: at most 6e-5 of a score,
+// under an eighth of fp16's half step once it weighs a key. Larger ones take tanhf.
+constexpr float kSmallCap = 256.0f;
 
 // DHP: head width padded to 32. DMA: 16-byte aligned tensors. MODE 0: scores only scaled, 1: capped, 2: any
-// (a bias, both, scaled by zero; caps in fp32).
+// (a bias, both, scaled by zero; caps in fp32 and large ones).
 template <int DT, int DHP, int WM, bool DMA, int MODE>
 __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(AttnArgs a) {
   typedef typename ElemOf<DT>::T T;
@@ -473,7 +476,8 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
   float slope = 0.f;
   if (MODE == 2 && a.slopes) slope = a.slopes[h];
 
-  // Where masking starts and ends for the wave. Limits rise with the row (padding aside, which sees nothing): the first row's and the last one's
+  // Where masking starts and ends for the wave. Limits rise with the row (padding aside, which sees
+  // nothing): the first row's and the last one's.
   const uint32_t seeing = (uint32_t)__ballot(live && qdoc >= 0);
   const bool all_see = seeing == (uint32_t)__ballot(live);
   const int32_t wmin = seeing && all_see ? lane_value(lim, 0) : 0;
@@ -643,7 +647,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if constexpr (DT == F32)
+            if (DT == F32 || a.cap > kSmallCap)
               S[t][i] = a.cap * tanhf(S[t][i] * inv_cap);
             else   // tanh y = 1 - 2 / (e^2y + 1)
               S[t][i] = a.cap - 2.0f * a.cap * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(S[t][i] * to_cap) + 1.0f);
@@ -872,7 +876,6 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
     const uint64_t o = __ballot(odd && live);
     redo = (uint32_t)o | (uint32_t)(o >> 32);
   }
-  // O and l are in units of 2^mexp
   if (WM == 4 && DMA && a.nsplit == 1 && a.o_rows) {
     // Rows leave through LDS, 16 bytes a lane along each (a lane's own pieces are 8 bytes of every 16): the
     // tiles' area is free when every wave is here.
@@ -900,11 +903,11 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
       if (row_to >= 0 && u * EPU < a.dh)
         *reinterpret_cast<Unit*>(static_cast<E*>(a.out) + row_to + u * EPU) = v;
     }
-  } else {
-  const float mexp = m == -INFINITY ? -INFINITY : m * c + (MODE == 1 ? a.cap * kLog2e : 0.f) - kShift;
-  if (live && !((redo >> col) & 1)) {
+  } else if (live && !((redo >> col) & 1)) {
     const int64_t row = sq.q0 + qi;
     if (a.nsplit > 1) {
+      // O and l are in units of 2^mexp
+      const float mexp = m == -INFINITY ? -INFINITY : m * c + (MODE == 1 ? a.cap * kLog2e : 0.f) - kShift;
       const int64_t pr = ((int64_t)z * a.nq + row) * a.hq + h;
       if (half == 0) {
         a.part_ml[2 * pr] = mexp;
@@ -942,7 +945,6 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
           }
         }
     }
-  }
   }
   while (redo) {
     const int rr = __builtin_ctz(redo);
@@ -1038,13 +1040,14 @@ hipError_t by_mode(const AttnArgs& a, bool dma, hipStream_t s) {
   if (!dma) return launch_mfma<DT, DHP, WM, false, 2>(a, s);
   if (a.slopes || a.scale == 0.f) return launch_mfma<DT, DHP, WM, true, 2>(a, s);
   if (a.cap == 0.f) return launch_mfma<DT, DHP, WM, true, 0>(a, s);
-  if constexpr (DT == F32) return launch_mfma<DT, DHP, WM, true, 2>(a, s);
-  else return launch_mfma<DT, DHP, WM, true, 1>(a, s);
+  if constexpr (DT != F32)
+    if (a.cap <= kSmallCap) return launch_mfma<DT, DHP, WM, true, 1>(a, s);
+  return launch_mfma<DT, DHP, WM, true, 2>(a, s);
 }
 
 template <int DT>
 hipError_t by_head(const AttnArgs& a, bool dma, bool few, hipStream_t s) {
-  // few rows: each wave needs its own double buffer, which 160 KB of LDS holds up to 128-wide heads
+  // few rows: each wave needs a buffer of its own, which 160 KB of LDS holds up to 128-wide heads
   if (few) {
     if (a.dh <= 64) return by_mode<DT, 64, 1>(a, dma, s);
     if (a.dh <= 96) return by_mode<DT, 96, 1>(a, dma, s);

@@ -82,6 +82,7 @@ def _attention(over=None, work_bytes=0, **kw):
     dict(seqs=-1), dict(seqs=1 << 31), dict(n_q=-1), dict(n_q=1 << 31), dict(n_kv=-1), dict(dtype=9), dict(q_heads=0),
     dict(kv_heads=0), dict(kv_heads=3), dict(kv_heads=8), dict(head_dim=0), dict(head_dim=1025), dict(causal=2),
     dict(scale=float("inf")), dict(scale=float("nan")), dict(softcap=-1.0), dict(softcap=float("nan")),
+    dict(scale=1e300), dict(softcap=1e300), dict(softcap=1e-300), dict(n_q=(1 << 30) + 2), dict(n_kv=(1 << 30) + 2),
     dict(q_ld=-1), dict(v_hp=-1), dict(k_ld=1 << 60), dict(out_hp=15), dict(out_ld=32),
     dict(seqs=3),                  # equal ranges need a multiple
     dict(n_kv=9),

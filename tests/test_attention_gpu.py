@@ -229,6 +229,8 @@ def test_attention_shared_heads(hq, hk, dtype):
     dict(bias=True, causal=False), dict(docs=3), dict(docs=-3), dict(docs=-3, causal=False),
     dict(docs=4, softcap=5.0, bias=True), dict(prefix=[0, 150, 20]), dict(prefix=[9, 500, -4], bias=True),
     dict(prefix=[5, 5, 5], docs=2, softcap=1.0), dict(prefix=[5, 5, 5], causal=False), dict(scale=-0.3),
+    dict(softcap=256.0), dict(softcap=5000.0), dict(softcap=1e7, bias=True), dict(softcap=1e-6),
+    dict(scale=-0.3, softcap=3.0), dict(scale=-0.3, bias=True), dict(docs=70), dict(docs=-70, causal=False),
 ], ids=str)
 def test_attention_masks(kw, dtype):
     _run_attention(dtype, 4, 2, 64, [(9, 9), (200, 200), (66, 140)], **kw)
@@ -241,6 +243,63 @@ def test_attention_long_caches(work, dtype):
     _run_attention(dtype, 8, 2, 128, [(1, 9001), (2, 700), (1, 1), (5, 4097)], work=work)
     _run_attention(dtype, 4, 4, 80, [(1, 5000)], docs=9, softcap=20.0, work=work)
     _run_attention(dtype, 2, 1, 64, [(3, 3000), (1, 0)], bias=True, causal=False, work=work)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_attention_documents_over_many_blocks(dtype):
+    """Keys beyond one scan of 64 tiles, documents that skip whole scans, recur and end inside tiles."""
+    n = 9300
+    r = np.random.default_rng(2)
+    torch = torch_cuda()
+    h, dh = 1, 32
+    q, k, v = (_rand((n, h, dh), s, dtype) for s in (1, 2, 3))
+    doc = np.repeat(np.arange(6), [3000, 70, 1, 4300, 1500, 429])
+    doc[100:130] = 4                 # an early piece of a late document
+    doc[8000:8040] = -1
+    d = _ints(doc)
+    rows = np.unique(np.concatenate([r.integers(0, n, 60), [0, 99, 100, 129, 130, 2999, 3000, 3070, 3071, 7999, 8000,
+                                                            8039, 8040, 8870, 9299]]))
+    out = _g().gptq_attention(q, k, v, q_doc=d, kv_doc=d)
+    torch.cuda.synchronize()
+    got = _np(out)[rows]
+    # the same rows one by one: a sequence of the first i + 1 keys, whose last token is the row
+    want, mag, spread = attn_ref.attention(np.repeat(_np(q)[rows], 1, 0), np.concatenate([_np(k)[:i + 1] for i in rows]),
+                                           np.concatenate([_np(v)[:i + 1] for i in rows]),
+                                           [(j, j + 1, *(int(x) for x in e)) for j, e in enumerate(
+                                               zip(_starts(rows + 1)[:-1], _starts(rows + 1)[1:]))],
+                                           dh ** -0.5, q_doc=doc[rows], kv_doc=np.concatenate([doc[:i + 1] for i in rows]))
+    p_step = 0.0 if dtype == "f32" else _half_step(dtype)
+    bound = _half_step(dtype) * np.abs(want) + (p_step + (2 * (dh + 8) * spread + 64) * U) * mag + 2.0 ** -25
+    assert np.all(np.abs(got - want) <= bound)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_attention_nan_everywhere(dh, dtype):
+    """All-NaN keys or values give NaN in every row that sees one, zeros in rows that see none."""
+    torch = torch_cuda()
+    n = 70
+    q, k, v = (_rand((n, 2, dh), s, dtype) for s in (1, 2, 3))
+    doc = np.zeros(n, dtype=np.int32)
+    doc[:5] = -1
+    for bad in (k, v):
+        kk, vv = (torch.full_like(t, float("nan")) if t is bad else t for t in (k, v))
+        o = _g().gptq_attention(q, kk, vv, q_doc=_ints(doc), kv_doc=_ints(doc))
+        torch.cuda.synchronize()
+        assert torch.all(o[:5] == 0) and torch.isnan(o[5:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_attention_infinite_scores_in_split_ranges(dtype):
+    """An infinity in one value that a long range sees shows in its column alone, split or not."""
+    torch = torch_cuda()
+    q, k, v = _rand((1, 2, 64), 1, dtype), _rand((6000, 1, 64), 2, dtype), _rand((6000, 1, 64), 3, dtype)
+    v[4000, 0, 9] = float("inf")
+    for work in (None, torch.empty(0, dtype=torch.uint8, device="cuda:0")):
+        o = _g().gptq_attention(q, k, v, work=work)
+        torch.cuda.synchronize()
+        bad = ~torch.isfinite(o)
+        assert torch.all(o[:, :, 9] == float("inf")) and bad.sum() == 2
 
 
 @pytest.mark.parametrize("dtype", DT)
@@ -430,6 +489,20 @@ def test_lora_views_in_place_and_unused_places(dtype):
     assert torch.equal(wide[:, :2], kept[:, :2]) and torch.equal(wide[:, 2 + rows:], kept[:, 2 + rows:])
 
 
+def test_lora_nan_stays_with_its_rows():
+    """NaN in one row of x, or in one adapter, reaches the rows that name it and no others, in mixed tiles."""
+    torch = torch_cuda()
+    for m in (20, 600):
+        x, A, B = _rand((m, 64), 1, "bf16"), _rand((3, 16, 64), 2, "bf16"), _rand((3, 40, 16), 3, "bf16")
+        x[7], A[2] = float("nan"), float("nan")
+        idx = np.arange(m) % 4 - 1
+        idx[7] = 0
+        y = _g().gptq_lora_gemm(x, A, B, _ints(idx))
+        torch.cuda.synchronize()
+        bad = torch.isnan(y).any(1).cpu().numpy()
+        assert np.array_equal(bad, (idx == 2) | (np.arange(m) == 7))
+
+
 def test_lora_without_adapters_copies_the_base():
     torch = torch_cuda()
     x, base = _rand((5, 16), 1, "f16"), _rand((5, 24), 2, "f32")
@@ -488,6 +561,47 @@ def test_captured_graph_replays(n):
         _three(s)
         torch.cuda.synchronize()
         assert torch.equal(got, s["y"]) and torch.equal(o, s["o"])
+
+
+def test_first_call_inside_a_capture():
+    """A head width and type that no call has used yet, captured at once."""
+    torch = torch_cuda()
+    q, k, v = (_rand((300, 4, 176), s, "bf16") for s in (1, 2, 3))
+    slopes = torch.tensor([0.5, 0.25, 0.1, 0.05], device="cuda:0")
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _g().gptq_attention(q, k, v, slopes=slopes, softcap=4.0, out=out)
+    for r in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, _g().gptq_attention(q, k, v, slopes=slopes, softcap=4.0))
+        torch.cuda.synchronize()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams with workspaces of their own give what each gives alone."""
+    torch = torch_cuda()
+    a, b = _state(n=300), _state("bf16", n=2)
+    want = []
+    for s in (a, b):
+        _three(s)
+        torch.cuda.synchronize()
+        want.append((s["o"].clone(), s["y"].clone()))
+        s["o"].zero_()
+        s["y"].zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for s, st in zip((a, b), streams):
+            s["stream"] = st
+            _three(s)
+    torch.cuda.synchronize()
+    for s, (o, y) in zip((a, b), want):
+        assert torch.equal(s["o"], o) and torch.equal(s["y"], y)
 
 
 def test_named_stream_matches_the_current_one():
