@@ -16,10 +16,15 @@
 // of a workgroup (joined in LDS in wave order) and, while there are few workgroups, over the grid; expand
 // adds the grid's partial sums in order. expand: fp32 MFMA, so T is never rounded to 16 bits: with r <= 256
 // the product is small beside y's bytes. Nothing depends on scheduling.
+//
+// Measured: 4096 bf16 rows of rank 64, 4096 x 11008, in 59 (shrink) + 50 us (expand), against 48 for the
+// bytes: A, T and B come from L2 once per tile. 64 rows over 48 adapters of rank 16, 11008 x 4096, 5 + 16 us;
+// 4 rows on 4 adapters, 4096 x 4096, 4 + 4 us.
 #include "common.hpp"
 
 namespace gptq {
 namespace {
+
 constexpr int EW = 4;   // waves of an expand workgroup
 
 typedef short v8s __attribute__((ext_vector_type(8)));
