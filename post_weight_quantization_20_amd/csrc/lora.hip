@@ -18,7 +18,7 @@
 // the product is small beside y's bytes. Nothing depends on scheduling.
 //
 // Measured: 4096 bf16 rows of rank 64, 4096 x 11008, in 59 (shrink) + 50 us (expand), against 48 for the
-// bytes: A, T and B come from L2 once per tile. 64 rows over 48 adapters of rank 16, 11008 x 4096, 5 + 16 us;
+// bytes: A, T and B come from L2 once per tile. 64 rows over 48 adapters of rank 16, 11008 x 4096, 5 + 13 us;
 // 4 rows on 4 adapters, 4096 x 4096, 4 + 4 us.
 #include "common.hpp"
 
@@ -208,27 +208,32 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
   });
 }
 
-// N consecutive elements of a row of B as floats, zeros from column r on.
+// N consecutive elements of a row of B, zeros from column r on.
 template <int DT, int N>
-GPTQ_DEV void load_b(const void* B, int64_t at, int k, int r, bool vec, float (&v)[N]) {
+using Piece = typename ElemOf<DT>::T __attribute__((ext_vector_type(N)));
+
+template <int DT, int N>
+GPTQ_DEV Piece<DT, N> load_b(const void* B, int64_t at, int k, int r, bool vec) {
   typedef typename ElemOf<DT>::T T;
   const T* p = static_cast<const T*>(B) + at + k;
+  Piece<DT, N> v = {};
   if (vec && k + N <= r) {
-    typedef T V __attribute__((ext_vector_type(N)));
-    const V u = *reinterpret_cast<const V*>(p);
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = (float)u[e];
+    v = *reinterpret_cast<const Piece<DT, N>*>(p);
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = k + e < r ? (float)p[e] : 0.f;
+    for (int e = 0; e < N; ++e)
+      if (k + e < r) v[e] = p[e];
   }
+  return v;
 }
 
 // y of 16 MT rows. SLOTS: the four waves share 16 NJ columns and take the tile's slots in turn (each row is
 // written by the wave of its slot); otherwise each wave takes 16 NJ columns of its own and every slot. The
 // MFMA's lane l holds B row (column of y) l % 16 and T row l % 16 at ranks 4 (l / 16) .. + 3, and gets four
-// consecutive columns of y of row l % 16.
-template <int DT, int MT, int NJ, int KN, bool SLOTS>
+// consecutive columns of y of row l % 16. AHEAD (SLOTS, B's rows one piece a lane, as ranks up to 16 or 32 are):
+// B of all the wave's slots is loaded while T is formed, so that the slots' latencies are paid once (64 requests
+// over 48 adapters of rank 16: 13.5 against 16 us).
+template <int DT, int MT, int NJ, int KN, bool SLOTS, bool AHEAD>
 __global__ __launch_bounds__(64 * EW) void expand_kernel(LoraArgs a) {
   extern __shared__ __align__(16) float ts[];   // [16 MT][rp + 4]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -266,6 +271,33 @@ __global__ __launch_bounds__(64 * EW) void expand_kernel(LoraArgs a) {
         }
       }
     }
+  }
+  // AHEAD: B of all the wave's slots is on its way too
+  constexpr int MINE = AHEAD ? 16 * MT / EW : 1;   // slots of a wave at most
+  int own[MINE];
+  uint64_t own_rows[MINE];
+  Piece<DT, KN> ahead_b[MINE][NJ];
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int q = 0; q < MINE; ++q) own[q] = -1;
+    each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
+#pragma unroll
+      for (int q = 0; q < MINE; ++q)
+        if (slot == EW * q + wave) {
+          own[q] = adapter;
+          own_rows[q] = mine;
+        }
+    });
+#pragma unroll
+    for (int q = 0; q < MINE; ++q)
+      if (own[q] >= 0) {
+        const int r = rank_of(a, own[q]);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int64_t jr = min(j0 + 16 * j + l16, a.rows - 1);
+          ahead_b[q][j] = load_b<DT, KN>(a.B, ((int64_t)own[q] * a.rows + jr) * a.rank, KN * quarter, r, a.bvec);
+        }
+      }
   }
   // T of the tile's rows, the ranges of d added in order, four ranks a thread and eight ranges at a time;
   // rows without an adapter (whose T is not written) are zero
@@ -306,7 +338,24 @@ __global__ __launch_bounds__(64 * EW) void expand_kernel(LoraArgs a) {
     }
   };
 
-  each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
+  if constexpr (AHEAD) {
+    floatx4 t4[KN / 4];
+#pragma unroll
+    for (int c = 0; c < KN / 4; ++c) t4[c] = *reinterpret_cast<const floatx4*>(ts + l16 * pitch + KN * quarter + 4 * c);
+#pragma unroll
+    for (int q = 0; q < MINE; ++q)
+      if (own[q] >= 0) {
+        const float scale = rank_of(a, own[q]) == 0 ? 0.f : a.scales ? a.scales[own[q]] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          floatx4 s = zero;
+#pragma unroll
+          for (int e = 0; e < KN; ++e)
+            s = __builtin_amdgcn_mfma_f32_16x16x4f32((float)ahead_b[q][j][e], t4[e / 4][e % 4], s, 0, 0, 0);
+          if ((own_rows[q] >> l16) & 1) store(0, j, s, scale, i0 + l16);
+        }
+      }
+  } else each_slot(ad, [&](int slot, int adapter, uint64_t mine) {
     if (SLOTS && slot % EW != wave) return;
     const int r = rank_of(a, adapter);
     const float scale = a.scales ? a.scales[adapter] : 1.0f;
@@ -317,12 +366,12 @@ __global__ __launch_bounds__(64 * EW) void expand_kernel(LoraArgs a) {
       for (int j = 0; j < NJ; ++j) acc[t][j] = zero;
     for (int k0 = 0; k0 < r; k0 += 4 * KN) {
       const int k = k0 + KN * quarter;
-      float b[NJ][KN];
+      Piece<DT, KN> b[NJ];
       floatx4 t4[MT][KN / 4];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int64_t jr = min(j0 + 16 * j + l16, a.rows - 1);
-        load_b<DT, KN>(a.B, ((int64_t)adapter * a.rows + jr) * a.rank, k, r, a.bvec, b[j]);
+        b[j] = load_b<DT, KN>(a.B, ((int64_t)adapter * a.rows + jr) * a.rank, k, r, a.bvec);
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -335,7 +384,7 @@ __global__ __launch_bounds__(64 * EW) void expand_kernel(LoraArgs a) {
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
-            acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j][e], t4[t][e / 4][e % 4], acc[t][j], 0, 0, 0);
+            acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x4f32((float)b[j][e], t4[t][e / 4][e % 4], acc[t][j], 0, 0, 0);
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -399,7 +448,7 @@ hipError_t shrink(const LoraArgs& a, const Plan& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int DT, int MT, int NJ, int KN, bool SLOTS>
+template <int DT, int MT, int NJ, int KN, bool SLOTS, bool AHEAD>
 hipError_t launch_expand_k(const LoraArgs& a, hipStream_t s) {
   const int64_t cols = (SLOTS ? 1 : EW) * 16 * NJ;
   const size_t lds = (size_t)16 * MT * (a.rp + 4) * sizeof(float);
@@ -409,7 +458,7 @@ hipError_t launch_expand_k(const LoraArgs& a, hipStream_t s) {
   for (int64_t t0 = 0; t0 < tiles; t0 += step) {
     LoraArgs b = a;
     b.tile0 = t0;
-    hipLaunchKernelGGL((expand_kernel<DT, MT, NJ, KN, SLOTS>), dim3((unsigned)xs, (unsigned)std::min(step, tiles - t0)),
+    hipLaunchKernelGGL((expand_kernel<DT, MT, NJ, KN, SLOTS, AHEAD>), dim3((unsigned)xs, (unsigned)std::min(step, tiles - t0)),
                        dim3(64 * EW), lds, s, b);
   }
   return hipGetLastError();
@@ -418,9 +467,15 @@ hipError_t launch_expand_k(const LoraArgs& a, hipStream_t s) {
 template <int DT, int MT, int NJ, bool SLOTS>
 hipError_t launch_expand(const LoraArgs& a, hipStream_t s) {
   // B's rows 16 bytes a lane at a time where the padded rank is whole pieces of four lanes
+  if constexpr (SLOTS) {
+    // one piece a lane is the whole rank: a wave's slots are loaded at once
+    if (a.rp == 16) return launch_expand_k<DT, MT, NJ, 4, true, true>(a, s);
+    if constexpr (DT != F32)
+      if (a.rp == 32) return launch_expand_k<DT, MT, NJ, 8, true, true>(a, s);
+  }
   if constexpr (DT != F32)
-    if (a.rp % 32 == 0) return launch_expand_k<DT, MT, NJ, 8, SLOTS>(a, s);
-  return launch_expand_k<DT, MT, NJ, 4, SLOTS>(a, s);
+    if (a.rp % 32 == 0) return launch_expand_k<DT, MT, NJ, 8, SLOTS, false>(a, s);
+  return launch_expand_k<DT, MT, NJ, 4, SLOTS, false>(a, s);
 }
 
 template <int DT>
