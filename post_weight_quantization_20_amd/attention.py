@@ -184,7 +184,8 @@ def gptq_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Opt
     sequence after sequence: rows q_start[s] .. q_start[s + 1] of q and kv_start[s] .. of k and v (int32
     [seqs + 1]; without them, `seqs` equal ranges). The queries are each sequence's last tokens. softcap,
     slopes (float32 [heads]), q_doc and kv_doc (int32 per token) and prefix (int32 per sequence) as in
-    gptq.h; scale is 1 / sqrt(head_dim) unless given. work: uint8, gptq_attention_workspace_bytes."""
+    gptq.h; scale is 1 / sqrt(head_dim) unless given. work: uint8, gptq_attention_workspace_bytes. Rows of
+    out that belong to no sequence are left as they were (undefined in an out made here)."""
     dev = _device(q, k=k, v=v, q_start=q_start, kv_start=kv_start, slopes=slopes, q_doc=q_doc, kv_doc=kv_doc,
                   prefix=prefix, out=out, work=work)
     for name, t in (("q_start", q_start), ("kv_start", kv_start)):

@@ -307,6 +307,8 @@ def test_attention_many_sequences(dtype):
     r = np.random.default_rng(3)
     lens = [(int(a), int(a)) for a in r.integers(0, 12, 300)]
     _run_attention(dtype, 2, 2, 32, lens)
+    lens = [(int(a), int(a + b)) for a, b in zip(r.integers(0, 60, 150), r.integers(0, 40, 150))]
+    _run_attention(dtype, 4, 1, 32, lens, docs=5, prefix=[3] * 150)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -417,6 +419,37 @@ def test_attention_equal_ranges_without_offsets():
     assert torch.equal(a, b)
 
 
+def test_attention_offsets_past_32_bits():
+    """A cache of more than 2^31 elements: queries that match one key each get its value."""
+    torch = torch_cuda()
+    n, hk, dh = 2_200_003, 8, 128
+    gen = torch.Generator(device="cuda:0")
+    gen.manual_seed(1)
+    k = torch.randn(n, hk, dh, generator=gen, device="cuda:0", dtype=torch.bfloat16)
+    v = torch.randn(n, hk, dh, generator=gen, device="cuda:0", dtype=torch.bfloat16)
+    at = [10, 2 ** 31 // (hk * dh) + 3, n - 1]
+    q = k[at].repeat_interleave(2, 1).contiguous() * 4
+    for work in (None, torch.empty(0, dtype=torch.uint8, device="cuda:0")):
+        o = _g().gptq_attention(q, k, v, causal=False, work=work)
+        torch.cuda.synchronize()
+        # each match's score is 4 |k|^2 / sqrt(dh), about 45, against about 4 for the others: e^-41 times their number
+        assert torch.all((o - v[at].repeat_interleave(2, 1)).abs().float() <= 2 ** -6 * (1 + o.abs().float()))
+
+
+def test_norm_rotate_large_sizes():
+    """More than 2^31 elements, and more tokens than one launch takes: rows equal those of small calls."""
+    torch = torch_cuda()
+    f = torch.rand(32, device="cuda:0")
+    for n, h, dh in ((270_001, 64, 128), ((1 << 22) + 77, 1, 64)):
+        q = torch.empty(n, h, dh, dtype=torch.bfloat16, device="cuda:0").uniform_(-1, 1)
+        pos = torch.arange(n, dtype=torch.int32, device="cuda:0")
+        o, _ = _g().gptq_norm_rotate(q, None, pos, f)
+        for a in (0, n // 2, min(n, 1 << 22) - 9, n - 40):
+            p, _ = _g().gptq_norm_rotate(q[a:a + 40], None, pos[a:a + 40].contiguous(), f)
+            torch.cuda.synchronize()
+            assert torch.equal(o[a:a + 40], p)
+
+
 # -------------------------------------------------------------------------------------------- lora
 
 LORA = [  # m, d, rows, adapters, rank
@@ -501,6 +534,21 @@ def test_lora_nan_stays_with_its_rows():
         torch.cuda.synchronize()
         bad = torch.isnan(y).any(1).cpu().numpy()
         assert np.array_equal(bad, (idx == 2) | (np.arange(m) == 7))
+
+
+def test_lora_more_rows_than_one_piece():
+    """Rows beyond 2^19 go in pieces that share the workspace: they equal a small call's."""
+    torch = torch_cuda()
+    m, d, rows, na, r = (1 << 19) + 300, 16, 24, 3, 4
+    rr = np.random.default_rng(1)
+    to = lambda *s: torch.from_numpy(rr.integers(-2, 3, s).astype(np.float32)).half().cuda()   # noqa: E731
+    x, A, B = to(m, d), to(na, r, d), to(na, rows, r)
+    idx = _ints(rr.integers(-1, na, m))
+    y = _g().gptq_lora_gemm(x, A, B, idx)
+    for a in (0, (1 << 19) - 30, m - 60):
+        p = _g().gptq_lora_gemm(x[a:a + 60], A, B, idx[a:a + 60].contiguous())
+        torch.cuda.synchronize()
+        assert torch.equal(y[a:a + 60], p)
 
 
 def test_lora_without_adapters_copies_the_base():
