@@ -432,7 +432,7 @@ typedef struct {
  *                  when there are few queries and joined in key order; with less (or NULL) they are not.
  *                  It must not be shared with a concurrent call, two captured graphs included.
  * Scores, the softmax's maximum and sum and the output are fp32. Results do not depend on scheduling.
- * Returns GPTQ_EUNSUPPORTED for more than 2^24 tiles of 32 queries (times the shared heads' group).
+ * Returns GPTQ_EUNSUPPORTED for 2^24 or more tiles of 128 queries (times the shared heads' group).
  */
 gptq_status_t gptq_attention(const gptq_attention_t *a, const void *q, const void *k, const void *v,
                              const int32_t *q_start, const int32_t *kv_start, const float *slopes,

@@ -16,6 +16,7 @@ namespace gptq {
 namespace {
 
 constexpr int kMaxHead = 1024;
+constexpr int64_t kRows = 128;   // packed rows of a tile
 
 struct AttnArgs {
   const void *q, *k, *v;
@@ -210,8 +211,8 @@ __global__ __launch_bounds__(256) void attn_row_kernel(AttnArgs a) {
 // (four rows of two units) fall in distinct banks. Units beyond the head or the keys read as zero through
 // the descriptor's range. Tensors that are not 16-byte aligned are staged through registers instead.
 //
-// WM = 4: the four waves hold 128 rows and share tiles of 64 keys. WM = 1: up to 32 rows (few queries),
-// each wave takes its own tiles of 32 keys and the four partial results are joined in LDS.
+// The four waves of a workgroup hold 128 rows and share tiles of 64 keys (fp32: 32). With few queries only the
+// first waves have rows to work for, which reading the keys leaves them time to do.
 //
 // The maximum is raised only when a score exceeds it by 8 (in powers of two); probabilities are kept 2^7
 // larger, so they stay below 2^15 and small ones keep their bits in fp16. A masked key's probability is
@@ -243,17 +244,13 @@ GPTQ_DEV i32x4 descriptor(uint64_t base, int64_t bytes) {
   return i32x4{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
-// Keys of a tile and buffers, within 160 KB of LDS: two workgroups a CU up to 128-wide heads (16-bit types).
-// WM = 1 waves have one buffer each: a wave's wait is covered by the seven others of its CU, and two
-// workgroups a CU with one buffer beat one with two (16 tokens against 4915 keys each, 32 / 8 heads of 128:
-// 67 against 71 us, one token against 16384: 21 against 28).
-template <int DT, int DHP, int WM>
+// Keys of a tile, double-buffered within 160 KB of LDS: two workgroups a CU up to 128-wide heads.
+template <int DT, int DHP>
 struct Tile {
   static constexpr int ESZ = DT == F32 ? 4 : 2;
-  static constexpr int KT = WM == 4 && DT != F32 ? 64 : 32;
+  static constexpr int KT = DT == F32 ? 32 : 64;
   static constexpr int TILEB = KT * DHP * ESZ;
-  static constexpr int NB = WM == 1 ? 1 : 2;
-  static constexpr int LDS = NB * 2 * TILEB * (4 / WM) + 2048 + 128;
+  static constexpr int LDS = 2 * 2 * TILEB + 2048 + 128;
 };
 
 template <int DT>
@@ -310,7 +307,7 @@ struct TileAt {
 
 GPTQ_DEV int32_t lane_value(int32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-GPTQ_DEV TileAt find_tile(const AttnArgs& a, int64_t t, int rows, int lane) {
+GPTQ_DEV TileAt find_tile(const AttnArgs& a, int64_t t, int lane) {
   TileAt r{-1, 0, {}, 0};
   if (!a.q_start) {
     const uint32_t per = a.seq_tiles, u = (uint32_t)t;   // a grid holds fewer than 2^24 tiles
@@ -332,7 +329,7 @@ GPTQ_DEV TileAt find_tile(const AttnArgs& a, int64_t t, int rows, int lane) {
       q = sequence(a, s);
       if (a.prefix) pre = a.prefix[s];
       // at most 2^30 rows of q: a sequence with more tiles than a grid has is never reached
-      n = (int32_t)min((q.lq * a.group + rows - 1) >> (rows == 32 ? 5 : 7), (int64_t)1 << 24);
+      n = (int32_t)min((q.lq * a.group + kRows - 1) / kRows, (int64_t)1 << 24);
     }
     int32_t sum = n;   // inclusive prefix sum over the lanes
 #pragma unroll
@@ -363,32 +360,32 @@ constexpr float kSmallCap = 256.0f;
 
 // DHP: head width padded to 32. DMA: 16-byte aligned tensors. MODE 0: scores only scaled, 1: capped, 2: any
 // (a bias, both, scaled by zero; caps in fp32 and large ones).
-template <int DT, int DHP, int WM, bool DMA, int MODE>
+template <int DT, int DHP, bool DMA, int MODE>
 __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(AttnArgs a) {
   typedef typename ElemOf<DT>::T T;
-  typedef Tile<DT, DHP, WM> C;
-  constexpr int KT = C::KT, NB = C::NB;         // keys of a tile, buffers
+  typedef Tile<DT, DHP> C;
+  constexpr int KT = C::KT;                     // keys of a tile
   constexpr int NT = KT / 32, NF = DHP / 32;
   constexpr int ESZ = C::ESZ, EPU = 16 / ESZ;   // elements of a 16-byte unit
   constexpr int NK = DHP / (2 * EPU);           // unit pairs of a row: one unit of a pair to each half wave
   constexpr int UN = DHP / EPU;                 // units of a row
   constexpr int ROWB = DHP * ESZ, TILEB = C::TILEB, BUFB = 2 * TILEB;
-  constexpr int LOADS = KT * UN / 64 / WM;      // units a lane stages of K (and of V)
-  constexpr int ROWS = 32 * WM;
+  constexpr int LOADS = KT * UN / 256;          // units a lane stages of K (and of V)
+  constexpr int ROWS = (int)kRows;
   typedef typename std::conditional<DT == F32, floatx4, v8s>::type Unit;
   extern __shared__ char smem_raw[];
   GPTQ_LDS char* smem = (GPTQ_LDS char*)smem_raw;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   // small LDS area behind the tiles: documents of a tile per wave, what the tiles of a block hold
-  GPTQ_LDS char* tail = smem + NB * BUFB * (4 / WM);
+  GPTQ_LDS char* tail = smem + 2 * BUFB;
   GPTQ_LDS int32_t* docs = (GPTQ_LDS int32_t*)tail + 128 * wave;   // two tiles' worth
 
   // the workgroup's key head, tile of rows and range of keys
   uint32_t kvh, rem;
   if (a.hk % 8 == 0) {
     // Workgroups go to the 8 XCDs in turn: each takes an eighth of the heads, which its L2 keeps, tile by
-    // tile (head by head, an XCD's last head would run alone: 4 x 2048 fp32 tokens took a fifth longer).
+    // tile (head by head, an XCD's last head would run alone: 4 x 2048 fp32 tokens took a quarter longer).
     const uint32_t mine = (uint32_t)a.hk >> 3, at = blockIdx.x >> 3;
     rem = at / mine;
     kvh = (blockIdx.x & 7) * mine + (at - rem * mine);
@@ -398,13 +395,13 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
   }
   const uint32_t tord = rem / (uint32_t)a.nsplit;
   const int z = (int)(rem - tord * a.nsplit);
-  const TileAt at = find_tile(a, a.tiles - 1 - tord, ROWS, lane);   // long (late) tiles first
+  const TileAt at = find_tile(a, a.tiles - 1 - tord, lane);   // long (late) tiles first
   if (at.seq < 0) return;
   const Seq sq = at.sq;
   const int64_t nrows = sq.lq * a.group, row0 = (int64_t)at.tile * ROWS;
 
   // this lane's row
-  const int64_t r = row0 + (WM == 4 ? 32 * wave : 0) + col;
+  const int64_t r = row0 + 32 * wave + col;
   const bool live = r < nrows;
   // packed rows of one sequence stay below 2^24 tiles of at most 128
   const int64_t qi = live ? (uint32_t)r / (uint32_t)a.group : 0;
@@ -436,13 +433,13 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
       for (int e = 0; e < QK; ++e) bd[e / 4][e % 4] = j0 + e < ke ? dp[e] : 0;
     }
   };
-  if (a.q_doc && WM == 4 && kb < ke) fetch_docs(kb);
+  if (a.q_doc && kb < ke) fetch_docs(kb);
 
   // Q^T operand: row col, unit 2 ks + half of it (on its way while the ranges are found). Loaded like that, a
   // row at a time, the 32 bytes of a row that an instruction reads come from L2 over and over: 16-bit tiles go
   // through the second buffer in whole rows.
   typedef typename std::conditional<DT == F32, float, short>::type E;   // an element's bits
-  constexpr bool QLDS = DMA && WM == 4 && DT != F32;
+  constexpr bool QLDS = DMA && DT != F32;
   Unit qf[NK];
   GPTQ_LDS char* qarea = smem + BUFB + wave * 32 * ROWB;
   if constexpr (QLDS) {
@@ -502,7 +499,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
       }
     }
   }
-  if (a.q_doc && WM == 4) {   // the workgroup's range of documents
+  if (a.q_doc) {   // the workgroup's range of documents
     if (lane == 0) {
       docs[0] = dmin;
       docs[1] = dmax;
@@ -534,11 +531,10 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
   if (!QLDS) negate_q();
 
   // staging: load q of this wave fills 16-byte units 64 (q + LOADS wave') + lane of a tile
-  const int sub = WM == 4 ? wave : 0;
   int srow[LOADS], ku[LOADS], vu[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
-    const int unit = 64 * (LOADS * sub + i) + lane;
+    const int unit = 64 * (LOADS * wave + i) + lane;
     const int row = unit / UN, up = unit - row * UN;
     srow[i] = row;
     ku[i] = up ^ swz_k<UN>(row);
@@ -553,12 +549,11 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
       vvo[i] = vu[i] * EPU < a.dh ? (uint32_t)((srow[i] * a.v_ld + vu[i] * EPU) * ESZ) : OOB;
     }
   }
-  GPTQ_LDS char* base = smem + (WM == 4 ? 0 : wave * NB * BUFB);
   // whole: every key of the tile has the document of all rows, so their documents are not needed
   auto stage = [&](int64_t j0, int buf, bool whole) {
     const int64_t left = sq.lk - j0;
     const int rows = left < KT ? (int)left : KT;
-    GPTQ_LDS char* kd = base + buf * BUFB + LOADS * sub * 1024;
+    GPTQ_LDS char* kd = smem + buf * BUFB + LOADS * wave * 1024;
     GPTQ_LDS char* vd = kd + TILEB;
     if (DMA) {
       const uint64_t ka = (uint64_t)(uintptr_t)(kp + j0 * a.k_ld), va = (uint64_t)(uintptr_t)(vp + j0 * a.v_ld);
@@ -615,7 +610,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
   const float to_cap = 2.0f * kLog2e * inv_cap;
 
   auto compute = [&](int64_t j0, int buf, bool whole) {
-    GPTQ_LDS char* kt = base + buf * BUFB;
+    GPTQ_LDS char* kt = smem + buf * BUFB;
     GPTQ_LDS char* vt = kt + TILEB;
     floatx16 S[NT];
 #pragma unroll
@@ -740,24 +735,18 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
   };
 
   auto ready = [&]() {   // the staged tile is in LDS, and the other buffer is no longer read
-    if (DMA) {
-      if (WM == 4) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    } else {
-      __syncthreads();
-    }
+    if (DMA) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else __syncthreads();
   };
 
   // Tiles in order, 64 at a time (a block): with documents, the block's tiles that hold a document of the
-  // rows' range are found first, a quarter tile a thread. `ready` in the unaligned WM = 1 form is a workgroup
-  // barrier, so there every wave takes the same number of steps.
-  const int64_t step = WM == 4 ? KT : 4 * KT;
+  // rows' range are found first, a quarter tile a thread.
   int parity = 0;
-  for (int64_t b0 = kb; b0 < ke; b0 += 64 * step) {
+  for (int64_t b0 = kb; b0 < ke; b0 += 64 * KT) {
     uint64_t active = ~0ull, whole = 0;
-    const int64_t left = (ke - b0 + step - 1) / step;
+    const int64_t left = (ke - b0 + KT - 1) / KT;
     if (left < 64) active = (1ull << left) - 1;
-    if (a.q_doc && WM == 4) {
+    if (a.q_doc) {
       const int64_t j0 = b0 + QK * (int64_t)threadIdx.x;
       int32_t lo = 0x7fffffff, hi = (int32_t)0x80000000;
 #pragma unroll
@@ -766,7 +755,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
           lo = min(lo, bd[e / 4][e % 4]);
           hi = max(hi, bd[e / 4][e % 4]);
         }
-      if (b0 + 64 * step < ke) fetch_docs(b0 + 64 * step);
+      if (b0 + 64 * KT < ke) fetch_docs(b0 + 64 * KT);
       lo = min(lo, __shfl_xor(lo, 1, 64));
       hi = max(hi, __shfl_xor(hi, 1, 64));
       lo = min(lo, __shfl_xor(lo, 2, 64));
@@ -785,17 +774,13 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
     active = uniform64(active);
     whole = uniform64(whole);
     if (!active) continue;
-    const int64_t my = WM == 4 ? 0 : wave * KT;   // WM = 1: the wave's tile of each step
-    auto tile_of = [&](int t) { return b0 + t * step + my; };
-    auto exists = [&](int t) { return WM == 4 || tile_of(t) < ke; };
+    auto tile_of = [&](int t) { return b0 + (int64_t)t * KT; };
     int t = __builtin_ctzll(active), buf = 0;
-    // every wave is done with both buffers (of the block before)
-    if (WM == 4 || !DMA) __syncthreads();
-    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (exists(t)) stage(tile_of(t), 0, (whole >> t) & 1);
+    __syncthreads();   // every wave is done with both buffers (of the block before)
+    stage(tile_of(t), 0, (whole >> t) & 1);
     while (true) {
       const int64_t j0 = tile_of(t);
-      const bool have = exists(t), full = (whole >> t) & 1;
+      const bool full = (whole >> t) & 1;
       active &= active - 1;
       ready();
       if (QLDS && !have_q) {
@@ -805,68 +790,17 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
         have_q = true;
         __syncthreads();   // the second buffer is free
       }
-      if (active) t = __builtin_ctzll(active);
-      if (NB == 2 && active && exists(t)) stage(tile_of(t), buf ^ 1, (whole >> t) & 1);
-      if (have && j0 < wmax) compute(j0, buf, full);
-      if (!active) break;
-      if (NB == 2) {
-        buf ^= 1;
-      } else {   // one buffer: the next tile is loaded when this one has been read
-        if (DMA) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        else __syncthreads();
-        if (exists(t)) stage(tile_of(t), 0, (whole >> t) & 1);
+      if (active) {
+        t = __builtin_ctzll(active);
+        stage(tile_of(t), buf ^ 1, (whole >> t) & 1);
       }
+      if (j0 < wmax) compute(j0, buf, full);
+      if (!active) break;
+      buf ^= 1;
     }
   }
   if (QLDS) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // also where no tile was active
   l = mirror_sum(l);
-
-  if (WM == 1) {
-    // join the waves' partial results in wave order; the tiles' area is free now
-    __syncthreads();
-    GPTQ_LDS float* sh = (GPTQ_LDS float*)smem;
-    constexpr int PITCH = 64 * (16 * NF + 1);
-    GPTQ_LDS float* mine = sh + (wave & 1) * PITCH;
-    GPTQ_LDS float* ml = (GPTQ_LDS float*)tail;   // the documents' area, read no more
-    if (half == 0) {
-      ml[64 * wave + col] = m;
-      ml[64 * wave + 32 + col] = l;
-    }
-    __syncthreads();
-    float mj = m;
-    for (int w = 0; w < 4; ++w) mj = fmaxf(mj, ml[64 * w + col]);
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - mj) * c);
-    l = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      const float mw = ml[64 * w + col];
-      l += mw == -INFINITY ? 0.f : ml[64 * w + 32 + col] * __builtin_amdgcn_exp2f((mw - mj) * c);
-    }
-    m = mj;
-#pragma unroll
-    for (int ft = 0; ft < NF; ++ft)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[ft][i] *= f;
-    // (0 + 2) and (1 + 3), then the two sums
-    for (int round = 0; round < 2; ++round) {
-      const bool give = round == 0 ? wave >= 2 : wave == 1, take = round == 0 ? wave < 2 : wave == 0;
-      if (give) {
-#pragma unroll
-        for (int ft = 0; ft < NF; ++ft)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) mine[(16 * ft + i) * 64 + lane] = acc[ft][i];
-      }
-      __syncthreads();
-      if (take) {
-        GPTQ_LDS float* other = round == 0 ? mine : sh + PITCH;
-#pragma unroll
-        for (int ft = 0; ft < NF; ++ft)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[ft][i] += other[(16 * ft + i) * 64 + lane];
-      }
-      __syncthreads();
-    }
-    if (wave != 0) return;
-  }
 
   // rows whose sum is not finite: computed again without the keys they do not see
   float nothing = l * 0.f;   // zero, unless a value is not finite
@@ -880,7 +814,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
     const uint64_t o = __ballot(odd && live);
     redo = (uint32_t)o | (uint32_t)(o >> 32);
   }
-  if (WM == 4 && DMA && a.nsplit == 1 && a.o_rows) {
+  if (DMA && a.nsplit == 1 && a.o_rows) {
     // Rows leave through LDS, 16 bytes a lane along each (a lane's own pieces are 8 bytes of every 16): the
     // tiles' area is free when every wave is here.
     __syncthreads();
@@ -1020,10 +954,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   }
 }
 
-template <int DT, int DHP, int WM, bool DMA, int MODE>
+template <int DT, int DHP, bool DMA, int MODE>
 hipError_t launch_mfma(const AttnArgs& a, hipStream_t s) {
-  constexpr size_t lds = Tile<DT, DHP, WM>::LDS;
-  auto f = attn_mfma_kernel<DT, DHP, WM, DMA, MODE>;
+  constexpr size_t lds = Tile<DT, DHP>::LDS;
+  auto f = attn_mfma_kernel<DT, DHP, DMA, MODE>;
   // the LDS beyond 64 KB is asked for once per device
   static std::atomic<uint64_t> asked{0};
   int dev = 0;
@@ -1039,33 +973,27 @@ hipError_t launch_mfma(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int DT, int DHP, int WM>
+template <int DT, int DHP>
 hipError_t by_mode(const AttnArgs& a, bool dma, hipStream_t s) {
-  if (!dma) return launch_mfma<DT, DHP, WM, false, 2>(a, s);
-  if (a.slopes || a.scale == 0.f) return launch_mfma<DT, DHP, WM, true, 2>(a, s);
-  if (a.cap == 0.f) return launch_mfma<DT, DHP, WM, true, 0>(a, s);
+  if (!dma) return launch_mfma<DT, DHP, false, 2>(a, s);
+  if (a.slopes || a.scale == 0.f) return launch_mfma<DT, DHP, true, 2>(a, s);
+  if (a.cap == 0.f) return launch_mfma<DT, DHP, true, 0>(a, s);
   if constexpr (DT != F32)
-    if (a.cap <= kSmallCap) return launch_mfma<DT, DHP, WM, true, 1>(a, s);
-  return launch_mfma<DT, DHP, WM, true, 2>(a, s);
+    if (a.cap <= kSmallCap) return launch_mfma<DT, DHP, true, 1>(a, s);
+  return launch_mfma<DT, DHP, true, 2>(a, s);
 }
 
 template <int DT>
-hipError_t by_head(const AttnArgs& a, bool dma, bool few, hipStream_t s) {
-  // few rows: each wave needs a buffer of its own, which 160 KB of LDS holds up to 128-wide heads
-  if (few) {
-    if (a.dh <= 64) return by_mode<DT, 64, 1>(a, dma, s);
-    if (a.dh <= 96) return by_mode<DT, 96, 1>(a, dma, s);
-    return by_mode<DT, 128, 1>(a, dma, s);
-  }
-  if (a.dh <= 64) return by_mode<DT, 64, 4>(a, dma, s);
-  if (a.dh <= 96) return by_mode<DT, 96, 4>(a, dma, s);
-  if (a.dh <= 128) return by_mode<DT, 128, 4>(a, dma, s);
-  return by_mode<DT, 256, 4>(a, dma, s);
+hipError_t by_head(const AttnArgs& a, bool dma, hipStream_t s) {
+  if (a.dh <= 64) return by_mode<DT, 64>(a, dma, s);
+  if (a.dh <= 96) return by_mode<DT, 96>(a, dma, s);
+  if (a.dh <= 128) return by_mode<DT, 128>(a, dma, s);
+  return by_mode<DT, 256>(a, dma, s);
 }
 
-// The launch's plan: rows a tile holds, tiles, ranges that keys are split into.
+// The launch's plan: tiles of rows, ranges that keys are split into.
 struct Plan {
-  bool mfma, few;
+  bool mfma;
   int64_t tiles;
   int nsplit;
 };
@@ -1075,10 +1003,7 @@ Plan plan(const gptq_attention_t& t) {
   p.mfma = t.head_dim <= 256;
   if (!p.mfma) return p;
   const int64_t group = t.q_heads / t.kv_heads;
-  // sequences of at most 32 packed rows on average: the four waves split the keys instead of the rows
-  p.few = t.head_dim <= 128 && t.n_q * group <= 32 * t.seqs;
-  const int64_t rows = p.few ? 32 : 128;
-  p.tiles = t.n_q * group / rows + t.seqs;
+  p.tiles = t.n_q * group / kRows + t.seqs;
   // Fewer than two workgroups a CU: split the keys until there are two, in ranges of at least 256 keys (of
   // the average sequence). More ranges cost more than they fill: 16 tokens against 4915 keys each take 67 us
   // with 512 workgroups and 71 with 768.
@@ -1124,8 +1049,7 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
   if (!work || work_bytes < need) p.nsplit = 1;
   a.tiles = p.tiles;
   a.nsplit = p.nsplit;
-  const int64_t rows = p.few ? 32 : 128;
-  a.seq_tiles = (uint32_t)std::min<int64_t>(1 << 24, (a.lq_even * a.group + rows - 1) / rows);
+  a.seq_tiles = (uint32_t)std::min<int64_t>(1 << 24, (a.lq_even * a.group + kRows - 1) / kRows);
   if (p.nsplit > 1) {
     a.part_ml = static_cast<float*>(work);
     a.part_o = a.part_ml + (int64_t)p.nsplit * a.nq * a.hq * 2;
@@ -1141,9 +1065,9 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
                    (128 / a.group + 2) * a.q_ld + a.group * a.q_hp < ((int64_t)1 << 28);
   a.o_rows = reinterpret_cast<uintptr_t>(out) % 16 == 0 && a.o_ld % unit == 0 && a.o_hp % unit == 0;
   a.o_vec = reinterpret_cast<uintptr_t>(out) % (t.dtype == F32 ? 16 : 8) == 0 && a.o_ld % 4 == 0 && a.o_hp % 4 == 0;
-  hipError_t e = t.dtype == F32   ? by_head<F32>(a, dma, p.few, s)
-                 : t.dtype == F16 ? by_head<F16>(a, dma, p.few, s)
-                                  : by_head<BF16>(a, dma, p.few, s);
+  hipError_t e = t.dtype == F32   ? by_head<F32>(a, dma, s)
+                 : t.dtype == F16 ? by_head<F16>(a, dma, s)
+                                  : by_head<BF16>(a, dma, s);
   if (e != hipSuccess || p.nsplit <= 1) return e;
   const dim3 grid((unsigned)std::min<int64_t>((a.nq * a.hq + 3) / 4, 65536));
   if (t.dtype == F32) hipLaunchKernelGGL(attn_join_kernel<F32>, grid, dim3(256), 0, s, a);

@@ -482,10 +482,13 @@ template <int DT>
 hipError_t run(const LoraArgs& a, const Plan& p, hipStream_t s) {
   hipError_t e = a.adapters == 0 ? hipSuccess : a.xvec ? shrink<DT, true>(a, p, s) : shrink<DT, false>(a, p, s);
   if (e != hipSuccess) return e;
-  // Long inputs: 32 rows and 128 columns a workgroup. 4096 x 4096 outputs of rank 64 take 55 us with them,
-  // 62 with 64 rows (half B's reads, fewer waves a CU) and 66 with 256 columns (half T's reads). Few rows:
-  // 16, slots over the waves, and narrow columns while a launch of wide ones has fewer than 512 workgroups.
-  if (a.m >= 512) return launch_expand<DT, 2, 2, false>(a, s);
+  // Long inputs: 32 rows and 128 columns a workgroup. 4096 x 4096 outputs of rank 64 took 55 us with them (50
+  // now), 62 with 64 rows (half B's reads, fewer waves a CU) and 66 with 256 columns (half T's reads). Few
+  // rows: 16, slots over the waves, and narrow columns while a launch of wide ones has fewer than 512
+  // workgroups (4 rows on 4096 columns: 4.2 us against 4.9; 64 on 11008: 21 against 13). The two meet near 256
+  // rows (rank 16): runs of 60 on 4096 columns take 5.7 us in long tiles and 8.0 in short ones, single tokens
+  // over 48 adapters on 11008 columns 40 and 37, 128 of them 28 and 20.
+  if (a.m >= 256) return launch_expand<DT, 2, 2, false>(a, s);
   const int64_t wide = (a.rows + 63) / 64 * ((a.m + 15) / 16);
   return wide >= 512 ? launch_expand<DT, 1, 4, true>(a, s) : launch_expand<DT, 1, 1, true>(a, s);
 }

@@ -211,7 +211,8 @@ hipError_t dispatch(RotArgs a, hipStream_t s) {
   int g = 2;
   while (g < a.chunks && g < 64) g *= 2;
   // Whole tokens for a workgroup, so that their angles are formed once; below 512 workgroups the
-  // heads of a token are shared out instead (each workgroup then forms the angles it needs again).
+  // heads of a token are shared out instead (each workgroup then forms the angles it needs again; 8 tokens of
+  // 40 heads: 5.0 us against 6.2).
   const int heads = a.hq + a.hk, slots = 256 / g;
   int tokens = std::max(1, (8 * slots) / heads);
   tokens = (int)std::min<int64_t>(tokens, std::max<int64_t>(1, a.n / 1024));
