@@ -382,9 +382,10 @@ typedef struct {
  *   pair_axis     device int32[rotary_dim / 2], the row of positions each pair takes (clamped into
  *                 [0, axes)), or NULL: row 0. positions, inv_freq and pair_axis are not used with
  *                 rotary_dim = 0.
- *   q_out, k_out  device arrays, output; each may be its input itself with the same pitches (in place),
- *                 and may otherwise share no element with q, k or the other output (column ranges of one
- *                 array with one token pitch are apart). Heads and tokens of an output must not overlap.
+ *   q_out, k_out  device arrays, output; each may be its input itself with the same pitches (in place).
+ *                 Otherwise its address range must be apart from those of q, k and the other output, or
+ *                 both be column ranges of one array with one token pitch that do not meet; anything
+ *                 else is GPTQ_EINVAL. Heads and tokens of an output must not overlap.
  * The angle is formed in 64 bits, so far positions lose nothing; sums and products are fp32, rounded
  * once to dtype. 16-byte accesses are used where columns, pitches and pointers allow them.
  */
@@ -426,7 +427,8 @@ typedef struct {
  *                  NULL. A negative document (padding) sees nothing and is not seen.
  *   prefix         device int32[seqs]: the first prefix[s] keys are seen by every query of the sequence
  *                  (with causal = 1; it changes nothing otherwise), or NULL.
- *   out            device array, output; must not overlap q, k or v, nor its heads and tokens each other.
+ *   out            device array, output; apart from q, k and v as in gptq_norm_rotate (not in place), its
+ *                  heads and tokens from each other.
  *   work           device workspace of work_bytes bytes (16-byte aligned), or NULL. With at least
  *                  gptq_attention_workspace_bytes(a) bytes, long key ranges are split across workgroups
  *                  when there are few queries and joined in key order; with less (or NULL) they are not.

@@ -45,14 +45,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _device(first: torch.Tensor, **others) -> torch.device:
+def _device(first: torch.Tensor, *others) -> torch.device:
     """The device of the call: every tensor must be on it."""
     if not first.is_cuda:
         raise ValueError("tensors must be on the GPU")
     dev = first.device
-    for name, t in others.items():
+    for t in others:
         if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}")
+            raise ValueError(f"every tensor must be on {dev}")
     return dev
 
 
@@ -91,8 +91,7 @@ def gptq_norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor] = None, position
     root of its mean square (norm), times q_weight / k_weight [head_dim], and its first
     2 * len(inv_freq) columns rotated by positions * inv_freq. positions is int32 [n], or [axes, n] with
     pair_axis (int32, one entry per pair) naming each pair's row. Outputs may be the inputs (in place)."""
-    dev = _device(q, k=k, positions=positions, inv_freq=inv_freq, pair_axis=pair_axis, q_weight=q_weight,
-                  k_weight=k_weight, q_out=q_out, k_out=k_out)
+    dev = _device(q, k, positions, inv_freq, pair_axis, q_weight, k_weight, q_out, k_out)
     n, hq, dh, q_ld, q_hp = _heads(q, "q")
     hk = k_ld = k_hp = ko_ld = ko_hp = 0
     if k is not None:
@@ -186,8 +185,7 @@ def gptq_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Opt
     slopes (float32 [heads]), q_doc and kv_doc (int32 per token) and prefix (int32 per sequence) as in
     gptq.h; scale is 1 / sqrt(head_dim) unless given. work: uint8, gptq_attention_workspace_bytes. Rows of
     out that belong to no sequence are left as they were (undefined in an out made here)."""
-    dev = _device(q, k=k, v=v, q_start=q_start, kv_start=kv_start, slopes=slopes, q_doc=q_doc, kv_doc=kv_doc,
-                  prefix=prefix, out=out, work=work)
+    dev = _device(q, k, v, q_start, kv_start, slopes, q_doc, kv_doc, prefix, out, work)
     for name, t in (("q_start", q_start), ("kv_start", kv_start)):
         if t is not None:
             if t.dim() != 1 or t.numel() < 1:
@@ -225,7 +223,7 @@ def gptq_lora_gemm(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, index: tor
     """y[i] = base[i] + scales[a] * (x[i] A[a]^T) B[a]^T with a = index[i] (outside [0, adapters): base[i]),
     for x [m, d], A [adapters, rank, d], B [adapters, rows, rank] of one dtype, and float32 base and y
     [m, rows]; base None is zeros, and y may be base (added in place, beside gptq_dequant_gemm's y)."""
-    dev = _device(x, A=A, B=B, index=index, scales=scales, ranks=ranks, base=base, y=y, work=work)
+    dev = _device(x, A, B, index, scales, ranks, base, y, work)
     if x.dim() != 2 or x.dtype not in _DTYPE or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be [m, d] with unit column stride, fp32/fp16/bf16")
     m, d = x.shape
