@@ -196,11 +196,12 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraArgs a) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) s[e] += o[e];
             }
+            // ranks past the adapter's are zero whatever x holds: an infinity times A's zeros is NaN here
             const int k = n0 + 16 * n + l16;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int row = 16 * t + 4 * quarter + e;
-              if (k < a.rp && ((mine >> row) & 1)) T[(i0 + row) * a.rp + k] = s[e];
+              if (k < a.rp && ((mine >> row) & 1)) T[(i0 + row) * a.rp + k] = aok[n] ? s[e] : 0.f;
             }
           }
       }
