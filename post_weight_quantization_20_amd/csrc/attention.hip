@@ -936,9 +936,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
       float v[8][NC];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float* po = a.part_o + ((int64_t)(z0 + e < a.nsplit ? z0 + e : z0) * total + it) * a.dh;
+        // zeros past the last range: zero times what another range holds would be NaN for an infinity
+        const float* po = a.part_o + ((int64_t)(z0 + e) * total + it) * a.dh;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) v[e][c] = 64 * c + lane < a.dh ? po[64 * c + lane] : 0.f;
+        for (int c = 0; c < NC; ++c) v[e][c] = z0 + e < a.nsplit && 64 * c + lane < a.dh ? po[64 * c + lane] : 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {   // lanes past the last range hold a factor of zero

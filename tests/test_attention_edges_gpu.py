@@ -46,3 +46,18 @@ def test_lora_infinite_inputs_beside_unused_ranks(m, rank, ranks, dtype):
 
 
 # --------------------------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("n", [600, 2000, 4200, 6000])
+def test_attention_infinity_in_each_split_range(n, dtype):
+    """One infinite value anywhere in a long range shows in its column alone, whatever number of ranges the keys are
+    split into (2, 7, 16 and 23 here)."""
+    torch = torch_cuda()
+    q, k, v = _rand((1, 2, 64), 1, dtype), _rand((n, 1, 64), 2, dtype), _rand((n, 1, 64), 3, dtype)
+    for at in range(60, n, 125):
+        w = v.clone()
+        w[at, 0, 9] = -float("inf")
+        o = _g().gptq_attention(q, k, w)
+        torch.cuda.synchronize()
+        bad = ~torch.isfinite(o)
+        assert torch.all(o[:, :, 9] == -float("inf")) and bad.sum() == 2, at
