@@ -121,7 +121,9 @@ GPTQ_DEV uint64_t uniform64(uint64_t v) {
 
 // One query and head by one wave over keys [j0, j1), 64 at a time: a lane takes a key for the scores and
 // columns lane, lane + 64, ... of the output. Only keys that are seen are read into the output, so this is
-// also the exact path for a row whose tile held infinities or NaN that it may not see. NC: columns a lane.
+// also the exact path for a row whose tile held infinities or NaN that it may not see. acc is the average of
+// the values so far, not their weighted sum, which can pass fp32's range where the average does not: a sum
+// of weights up to l times values above 2^128 / l. NC: columns a lane.
 template <int DT, int NC>
 GPTQ_DEV void attn_row(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i, int h, int lane, int64_t j0, int64_t j1,
                        float (&acc)[NC], float& m, float& l) {
@@ -153,15 +155,16 @@ GPTQ_DEV void attn_row(const AttnArgs& a, const Seq& sq, int64_t s, int64_t i, i
     if (!__ballot(seen && !(sc == -INFINITY))) continue;
     const float mn = fmaxf(m, wave_max(sc));
     const float w = seen ? expf(sc - mn) : 0.f;
-    const float f = expf(m - mn);
+    const float before = l * expf(m - mn);
     m = mn;
-    l = l * f + wave_add(w);
+    l = before + wave_add(w);
+    const float keep = before / l, share = w / l;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) acc[c] *= f;
+    for (int c = 0; c < NC; ++c) acc[c] *= keep;
     const uint64_t vis = __ballot(seen);
     for (int e = 0; e < 64; ++e) {
       if (!((vis >> e) & 1)) continue;
-      const float we = __shfl(w, e, 64);
+      const float we = __shfl(share, e, 64);
       const T* vr = vb + (jb + e) * a.v_ld;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
@@ -176,7 +179,7 @@ GPTQ_DEV void store_row(const AttnArgs& a, int64_t row, int h, int lane, const f
   T* o = static_cast<T*>(a.out) + row * a.o_ld + h * a.o_hp;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
-    if (c * 64 + lane < a.dh) o[c * 64 + lane] = (T)(l == 0.f ? 0.f : acc[c] / l);
+    if (c * 64 + lane < a.dh) o[c * 64 + lane] = (T)(l == 0.f ? 0.f : acc[c]);
 }
 
 // Heads wider than the matrix-core kernels take: waves over (sequence, query, head).
@@ -217,7 +220,9 @@ __global__ __launch_bounds__(256) void attn_row_kernel(AttnArgs a) {
 // The maximum is raised only when a score exceeds it by 8 (in powers of two); probabilities are kept 2^7
 // larger, so they stay below 2^15 and small ones keep their bits in fp16. A masked key's probability is
 // an exact zero, but zero times an infinity or NaN in V is NaN: a row whose result is not finite is
-// computed again by attn_row, which reads the keys that are seen and no others.
+// computed again by attn_row, which reads the keys that are seen and no others. So is a row whose weighted sum
+// passes fp32's range (values above about 2^113, at weights up to 2^15). It is a wave a row and many times
+// slower.
 //
 // Long inputs are bound by the matrix cores and the softmax's vector instructions beside them (2 x 8192 causal
 // bf16 tokens, 32 / 8 heads of 128: 1.21 ms, 0.91 PFLOP/s of the pairs seen; 4 x 2048 fp32 tokens of 32 heads:
@@ -895,13 +900,15 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void attn_mfma_kernel(Attn
     attn_row<DT>(a, sq, at.seq, i2, h2, lane, kb, ke, ar, m2, l2);
     if (a.nsplit > 1) {
       const int64_t pr = ((int64_t)z * a.nq + sq.q0 + i2) * a.hq + h2;
+      int e2;   // the sum as a fraction below one, so that the average times it stays in range
+      const float lf = frexpf(l2, &e2);
       if (lane == 0) {
-        a.part_ml[2 * pr] = m2 * kLog2e;
-        a.part_ml[2 * pr + 1] = l2;
+        a.part_ml[2 * pr] = l2 == 0.f ? m2 : m2 * kLog2e + (float)e2;
+        a.part_ml[2 * pr + 1] = lf;
       }
 #pragma unroll
       for (int cc = 0; cc < NC; ++cc)
-        if (64 * cc + lane < a.dh) a.part_o[pr * a.dh + 64 * cc + lane] = ar[cc];
+        if (64 * cc + lane < a.dh) a.part_o[pr * a.dh + 64 * cc + lane] = ar[cc] * lf;
     } else {
       store_row<DT>(a, sq.q0 + i2, h2, lane, ar, l2);
     }
@@ -930,6 +937,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     // a range that the row does not see takes no part
     const float f = mz == -INFINITY && lz == 0.f ? 0.f : __builtin_amdgcn_exp2f(mz - m);
     const float l = wave_add(lz * f);
+    const float part = l == 0.f ? 0.f : f / l;   // weights of the average: the sum itself may pass fp32's range
     constexpr int NC = 4;
     float acc[NC] = {};
     for (int z0 = 0; z0 < a.nsplit; z0 += 8) {
@@ -943,7 +951,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {   // lanes past the last range hold a factor of zero
-        const float fz = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), z0 + e));
+        const float fz = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, part), z0 + e));
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[c] = __builtin_fmaf(v[e][c], fz, acc[c]);
       }
@@ -951,7 +959,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     T* o = static_cast<T*>(a.out) + row * a.o_ld + h * a.o_hp;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      if (64 * c + lane < a.dh) o[64 * c + lane] = (T)(l == 0.f ? 0.f : acc[c] / l);
+      if (64 * c + lane < a.dh) o[64 * c + lane] = (T)acc[c];
   }
 }
 

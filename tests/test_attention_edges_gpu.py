@@ -61,3 +61,33 @@ def test_attention_infinity_in_each_split_range(n, dtype):
         torch.cuda.synchronize()
         bad = ~torch.isfinite(o)
         assert torch.all(o[:, :, 9] == -float("inf")) and bad.sum() == 2, at
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dh", [64, 128, 300])
+@pytest.mark.parametrize("size", [1e33, 3e34, 1e36, 3e38])
+def test_attention_values_near_the_largest(size, dh, dtype):
+    """Weighted sums of finite values may pass fp32's range; their averages do not. Of one sign and of both, in one
+    range of keys and in several. An average over n keys that is kept key by key errs by u of itself at each, which
+    the keys after it dilute: n / 2 u for even weights, and n / 32 u for four roundings each 64 keys. 1200 keys make
+    638 u; the bound's (2 (dh + 8) spread + 64) u is above 784 u, as the spread is above 5 here."""
+    torch = torch_cuda()
+    r = np.random.default_rng(8)
+    for both in (False, True):
+        for lens in ([(300, 300)], [(1, 1200)], [(2, 700), (3, 800)]):
+            lq, lk = [a for a, _ in lens], [b for _, b in lens]
+            q0, k0 = _starts(lq), _starts(lk)
+            q, k = _rand((q0[-1], 2, dh), 1, dtype, 1.5), _rand((k0[-1], 1, dh), 2, dtype)
+            val = r.uniform(0.3, 1.0, (k0[-1], 1, dh)) * (r.choice([-1.0, 1.0], (k0[-1], 1, dh)) if both else 1.0)
+            v = torch.from_numpy(val * size).to(_dtype(dtype)).cuda()
+            for work in (None, torch.empty(0, dtype=torch.uint8, device="cuda:0")):
+                print(f"values {(size, dh, dtype, both, lens, work is None)}", flush=True)
+                o = _g().gptq_attention(q, k, v, q_start=_ints(q0), kv_start=_ints(k0), work=work)
+                torch.cuda.synchronize()
+                assert torch.isfinite(o).all()
+                # compared in units of the size: the bounds are relative
+                _check_attention(dtype, q, k, v.double() / size, o.double() / size,
+                                 list(zip(q0[:-1], q0[1:], k0[:-1], k0[1:])), dh ** -0.5)
+
+
+# ------------------------------------------------------------------------------------- norm_rotate
