@@ -387,7 +387,7 @@ typedef struct {
  *                 both be column ranges of one array with one token pitch that do not meet; anything
  *                 else is GPTQ_EINVAL. Heads and tokens of an output must not overlap.
  * The angle is formed in 64 bits, so far positions lose nothing; sums and products are fp32, rounded
- * once to dtype. 16-byte accesses are used where columns, pitches and pointers allow them.
+ * once to dtype. Finite heads of any size are normed (squares that leave fp32's range are scaled). 16-byte accesses are used where columns, pitches and pointers allow them.
  */
 gptq_status_t gptq_norm_rotate(const gptq_norm_rotate_t *a, const void *q, const void *k, const void *q_weight,
                                const void *k_weight, const int32_t *positions, const float *inv_freq,

@@ -64,6 +64,42 @@ GPTQ_DEV float2 turn(int32_t pos, float f) {
   return make_float2(c, s);
 }
 
+// Squares of fp32 overflow above 2^64 and lose their bits below 2^-63, in heads that are themselves finite and
+// normal (bf16 has the same range). Where the mean with eps is below 2^-80 (from there on, what at most 1024
+// squares lose, half of 2^-149 each, is under 2^-59 of it) or is not finite, the head is scaled first, by the
+// power of two that takes the larger of its largest element and sqrt(eps) to 1..2: exact, and y = x / rms is
+// the same for both. Returns the mean of the scaled squares plus the scaled eps. A head that holds an infinity or
+// NaN, or nothing but zeros with eps = 0, is left as it was. The group's lanes come here together.
+constexpr float kSmallMean = 0x1p-80f;
+
+template <int G, int MC, int V>
+GPTQ_DEV float rescale(float (&u)[MC][V], float (&v)[MC][V], float eps, float dh, float mean) {
+  float top = sqrtf(eps);
+#pragma unroll
+  for (int m = 0; m < MC; ++m)
+#pragma unroll
+    for (int e = 0; e < V; ++e) top = fmaxf(top, fmaxf(fabsf(u[m][e]), fabsf(v[m][e])));
+#pragma unroll
+  for (int s = 1; s < G; s <<= 1) top = fmaxf(top, __shfl_xor(top, s, G));
+  if (!(top > 0.f && top < INFINITY)) return mean;
+  // within the exponents of normal fp32 numbers; elements below 2^-100 have squares in range at 2^100 times
+  const int e = min(max(ilogbf(top), -100), 126);
+  const float scale = ldexpf(1.0f, -e);
+  float ss = 0.f;
+#pragma unroll
+  for (int m = 0; m < MC; ++m)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      u[m][i] *= scale;
+      v[m][i] *= scale;
+      ss = __builtin_fmaf(u[m][i], u[m][i], ss);
+      ss = __builtin_fmaf(v[m][i], v[m][i], ss);
+    }
+#pragma unroll
+  for (int s = 1; s < G; s <<= 1) ss += __shfl_xor(ss, s, G);
+  return ss / dh + eps * scale * scale;
+}
+
 // The workgroup takes tokens_per_wg tokens and heads_per_wg of their hq + hk heads (queries first).
 // MC: chunks per lane.
 template <int DT, int V, int G, int MC, bool WEIGHTS>
@@ -140,7 +176,9 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(RotArgs a) {
     if (a.norm) {
 #pragma unroll
       for (int s = 1; s < G; s <<= 1) ss += __shfl_xor(ss, s, G);
-      const float r = 1.0f / sqrtf(ss / (float)a.dh + a.eps);
+      float mean = ss / (float)a.dh + a.eps;
+      if (!(mean >= kSmallMean && mean < INFINITY)) mean = rescale<G, MC, V>(u, v, a.eps, (float)a.dh, mean);
+      const float r = 1.0f / sqrtf(mean);
 #pragma unroll
       for (int m = 0; m < MC; ++m)
 #pragma unroll

@@ -91,3 +91,29 @@ def test_attention_values_near_the_largest(size, dh, dtype):
 
 
 # ------------------------------------------------------------------------------------- norm_rotate
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dh,rd,inter", [(2, 2, False), (7, 4, True), (64, 32, False), (128, 128, True),
+                                         (1024, 1024, False)])
+def test_norm_rotate_heads_of_any_size(dh, rd, inter, dtype):
+    """Finite heads whose squares overflow or vanish in fp32 are normed like any other; heads of one huge element
+    too. Scaling by a power of two is exact, so the bound is test_attention_gpu.py's. In 64 bits the oracle's squares
+    stay in range (1e-80 .. 1e77)."""
+    torch = torch_cuda()
+    f = torch.rand(rd // 2, device="cuda:0")
+    qw = _rand((dh,), 3, "f32")
+    for eps, sizes in ((0.0, [1e-40, 1e-30, 1e-22, 1e-12, 1.0, 1e18, 1e19, 1e20, 1e30, 6e37]),
+                       (1e-6, [1.0, 1e18, 1e20, 6e37]), (1e-30, [1e-24, 1e-15, 1e-10, 1e20]),
+                       (1e-42, [1e-30, 1e-21, 1e-20])):
+        n = len(sizes)
+        r = np.random.default_rng(9)
+        x = r.uniform(0.5, 5.0, (n, 3, dh)) * r.choice([-1.0, 1.0], (n, 3, dh)) * np.array(sizes)[:, None, None]
+        x[:, 1, 1:] = x[:, 1, 1:] * 1e-3
+        q = torch.from_numpy(x).to(_dtype(dtype)).cuda()
+        assert torch.isfinite(q).all()
+        pos = _ints(np.arange(n) * 37)
+        print(f"norm_rotate {(dh, rd, inter, dtype, eps)}", flush=True)
+        o, _ = _g().gptq_norm_rotate(q, None, pos, f, q_weight=qw, eps=eps, interleaved=inter)
+        torch.cuda.synchronize()
+        # eps as the fp32 number that the kernel takes
+        _check_rotate(dtype, q, None, o, None, qw, None, pos, f, None, True, float(np.float32(eps)), inter)
