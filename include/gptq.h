@@ -387,7 +387,8 @@ typedef struct {
  *                 both be column ranges of one array with one token pitch that do not meet; anything
  *                 else is GPTQ_EINVAL. Heads and tokens of an output must not overlap.
  * The angle is formed in 64 bits, so far positions lose nothing; sums and products are fp32, rounded
- * once to dtype. Finite heads of any size are normed (squares that leave fp32's range are scaled). 16-byte accesses are used where columns, pitches and pointers allow them.
+ * once to dtype. Finite heads of any size are normed (squares that leave fp32's range are scaled).
+ * 16-byte accesses are used where columns, pitches and pointers allow them.
  */
 gptq_status_t gptq_norm_rotate(const gptq_norm_rotate_t *a, const void *q, const void *k, const void *q_weight,
                                const void *k_weight, const int32_t *positions, const float *inv_freq,
@@ -434,7 +435,8 @@ typedef struct {
  *                  when there are few queries and joined in key order; with less (or NULL) they are not.
  *                  It must not be shared with a concurrent call, two captured graphs included.
  * Scores, the softmax's maximum and sum and the output are fp32. Results do not depend on scheduling.
- * Returns GPTQ_EUNSUPPORTED for 2^24 or more tiles of 128 queries (times the shared heads' group).
+ * Returns GPTQ_EUNSUPPORTED, before anything is queued, when head_dim <= 256 and
+ * (n_q * (q_heads / kv_heads) / 128 + seqs) * kv_heads >= 2^24 (tiles of 128 rows; one launch takes all of them).
  */
 gptq_status_t gptq_attention(const gptq_attention_t *a, const void *q, const void *k, const void *v,
                              const int32_t *q_start, const int32_t *kv_start, const float *slopes,
@@ -540,7 +542,8 @@ typedef struct {
   int32_t causal;
 } gptq_block_attn_t;
 
-/* Workspace bytes for gptq_quantize_block_attn; 0 for invalid arguments. */
+/* Workspace bytes for gptq_quantize_block_attn; 0 for invalid arguments, and for more rows than gptq_attention
+ * takes (the call itself returns GPTQ_EUNSUPPORTED for them). */
 size_t gptq_block_attn_workspace_bytes(const gptq_block_shape_t *shape, const gptq_block_attn_t *attn,
                                        const gptq_params_t *p);
 

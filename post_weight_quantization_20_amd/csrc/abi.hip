@@ -30,9 +30,7 @@ gptq_status_t check_params(const gptq_params_t* p, int64_t d, bool quant) {
   return GPTQ_OK;
 }
 
-gptq_status_t hip_status(hipError_t e) {
-  return e == hipSuccess ? GPTQ_OK : e == hipErrorNotSupported ? GPTQ_EUNSUPPORTED : GPTQ_EHIP;
-}
+gptq_status_t hip_status(hipError_t e) { return e == hipSuccess ? GPTQ_OK : GPTQ_EHIP; }
 
 }  // namespace
 
@@ -398,6 +396,7 @@ gptq_status_t gptq_attention(const gptq_attention_t* a, const void* q, const voi
   if (!q || !out || (a->n_kv > 0 && (!k || !v))) return GPTQ_EINVAL;
   if (!elements_apart(o3) || !apart(o3, q3) || !apart(o3, k3) || !apart(o3, v3)) return GPTQ_EINVAL;
   if (reinterpret_cast<uintptr_t>(work) % 16 != 0) return GPTQ_EINVAL;
+  if (!gptq::attention_fits(*a)) return GPTQ_EUNSUPPORTED;
   return hip_status(gptq::attention(*a, q, k, v, q_start, kv_start, slopes, q_doc, kv_doc, prefix, out, work,
                                     work ? work_bytes : 0, static_cast<hipStream_t>(stream)));
 }
@@ -436,6 +435,7 @@ gptq_status_t block_call(const gptq_block_shape_t* shape, const gptq_block_attn_
     if (!l.W || !l.codes || !l.scales || !l.zeros || !l.g_idx || !l.perm || !l.loss || !dtype_ok(l.w_dtype))
       return GPTQ_EINVAL;
   }
+  if (attn && !gptq::attention_fits(gptq::block_attention(*shape, *attn))) return GPTQ_EUNSUPPORTED;
   if (work_bytes < gptq::block_layout(*shape, attn, *p).total) return GPTQ_ENOMEM;
   return gptq::quantize_block(*shape, attn, X, x_dtype, *p, true_sequential, layers, Y, hess,
                               static_cast<char*>(work), info, static_cast<hipStream_t>(stream));
@@ -451,6 +451,7 @@ size_t gptq_block_workspace_bytes(const gptq_block_shape_t* shape, const gptq_pa
 size_t gptq_block_attn_workspace_bytes(const gptq_block_shape_t* shape, const gptq_block_attn_t* attn,
                                        const gptq_params_t* p) {
   if (!block_shape_ok(shape) || !block_attn_ok(*shape, attn) || !p || p->block_size < 1 || p->block_size > 128) return 0;
+  if (!gptq::attention_fits(gptq::block_attention(*shape, *attn))) return 0;
   return gptq::block_layout(*shape, attn, *p).total;
 }
 

@@ -1025,6 +1025,12 @@ Plan plan(const gptq_attention_t& t) {
 
 }  // namespace
 
+// A grid holds fewer than 2^32 threads; keys are split only far below that.
+bool attention_fits(const gptq_attention_t& t) {
+  const Plan p = plan(t);
+  return !p.mfma || p.tiles * t.kv_heads < (int64_t)1 << 24;
+}
+
 size_t attention_workspace_bytes(const gptq_attention_t& t) {
   const Plan p = plan(t);
   if (!p.mfma || p.nsplit <= 1) return 0;
@@ -1063,7 +1069,6 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
     a.part_ml = static_cast<float*>(work);
     a.part_o = a.part_ml + (int64_t)p.nsplit * a.nq * a.hq * 2;
   }
-  if (a.tiles * a.hk * a.nsplit >= ((int64_t)1 << 24)) return hipErrorNotSupported;   // a grid's 2^32 threads
   // 16-byte units: pointers, pitches and head width multiples of 16 bytes, and a tile inside 31-bit offsets
   const int unit = t.dtype == F32 ? 4 : 8;
   auto al = [&](const void* ptr, int64_t ld, int64_t hp) {

@@ -202,7 +202,9 @@ hipError_t norm_rotate(const gptq_norm_rotate_t& r, const void* q, const void* k
                        const int32_t* pos, const float* inv_freq, const int32_t* pair_axis, void* qo, void* ko,
                        hipStream_t s);
 
-// Attention over packed sequences (attention.hip).
+// Attention over packed sequences (attention.hip). attention_fits: whether one launch takes the call's rows
+// (sequences and queries not zero).
+bool attention_fits(const gptq_attention_t& t);
 size_t attention_workspace_bytes(const gptq_attention_t& t);
 hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, const void* v, const int32_t* q_start,
                      const int32_t* kv_start, const float* slopes, const int32_t* q_doc, const int32_t* kv_doc,

@@ -1,0 +1,35 @@
+"""Refusals and workspace sizes of gptq_norm_rotate, gptq_attention, gptq_lora_gemm and the block driver that reads
+them (CPU only: no call here launches a kernel)."""
+
+import ctypes
+
+import pytest
+
+from test_attention_cpu import EINVAL, FAKE, _attention, _lib
+
+EUNSUPPORTED = -3
+
+
+# ------------------------------------------------------------------------------ more than a launch
+
+def test_attention_refuses_more_tiles_than_one_launch():
+    """(n_q * group / 128 + seqs) * kv_heads from 2^24 on."""
+    big = dict(n_kv=0, seqs=1, q_ld=128, out_ld=128, q_heads=8, head_dim=16, out_hp=16)
+    at = dict(out=FAKE << 30)
+    assert _attention(at, n_q=1 << 30, kv_heads=8, **big) == EUNSUPPORTED
+    assert _attention(at, n_q=1 << 30, kv_heads=1, **big) == EUNSUPPORTED
+    assert _attention(at, n_q=1 << 29, kv_heads=2, **big) == EUNSUPPORTED
+
+
+def test_block_attention_refuses_more_tiles_than_one_launch():
+    """The block driver refuses what its attention would, before anything is queued."""
+    L = _lib()
+    shape = L.gptq_block_shape_t(8, 8, 8, 1 << 8, 1 << 20, 1e-6)
+    at = L.gptq_block_attn_t(kv_heads=8, norm_eps=1e-6, axes=1, causal=1)
+    p = L.gptq_params_t(4, 8, 8, 0, 0, 0, 0, 0.01)
+    assert L.lib().gptq_block_attn_workspace_bytes(ctypes.byref(shape), ctypes.byref(at), ctypes.byref(p)) == 0
+    lay = (L.gptq_block_layer_t * 7)(*[L.gptq_block_layer_t(*[FAKE] * 7, 1) for _ in range(7)])
+    info = (ctypes.c_int64 * 2)()
+    P = ctypes.c_void_p(FAKE)
+    assert L.lib().gptq_quantize_block_attn(ctypes.byref(shape), ctypes.byref(at), P, 1, ctypes.byref(p), 1, lay, P, None,
+                                            P, 1 << 62, info, None) == EUNSUPPORTED
