@@ -346,7 +346,9 @@ gptq_status_t gptq_lora_gemm(const void* x, int32_t dtype, int64_t m, int64_t ld
   if (base && (ld_base < rows || ld_base > kMaxDim)) return GPTQ_EINVAL;
   if (m == 0 || rows == 0) return GPTQ_OK;
   if (!x || !index || !y || (adapters > 0 && (!A || !B || !work))) return GPTQ_EINVAL;
-  const Tensor3 ty{y, m, 1, rows, ld_y, 0, 4}, tb{base, m, 1, rows, ld_base, 0, 4};
+  const Tensor3 tx{x, m, 1, d, ld_x, 0, elem_bytes(dtype)}, ty{y, m, 1, rows, ld_y, 0, 4},
+      tb{base, m, 1, rows, ld_base, 0, 4};
+  if (!pitches_ok(tx) || !pitches_ok(ty) || (base && !pitches_ok(tb))) return GPTQ_EINVAL;
   if (base && !same(ty, tb) && !apart(ty, tb)) return GPTQ_EINVAL;
   if (reinterpret_cast<uintptr_t>(work) % 16 != 0) return GPTQ_EINVAL;
   if (adapters > 0 && work_bytes < gptq::lora_workspace_bytes(m, d, rows, adapters, rank)) return GPTQ_ENOMEM;

@@ -5,7 +5,7 @@ import ctypes
 
 import pytest
 
-from test_attention_cpu import EINVAL, FAKE, _attention, _lib
+from test_attention_cpu import EINVAL, ENOMEM, FAKE, _attention, _lib, _lora
 
 EUNSUPPORTED = -3
 
@@ -33,3 +33,14 @@ def test_block_attention_refuses_more_tiles_than_one_launch():
     P = ctypes.c_void_p(FAKE)
     assert L.lib().gptq_quantize_block_attn(ctypes.byref(shape), ctypes.byref(at), P, 1, ctypes.byref(p), 1, lay, P, None,
                                             P, 1 << 62, info, None) == EUNSUPPORTED
+
+
+# -------------------------------------------------------------------------------------------- lora
+
+@pytest.mark.parametrize("kw", [
+    dict(base=5 * FAKE + 16, ld_y=1 << 31, ld_base=1 << 31),     # overlapping, at a byte count past 64 bits
+    dict(ld_y=1 << 31), dict(ld_x=1 << 31), dict(base=1 << 60, ld_base=1 << 31),
+], ids=str)
+def test_lora_rejects_arrays_past_the_address_space(kw):
+    assert _lora(m=1 << 31, work_bytes=0) == ENOMEM
+    assert _lora(m=1 << 31, work_bytes=0, **kw) == EINVAL
