@@ -392,11 +392,15 @@ class BlockShape:
         return _lib.gptq_block_shape_t(int(self.hidden), int(self.heads), int(self.inter), int(self.seqs),
                                        int(self.seq_len), float(self.eps))
 
+    def head_dim(self) -> int:
+        """Width of a head (no heads: the library refuses the shape)."""
+        return self.hidden // self.heads if self.heads else self.hidden
+
     def layer_dims(self, i: int, kv_heads: Optional[int] = None) -> Tuple[int, int]:
         """(rows, d) of layer i in BLOCK_LAYERS order; kv_heads (None: heads) sets the rows of k and v."""
         rows = self.inter if i in (4, 5) else self.hidden
         if i in (1, 2) and kv_heads is not None:
-            rows = kv_heads * (self.hidden // self.heads)
+            rows = kv_heads * self.head_dim()
         return rows, (self.inter if i == 6 else self.hidden)
 
 
@@ -424,7 +428,7 @@ class BlockAttention:
 
     def c(self, shape: BlockShape, device=None) -> _lib.gptq_block_attn_t:
         """The C descriptor; checks the tensors (on `device`, when given)."""
-        n, dh = shape.seqs * shape.seq_len, shape.hidden // shape.heads
+        n, dh = shape.seqs * shape.seq_len, shape.head_dim()
         rd = 0 if self.inv_freq is None else 2 * self.inv_freq.numel()
         axes = self.positions.shape[0] if self.positions is not None and self.positions.dim() == 2 else 1
         pos = (n,) if self.positions is None or self.positions.dim() == 1 else (axes, n)
