@@ -423,7 +423,11 @@ Plan plan(int64_t m, int64_t d, int64_t adapters) {
   // of at least 512 columns (128 a wave).
   // Long inputs: workgroups for two slots of a tile, so that a tile where two prompts meet takes no longer.
   p.slot_groups = (int)std::min<int64_t>(tiles >= 64 ? 2 : std::min(tile, m), std::max<int64_t>(1, adapters));
-  const int64_t wgs = tiles >= 64 ? tiles : tiles * p.slot_groups;
+  // A tile's slots are not known here and rows mostly share adapters: of the loaded ones at most four a tile count
+  // as work, so that a prompt does not pay for adapters that no row names (1024 rows of one of 64 adapters, rank 64,
+  // 11008 x 4096: 36 us, 76 with all of them counted and 33 with one loaded; single tokens over all 64 take
+  // 386 and 380). Counting one a tile costs them more (429).
+  const int64_t wgs = tiles >= 64 ? tiles : tiles * std::min(p.slot_groups, 4);
   p.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, (512 + wgs - 1) / wgs), d / 512));
   p.kper = ((d + p.ksplit - 1) / p.ksplit + 127) / 128 * 128;
   p.ksplit = (int)((d + p.kper - 1) / p.kper);

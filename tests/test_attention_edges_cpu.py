@@ -56,3 +56,13 @@ def test_block_shape_without_heads_is_refused_by_the_library():
         for heads in (0, 3, -1):
             assert g.gptq_block_workspace_bytes(g.BlockShape(8, heads, 8, 1, 4), p, attn) == 0
     assert g.BlockShape(8, 0, 8, 1, 4).layer_dims(1, 1) == (8, 8)
+
+
+# ------------------------------------------------------------------- adapters that no row names
+
+@pytest.mark.parametrize("m,d", [(40, 4096), (333, 4096), (512, 11008), (1000, 11008), (1024, 4096), (2000, 11008)])
+def test_lora_split_of_features_does_not_follow_the_loaded_adapters(m, d):
+    """The workspace holds one T for each range of d: as many ranges with 64 or 1000 adapters as with four."""
+    f = _lib().lib().gptq_lora_workspace_bytes
+    need = f(m, d, 4096, 4, 16)
+    assert need > 0 and f(m, d, 4096, 64, 16) == need and f(m, d, 4096, 1000, 16) == need
