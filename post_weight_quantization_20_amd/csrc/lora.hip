@@ -492,7 +492,7 @@ hipError_t run(const LoraArgs& a, const Plan& p, hipStream_t s) {
   // rows: 16, slots over the waves, and narrow columns while a launch of wide ones has fewer than 512
   // workgroups (4 rows on 4096 columns: 4.2 us against 4.9; 64 on 11008: 21 against 13). The two meet near 256
   // rows (rank 16): runs of 60 on 4096 columns take 5.7 us in long tiles and 8.0 in short ones, single tokens
-  // over 48 adapters on 11008 columns 40 and 37, 128 of them 28 and 20.
+  // over 48 adapters on 11008 columns 40 and 37, 128 of them 28 and 21.
   if (a.m >= 256) return launch_expand<DT, 2, 2, false>(a, s);
   const int64_t wide = (a.rows + 63) / 64 * ((a.m + 15) / 16);
   return wide >= 512 ? launch_expand<DT, 1, 4, true>(a, s) : launch_expand<DT, 1, 1, true>(a, s);

