@@ -441,10 +441,11 @@ typedef struct {
  *     of the unrounded ones. Random inputs: 2.4e-4..2.9e-4 off in norm in fp16, 2.1e-3 in bf16 (2.1e-4 and 1.6e-3
  *     for the result's rounding alone).
  *   - with a softcap c up to 256, a capped score is up to 2^-22 c off (6e-5 at 256).
- * Results do not depend on scheduling. Finite values of any size give finite averages. Rows whose keys lie beside
- * ones that they do not see and that hold infinities or NaN are right, but computed one by one, as are rows whose
- * weighted sum passes fp32's range: hundreds of times slower (2 x 2048 bf16 tokens, 32 query heads: 29 ms instead
- * of 0.1 with NaN in every padding key and value). Padding is best kept finite.
+ * Results do not depend on scheduling. Finite values give finite averages (within fp32 roundings of its largest
+ * number they may round to infinity). Rows that see infinities or NaN, or whose tiles of keys hold some that they do
+ * not see, are right, but computed one by one, as are rows whose weighted sum passes fp32's range: hundreds of
+ * times slower (2 x 2048 bf16 tokens, 32 query heads: 29 ms instead of 0.1 with NaN in every padding key and value).
+ * Padding is best kept finite.
  * Returns GPTQ_EUNSUPPORTED, before anything is queued, when head_dim <= 256 and
  * (n_q * (q_heads / kv_heads) / 128 + seqs) * kv_heads >= 2^24 (tiles of 128 rows; one launch takes all of them).
  */
