@@ -1,0 +1,519 @@
+"""Cases that time the operators of serving in 8 bits.
+
+Four operators: the root-mean-square norm with the residual's addition and int8 rows as its output
+(norm_quant), the matrix product of such rows with 8-bit weights (int8_gemm), appending keys and values
+to a paged int8 cache with the position rotation on the way (kv_append), and attention over that cache
+(kv_attention).
+
+`run` computes them in their plain form (elementary torch operations in 32 bits, in 64 where a code is
+decided), or, with `own` set, through this package's entry points. `exact` computes them in 64 bits.
+Codes are returned as the values they stand for, in the type of the inputs they were taken from.
+Widths are those of the package's own workloads: 4096 wide with 32 heads of 128, 11008 in the MLP,
+2048-token calibration sequences.
+"""
+
+import math
+import random
+
+import numpy as np
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+BYTES = {"f32": 4, "f16": 2, "bf16": 2}
+
+
+# ---------------------------------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # one step of a small decode batch before its projections: latency
+        dict(name="norm_quant_tokens", op="norm_quant", dtype="f16", n=8, d=4096, residual=True),
+        # four calibration sequences of 2048 tokens through a block's norm
+        dict(name="norm_quant_prompts", op="norm_quant", dtype="bf16", n=8192, d=4096, residual=True),
+        # the MLP's width, an odd token count, fp32 activations, no residual
+        dict(name="norm_quant_wide", op="norm_quant", dtype="f32", n=5003, d=11008, residual=False),
+        # eight requests through a 4096 x 4096 projection: one read of the weights
+        dict(name="int8_gemm_tokens", op="int8_gemm", dtype="f16", m=8, d=4096, rows=4096, stored=False),
+        # a decode batch of 96 requests through a layer stored in 8 bits with zeros
+        dict(name="int8_gemm_requests", op="int8_gemm", dtype="bf16", m=96, d=4096, rows=11008, stored=True),
+        # prompts through the MLP's projection: the matrix cores' rate
+        dict(name="int8_gemm_prompts", op="int8_gemm", dtype="f16", m=8192, d=4096, rows=11008, stored=False),
+        # one new token of each of 32 requests
+        dict(name="kv_append_tokens", op="kv_append", dtype="f16", seqs=32, new=1, past=200, hk=8, dh=128, rd=128,
+             ps=16, interleaved=False, mix=1),
+        # prompts of uneven lengths into an empty cache
+        dict(name="kv_append_prompts", op="kv_append", dtype="bf16", seqs=8, new=2048, past=0, hk=8, dh=128, rd=128,
+             ps=16, interleaved=False, mix=2),
+        # decode: one new token of each of 16 requests against caches of uneven lengths
+        dict(name="kv_attention_tokens", op="kv_attention", dtype="f16", hq=32, hk=8, dh=128, ps=16, seqs=16, new=1,
+             kvlen=8192, ragged=True, causal=True, window=0, cap=0.0, bias=False, mix=3),
+        # one request far into a long document
+        dict(name="kv_attention_long", op="kv_attention", dtype="bf16", hq=32, hk=8, dh=128, ps=64, seqs=1, new=1,
+             kvlen=100003, ragged=False, causal=True, window=0, cap=0.0, bias=False, mix=4),
+        # chunks of four prompts against what is cached of them
+        dict(name="kv_attention_chunks", op="kv_attention", dtype="bf16", hq=32, hk=8, dh=128, ps=16, seqs=4, new=512,
+             kvlen=4096, ragged=True, causal=True, window=0, cap=0.0, bias=False, mix=5),
+        # many short requests that guess a few tokens ahead: fp32, capped scores in a window, 80-wide heads
+        dict(name="kv_attention_guesses", op="kv_attention", dtype="f32", hq=16, hk=16, dh=80, ps=32, seqs=48, new=5,
+             kvlen=700, ragged=True, causal=True, window=256, cap=30.0, bias=False, mix=6),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    mix = rng.randrange(1 << 30)
+    dtype = rng.choice(["f32", "f16", "bf16"])
+    op = rng.choice(["norm_quant", "int8_gemm", "kv_append", "kv_attention", "kv_attention"])
+    if op == "norm_quant":
+        d = rng.choice([1000, 1024, 2048, 4096, 4097, 5120, 11008])
+        return dict(op=op, dtype=dtype, n=_log(rng, 1, 65536 * 512 // d), d=d, residual=rng.random() < 0.8)
+    if op == "int8_gemm":
+        d = rng.choice([1000, 1001, 2048, 4096, 4096, 11008])
+        rows = rng.choice([1000, 2048, 4096, 4097, 11008])
+        return dict(op=op, dtype=dtype, m=_log(rng, 1, min(8192, 8192 * 4096 * 11008 // (d * rows))), d=d, rows=rows,
+                    stored=rng.random() < 0.5)
+    if op == "kv_append":
+        dh = rng.choice([64, 72, 80, 96, 128, 256])
+        hk = rng.choice([1, 2, 4, 8, 16])
+        seqs = _log(rng, 1, 64)
+        new = rng.choice([1, 1, 3, _log(rng, 1, 2048)])
+        new = max(1, min(new, 16384 * 1024 // (seqs * hk * dh)))
+        return dict(op=op, dtype=dtype, seqs=seqs, new=new, past=rng.choice([0, _log(rng, 1, 500)]), hk=hk, dh=dh,
+                    rd=rng.choice([0, dh, dh // 2]), ps=rng.choice([16, 32, 48, 64, 128]),
+                    interleaved=rng.random() < 0.4, mix=mix)
+    dh = rng.choice([64, 72, 80, 96, 128, 256])
+    hk = rng.choice([1, 2, 4, 8])
+    hq = hk * rng.choice([1, 2, 4, 7, 8])
+    seqs = _log(rng, 1, 64)
+    kvlen = _log(rng, 1, 65536)
+    new = rng.choice([1, 1, 1, 2, 5, 33, _log(rng, 1, 1024)])
+    while seqs * kvlen * hk * dh > 16 * 8192 * 1024 and (seqs > 1 or kvlen > 1024):
+        seqs, kvlen = max(1, seqs * 3 // 4), max(1, kvlen * 3 // 4)
+    new = min(new, kvlen)
+    while seqs * hq * new * kvlen * max(dh, 128) > 3 * 10 ** 10 and new > 1:
+        new = new * 3 // 4
+    return dict(op=op, dtype=dtype, hq=hq, hk=hk, dh=dh, ps=rng.choice([16, 16, 32, 48, 64, 128]), seqs=seqs, new=new,
+                kvlen=kvlen, ragged=rng.random() < 0.6, causal=rng.random() < 0.85,
+                window=rng.choice([0, 0, 0, 128, 1000]), cap=rng.choice([0.0, 0.0, 30.0]), bias=rng.random() < 0.2,
+                mix=mix)
+
+
+# ---------------------------------------------------------------------------------------- layouts
+
+def _lengths(case):
+    """(new tokens, tokens with the new ones) of each sequence of a cache case."""
+    r = random.Random(case["mix"])
+    new, total = [], []
+    for _ in range(case["seqs"]):
+        if case["op"] == "kv_append":
+            past = r.randint(0, 2 * case["past"])
+            a = case["new"] if case["new"] < 8 else max(1, int(case["new"] * r.uniform(0.3, 1.0)))
+            new.append(a)
+            total.append(past + a)
+        else:
+            lk = max(1, int(case["kvlen"] * r.uniform(0.3, 1.0))) if case["ragged"] else case["kvlen"]
+            new.append(min(case["new"], lk))
+            total.append(lk)
+    return new, total
+
+
+def _pairs(case, lq, lk):
+    """(query and key pairs that are seen, keys that any query sees) of a sequence."""
+    w = case["window"]
+    if not case["causal"]:
+        if not w:
+            return lq * lk, lk
+        return sum(lk - max(0, p - w + 1) for p in range(lk - lq, lk)), lk - max(0, lk - lq - w + 1)
+    if not w:
+        return (lk - lq + 1 + lk) * lq // 2, lk
+    return sum(min(w, p + 1) for p in range(lk - lq, lk)), lk - max(0, lk - lq - w + 1)
+
+
+def work(case):
+    e = BYTES[case["dtype"]]
+    if case["op"] == "norm_quant":
+        n, d = case["n"], case["d"]
+        return {"bytes": n * d * (e * (3 if case["residual"] else 1) + 1) + d * e + 4 * n, "flops": 8 * n * d}
+    if case["op"] == "int8_gemm":
+        m, d, rows = case["m"], case["d"], case["rows"]
+        return {"bytes": m * d + rows * d + m * rows * e + 4 * (m + rows * (2 if case["stored"] else 1)),
+                "flops": 2 * m * d * rows}
+    new, total = _lengths(case)
+    if case["op"] == "kv_append":
+        elems = 2 * sum(new) * case["hk"] * case["dh"]
+        blocks = sum(-(-t // case["ps"]) - (t - a) // case["ps"] for a, t in zip(new, total))
+        return {"bytes": elems * (e + 1) + 16 * blocks * case["hk"], "flops": 8 * elems}
+    pairs, keys = (sum(v) for v in zip(*(_pairs(case, a, t) for a, t in zip(new, total))))
+    return {"bytes": 2 * e * sum(new) * case["hq"] * case["dh"] + 2 * keys * case["hk"] * case["dh"]
+            + 8 * keys * case["hk"] // case["ps"],
+            "flops": 4 * case["dh"] * case["hq"] * pairs}
+
+
+# ---------------------------------------------------------------------------------------- inputs
+
+def _pages(case, total, gen, dev):
+    """A table of distinct pages in random order (-1 behind a sequence's last) and the pool's size: one page in
+    sixteen is another program's."""
+    counts = [-(-t // case["ps"]) for t in total]
+    used = sum(counts)
+    pool = used + used // 16 + 1
+    order = torch.randperm(pool, generator=gen, device=dev)[:used].int()
+    at = torch.cumsum(torch.tensor([0] + counts[:-1], device=dev), 0)[:, None] + torch.arange(max(counts), device=dev)
+    live = torch.arange(max(counts), device=dev) < torch.tensor(counts, device=dev)[:, None]
+    return torch.where(live, order[torch.where(live, at, 0)], -1).contiguous(), pool
+
+
+def _cache(case, pool, gen, dev):
+    """Codes and scales of a cache in use; heads of different sizes."""
+    hk, dh, ps = case["hk"], case["dh"], case["ps"]
+    got = []
+    for _ in range(2):
+        size = torch.rand(1, hk, generator=gen, device=dev) * 1.5 + 0.3
+        scale = size * (torch.rand(pool, hk, generator=gen, device=dev) * 0.4 + 0.9) / 36.0
+        codes = torch.randn(pool, ps, hk, dh, generator=gen, device=dev).mul_(36.0).round_().clamp_(-127, 127)
+        got += [codes.to(torch.int8), scale]
+    return got
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    dt = DTYPES[case["dtype"]]
+
+    def normal(*shape, scale=1.0):
+        return torch.randn(*shape, generator=gen, device=dev) * scale
+
+    def ints(values):
+        return torch.tensor(values, dtype=torch.int32, device=dev)
+
+    s = {"case": case, "dtype": dt}
+    if case["op"] == "norm_quant":
+        n, d = case["n"], case["d"]
+        # one channel in a hundred is an outlier, as in the calibration activations
+        size = torch.where(torch.rand(d, generator=gen, device=dev) < 0.01, 20.0, 1.0)
+        s["x"] = (normal(n, d) * size).to(dt)
+        s["residual"] = normal(n, d, scale=2.0).to(dt) if case["residual"] else None
+        s["weight"] = (1 + normal(d, scale=0.2)).to(dt)
+        s["sum"] = torch.empty(n, d, dtype=dt, device=dev) if case["residual"] else None
+        s["codes"] = torch.empty(n, d, dtype=torch.int8, device=dev)
+        s["scales"] = torch.empty(n, device=dev)
+        s["values"] = torch.empty(n, d, dtype=dt, device=dev)
+        s["eps"] = 1e-6
+    elif case["op"] == "int8_gemm":
+        m, d, rows = case["m"], case["d"], case["rows"]
+        s["x"] = normal(m, d, scale=36.0).round_().clamp_(-127, 127).to(torch.int8)
+        s["x_scales"] = torch.rand(m, generator=gen, device=dev) * 0.02 + 0.01
+        w = normal(rows, d, scale=36.0)
+        s["zeros"] = None
+        if case["stored"]:             # codes of an asymmetric grid
+            s["zeros"] = torch.randint(118, 139, (rows,), generator=gen, device=dev).int()
+            s["w"] = w.add_(s["zeros"][:, None]).round_().clamp_(0, 255).to(torch.uint8)
+        else:
+            s["w"] = w.round_().clamp_(-127, 127).to(torch.int8)
+        s["w_scales"] = (torch.rand(rows, generator=gen, device=dev) + 0.5) * 0.02 / 36
+        s["y"] = torch.empty(m, rows, dtype=dt, device=dev)
+    else:
+        new, total = _lengths(case)
+        hk, dh = case["hk"], case["dh"]
+        s["table"], pool = _pages(case, total, gen, dev)
+        s["k_cache"], s["k_scales"], s["v_cache"], s["v_scales"] = _cache(case, pool, gen, dev)
+        s["new"], s["total"] = new, total
+        s["start"] = ints([sum(new[:i]) for i in range(len(new) + 1)])
+        if case["op"] == "kv_append":
+            n = sum(new)
+            qkv = normal(n, 2 * hk, dh).to(dt)          # column ranges of one projection's output
+            s["k"], s["v"] = qkv[:, :hk], qkv[:, hk:]
+            s["past"] = ints([t - a for a, t in zip(new, total)])
+            rd = case["rd"]
+            s["inv_freq"] = None
+            if rd:
+                s["inv_freq"] = (10000.0 ** (-torch.arange(rd // 2, dtype=torch.float64, device=dev) * 2 / rd)).float()
+            s["k_values"] = torch.empty(s["k_cache"].shape, dtype=dt, device=dev)
+            s["v_values"] = torch.empty(s["v_cache"].shape, dtype=dt, device=dev)
+        else:
+            hq = case["hq"]
+            s["q"] = normal(sum(new), hq, dh, scale=1.5).to(dt)
+            s["lens"] = ints(total)
+            s["scale"] = 1.0 / math.sqrt(dh)
+            s["slopes"] = None
+            if case["bias"]:
+                s["slopes"] = torch.tensor([2.0 ** (-8.0 * (h + 1) / hq) for h in range(hq)], device=dev)
+            s["out"] = torch.empty(sum(new), hq, dh, dtype=dt, device=dev)
+            s["work"] = None
+            if own:
+                import post_weight_quantization_20_amd as g
+                nb = g.gptq_kv_attention_workspace_bytes(s["q"], s["k_cache"], s["table"])
+                s["work"] = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+    return s
+
+
+# ---------------------------------------------------------------------------------------- one pass
+
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        return {"norm_quant": _own_norm_quant, "int8_gemm": _own_int8_gemm, "kv_append": _own_kv_append,
+                "kv_attention": _own_kv_attention}[op](state)
+    return {"norm_quant": _plain_norm_quant, "int8_gemm": _plain_int8_gemm, "kv_append": _plain_kv_append,
+            "kv_attention": _plain_kv_attention}[op](state)
+
+
+def _cache_values(s):
+    """What the cache's codes stand for, in the type of the keys and values."""
+    torch.mul(s["k_cache"], s["k_scales"][:, None, :, None], out=s["k_values"])
+    torch.mul(s["v_cache"], s["v_scales"][:, None, :, None], out=s["v_values"])
+    return s["k_values"], s["v_values"], s["k_scales"], s["v_scales"]
+
+
+def _own_norm_quant(s):
+    import post_weight_quantization_20_amd as g
+    codes, scales, total = g.gptq_norm_quant(s["x"], residual=s["residual"], weight=s["weight"], eps=s["eps"],
+                                             sum_out=s["sum"], codes=s["codes"], scales=s["scales"])
+    return torch.mul(codes, scales[:, None], out=s["values"]), scales, total
+
+
+def _own_int8_gemm(s):
+    import post_weight_quantization_20_amd as g
+    return g.gptq_int8_gemm(s["x"], s["x_scales"], s["w"], s["w_scales"], zeros=s["zeros"], y=s["y"])
+
+
+def _own_kv_append(s):
+    import post_weight_quantization_20_amd as g
+    g.gptq_kv_append(s["k"], s["v"], s["k_cache"], s["v_cache"], s["k_scales"], s["v_scales"], s["table"], s["past"],
+                     start=s["start"], inv_freq=s["inv_freq"], interleaved=s["case"]["interleaved"])
+    return _cache_values(s)
+
+
+def _own_kv_attention(s):
+    import post_weight_quantization_20_amd as g
+    case = s["case"]
+    return g.gptq_kv_attention(s["q"], s["k_cache"], s["v_cache"], s["k_scales"], s["v_scales"], s["table"], s["lens"],
+                               scale=s["scale"], causal=case["causal"], q_start=s["start"], window=case["window"],
+                               softcap=case["cap"], slopes=s["slopes"], out=s["out"], work=s["work"])
+
+
+def _plain_norm_quant(s):
+    h = s["x"]
+    if s["residual"] is not None:
+        h = (h.float() + s["residual"].float()).to(s["dtype"])
+    rms = torch.sqrt((h.float() * h.float()).mean(-1, keepdim=True) + s["eps"])
+    p = h.double() * s["weight"].double()                # a code is decided by p / max |p|
+    top = p.abs().amax(-1, keepdim=True)
+    codes = torch.round(p * 127.0 / torch.where(top == 0, 1.0, top))
+    scales = (top.float() / 127.0 / rms)[:, 0]
+    values = (codes.float() * scales[:, None]).to(s["dtype"])
+    return values, scales, h if s["residual"] is not None else None
+
+
+def _plain_int8_gemm(s):
+    w = s["w"].float()
+    if s["zeros"] is not None:
+        w = w - s["zeros"].float()[:, None]
+    y = torch.matmul(s["x"].float(), w.T)
+    return (y * s["x_scales"][:, None] * s["w_scales"]).to(s["dtype"])
+
+
+def _plain_kv_append(s):
+    case = s["case"]
+    ps, hk, rd = case["ps"], case["hk"], case["rd"]
+    dev = s["k"].device
+    tok = torch.arange(s["k"].shape[0], device=dev)
+    seq = torch.bucketize(tok, s["start"][1:].long(), right=True)
+    place = s["past"][seq].long() + tok - s["start"][seq]
+    page = s["table"][seq, place // ps].long()
+    off = place % ps
+
+    k = s["k"].double()                                   # a code is decided in 64 bits
+    if rd:
+        angle = place.double()[:, None] * s["inv_freq"].double()
+        cos, sin = angle.cos()[:, None], angle.sin()[:, None]
+        rot, rest = k[..., :rd], k[..., rd:]
+        if case["interleaved"]:
+            a, b = rot[..., 0::2], rot[..., 1::2]
+            rot = torch.stack((a * cos - b * sin, b * cos + a * sin), -1).flatten(-2)
+        else:
+            a, b = rot[..., :rd // 2], rot[..., rd // 2:]
+            rot = torch.cat((a * cos - b * sin, b * cos + a * sin), -1)
+        k = torch.cat((rot, rest), -1)
+
+    pool = s["k_cache"].shape[0]
+    first = torch.full((pool,), ps, dtype=torch.long, device=dev).scatter_reduce_(0, page, off, "amin")
+    touched = torch.unique(page)
+    begun = (first[touched] > 0)[:, None]                 # the page holds earlier tokens
+    early = (torch.arange(ps, device=dev) < first[touched][:, None])[..., None, None]
+
+    def store(x, cache, scales):
+        top = torch.zeros(pool, hk, dtype=torch.float64, device=dev)
+        top.scatter_reduce_(0, page[:, None].expand(-1, hk), x.abs().amax(-1), "amax")
+        before = scales[touched]
+        now = torch.maximum((top[touched] / 127.0).float(), torch.where(begun, before, 0.0))
+        ratio = torch.where(now == 0, 0.0, before.double()) / torch.where(now == 0, 1.0, now.double())
+        old = cache[touched]
+        cache[touched] = torch.where(early, torch.round(old.double() * ratio[:, None, :, None]), old.double()).to(torch.int8)
+        scales[touched] = now
+        step = scales[page].double()
+        step = torch.where(step == 0, 1.0, step)
+        cache[page, off] = torch.round(x / step[..., None]).clamp(-127, 127).to(torch.int8)
+
+    store(k, s["k_cache"], s["k_scales"])
+    store(s["v"].double(), s["v_cache"], s["v_scales"])
+    return _cache_values(s)
+
+
+def _plain_kv_attention(s):
+    # every sequence padded to the longest
+    case = s["case"]
+    hq, hk, dh, ps = case["hq"], case["hk"], case["dh"], case["ps"]
+    group, dev = hq // hk, s["q"].device
+    seqs, pages = s["table"].shape
+    lens = s["lens"].long()
+    tok = torch.arange(s["q"].shape[0], device=dev)
+    seq = torch.bucketize(tok, s["start"][1:].long(), right=True)
+    at = tok - s["start"][seq]
+    counts = (s["start"][1:] - s["start"][:-1]).long()
+    most = max(s["new"])
+
+    rows = s["table"].clamp(min=0).long()
+
+    def read(cache, scales):                              # [seqs, hk, keys, dh]
+        x = cache[rows].float() * scales[rows][:, :, None, :, None]
+        return x.reshape(seqs, pages * ps, hk, dh).transpose(1, 2).contiguous()
+
+    k, v = read(s["k_cache"], s["k_scales"]), read(s["v_cache"], s["v_scales"])
+    q = torch.zeros(seqs, most, hq, dh, device=dev)
+    q[seq, at] = s["q"].float()
+    q = q.reshape(seqs, most, hk, group, dh).permute(0, 2, 3, 1, 4).reshape(seqs, hk, group * most, dh)
+    score = torch.matmul(q, k.transpose(2, 3).contiguous()) * s["scale"]
+    score = score.view(seqs, hk, group, most, pages * ps)
+    if case["cap"]:
+        score = torch.tanh(score / case["cap"]) * case["cap"]
+    pos = (torch.arange(most, device=dev) + (lens - counts)[:, None])[:, None, None, :, None]
+    key = torch.arange(pages * ps, device=dev)
+    if s["slopes"] is not None:
+        score = score - s["slopes"].view(hk, group, 1, 1) * (pos - key).abs().float()
+    seen = (key < lens.view(-1, 1, 1, 1, 1)) & (s["table"] >= 0).repeat_interleave(ps, 1)[:, None, None, None]
+    if case["causal"]:
+        seen = seen & (key <= pos)
+    if case["window"]:
+        seen = seen & (pos - key < case["window"])
+    score = torch.where(seen, score, float("-inf"))
+    top = score.amax(-1, keepdim=True)
+    e = torch.exp(score - torch.where(top == float("-inf"), 0.0, top))
+    total = e.sum(-1, keepdim=True)
+    out = torch.matmul(e.reshape(seqs, hk, group * most, pages * ps), v).view(seqs, hk, group, most, dh)
+    out = out / torch.where(total == 0, 1.0, total)
+    return out.permute(0, 3, 1, 2, 4).reshape(seqs, most, hq, dh)[seq, at].to(s["dtype"])
+
+
+# ---------------------------------------------------------------------------------------- 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"norm_quant": _exact_norm_quant, "int8_gemm": _exact_int8_gemm, "kv_append": _exact_kv_append,
+            "kv_attention": _exact_kv_attention}[case["op"]](s)
+
+
+def _exact_norm_quant(s):
+    # in pieces of rows; the norm is of the sum as it is stored
+    values, scales, sums = [], [], []
+    for t in range(0, s["x"].shape[0], 4096):
+        total = s["x"][t:t + 4096].to(torch.float64)
+        held = total
+        if s["residual"] is not None:
+            total = total + s["residual"][t:t + 4096].to(torch.float64)
+            held = total.to(s["dtype"]).to(torch.float64)
+        norm = torch.linalg.vector_norm(held, dim=1, keepdim=True)
+        y = held / (norm ** 2 / held.shape[1] + s["eps"]).sqrt() * s["weight"].to(torch.float64)
+        p = held * s["weight"].to(torch.float64)
+        peak = torch.linalg.vector_norm(p, ord=math.inf, dim=1, keepdim=True)
+        codes = ((p * 127.0) / peak.clamp_min(1e-300)).round()
+        step = torch.linalg.vector_norm(y, ord=math.inf, dim=1, keepdim=True) / 127.0
+        values.append(codes * step)
+        scales.append(step[:, 0])
+        sums.append(total)
+    return torch.cat(values), torch.cat(scales), torch.cat(sums) if s["residual"] is not None else None
+
+
+def _exact_int8_gemm(s):
+    # whole numbers below 2^53 are exact
+    zeros = torch.zeros(s["w"].shape[0], dtype=torch.float64, device=s["w"].device) if s["zeros"] is None \
+        else s["zeros"].to(torch.float64)
+    x, w = s["x"].to(torch.float64), s["w"].to(torch.float64)
+    whole = x @ w.T - x.sum(1, keepdim=True) * zeros
+    return whole * torch.outer(s["x_scales"].to(torch.float64), s["w_scales"].to(torch.float64))
+
+
+def _exact_kv_append(s):
+    # page by page, on the host
+    case = s["case"]
+    ps, rd = case["ps"], case["rd"]
+    half = rd // 2
+    k, v = s["k"].double().cpu().numpy().copy(), s["v"].double().cpu().numpy()
+    table = s["table"].cpu().numpy()
+    caches = [s[n].cpu().numpy().astype(np.float64) for n in ("k_cache", "v_cache")]
+    steps = [s[n].cpu().numpy().copy() for n in ("k_scales", "v_scales")]
+    r0 = 0
+    for i, (a, t) in enumerate(zip(s["new"], s["total"])):
+        past = t - a
+        if rd:
+            turn = np.exp(1j * np.arange(past, t)[:, None] * s["inv_freq"].double().cpu().numpy()[None])[:, None]
+            re = np.arange(half) * 2 if case["interleaved"] else np.arange(half)
+            im = re + (1 if case["interleaved"] else half)
+            mine = k[r0:r0 + a]
+            z = (mine[..., re] + 1j * mine[..., im]) * turn
+            mine[..., re], mine[..., im] = z.real, z.imag
+        for b in range(past // ps, -(-t // ps)):
+            lo, hi = max(past, b * ps), min(t, (b + 1) * ps)
+            page, o0 = table[i, b], lo - b * ps
+            for x, cache, step in zip((k, v), caches, steps):
+                rows = x[r0 + lo - past:r0 + hi - past]
+                peak = (np.abs(rows).max((0, 2)) / 127.0).astype(np.float32)
+                if o0:
+                    peak = np.maximum(peak, step[page])
+                    d = np.where(peak == 0, 1.0, peak.astype(np.float64))
+                    cache[page, :o0] = np.rint(cache[page, :o0] * (step[page].astype(np.float64) / d)[:, None])
+                step[page] = peak
+                d = np.where(peak == 0, 1.0, peak.astype(np.float64))
+                cache[page, o0:o0 + hi - lo] = np.clip(np.rint(rows / d[:, None]), -127, 127)
+        r0 += a
+    values = [c * t.astype(np.float64)[:, None, :, None] for c, t in zip(caches, steps)]
+    return values[0], values[1], steps[0].astype(np.float64), steps[1].astype(np.float64)
+
+
+def _exact_kv_attention(s):
+    # sequence by sequence and head by head, in pieces of queries
+    case = s["case"]
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device=s["q"].device)
+    group, ps = case["hq"] // case["hk"], case["ps"]
+    q0 = 0
+    for i, (lq, lk) in enumerate(zip(s["new"], s["total"])):
+        mine = s["table"][i, :-(-lk // ps)].long()
+        j = torch.arange(lk, device=out.device)
+        for g in range(case["hk"]):
+            kd = (s["k_cache"][mine, :, g].double() * s["k_scales"][mine, g].double()[:, None, None]).flatten(0, 1)[:lk]
+            vd = (s["v_cache"][mine, :, g].double() * s["v_scales"][mine, g].double()[:, None, None]).flatten(0, 1)[:lk]
+            for a in range(0, lq, 256):
+                b = min(lq, a + 256)
+                p = (torch.arange(a, b, device=out.device) + lk - lq).unsqueeze(1)
+                hidden = torch.zeros(b - a, lk, dtype=torch.bool, device=out.device)
+                if case["causal"]:
+                    hidden = hidden | (j > p)
+                if case["window"]:
+                    hidden = hidden | (j <= p - case["window"])
+                for h in range(g * group, (g + 1) * group):
+                    z = (s["q"][q0 + a:q0 + b, h].double() @ kd.T).mul_(s["scale"])
+                    if case["cap"]:
+                        z = z.div_(case["cap"]).tanh_().mul_(case["cap"])
+                    if s["slopes"] is not None:
+                        z -= s["slopes"][h].double() * (p - j).abs()
+                    z.masked_fill_(hidden, -math.inf)
+                    shift = torch.logsumexp(z, 1, keepdim=True)
+                    out[q0 + a:q0 + b, h] = torch.where(torch.isinf(shift), 0.0, (z - shift).exp()) @ vd
+        q0 += lq
+    return out
