@@ -1,7 +1,7 @@
 """Cases that time the operators of serving in 8 bits.
 
 Four operators: the root-mean-square norm with the residual's addition and int8 rows as its output
-(norm_quant), the matrix product of such rows with 8-bit weights (int8_gemm), appending keys and values
+(norm_quant), the matrix product of such rows with 8-bit weights (byte_gemm), appending keys and values
 to a paged int8 cache with the position rotation on the way (kv_append), and attention over that cache
 (kv_attention).
 
@@ -35,11 +35,11 @@ def listed():
         # the MLP's width, an odd token count, fp32 activations, no residual
         dict(name="norm_quant_wide", op="norm_quant", dtype="f32", n=5003, d=11008, residual=False),
         # eight requests through a 4096 x 4096 projection: one read of the weights
-        dict(name="int8_gemm_tokens", op="int8_gemm", dtype="f16", m=8, d=4096, rows=4096, stored=False),
+        dict(name="byte_gemm_tokens", op="byte_gemm", dtype="f16", m=8, d=4096, rows=4096, stored=False),
         # a decode batch of 96 requests through a layer stored in 8 bits with zeros
-        dict(name="int8_gemm_requests", op="int8_gemm", dtype="bf16", m=96, d=4096, rows=11008, stored=True),
+        dict(name="byte_gemm_requests", op="byte_gemm", dtype="bf16", m=96, d=4096, rows=11008, stored=True),
         # prompts through the MLP's projection: the matrix cores' rate
-        dict(name="int8_gemm_prompts", op="int8_gemm", dtype="f16", m=8192, d=4096, rows=11008, stored=False),
+        dict(name="byte_gemm_prompts", op="byte_gemm", dtype="f16", m=8192, d=4096, rows=11008, stored=False),
         # one new token of each of 32 requests
         dict(name="kv_append_tokens", op="kv_append", dtype="f16", seqs=32, new=1, past=200, hk=8, dh=128, rd=128,
              ps=16, interleaved=False, mix=1),
@@ -68,11 +68,11 @@ def _log(rng, lo, hi):
 def draw(rng):
     mix = rng.randrange(1 << 30)
     dtype = rng.choice(["f32", "f16", "bf16"])
-    op = rng.choice(["norm_quant", "int8_gemm", "kv_append", "kv_attention", "kv_attention"])
+    op = rng.choice(["norm_quant", "byte_gemm", "kv_append", "kv_attention", "kv_attention"])
     if op == "norm_quant":
         d = rng.choice([1000, 1024, 2048, 4096, 4097, 5120, 11008])
         return dict(op=op, dtype=dtype, n=_log(rng, 1, 65536 * 512 // d), d=d, residual=rng.random() < 0.8)
-    if op == "int8_gemm":
+    if op == "byte_gemm":
         d = rng.choice([1000, 1001, 2048, 4096, 4096, 11008])
         rows = rng.choice([1000, 2048, 4096, 4097, 11008])
         return dict(op=op, dtype=dtype, m=_log(rng, 1, min(8192, 8192 * 4096 * 11008 // (d * rows))), d=d, rows=rows,
@@ -139,7 +139,7 @@ def work(case):
     if case["op"] == "norm_quant":
         n, d = case["n"], case["d"]
         return {"bytes": n * d * (e * (3 if case["residual"] else 1) + 1) + d * e + 4 * n, "flops": 8 * n * d}
-    if case["op"] == "int8_gemm":
+    if case["op"] == "byte_gemm":
         m, d, rows = case["m"], case["d"], case["rows"]
         return {"bytes": m * d + rows * d + m * rows * e + 4 * (m + rows * (2 if case["stored"] else 1)),
                 "flops": 2 * m * d * rows}
@@ -205,7 +205,7 @@ def prepare(case, seed):
         s["scales"] = torch.empty(n, device=dev)
         s["values"] = torch.empty(n, d, dtype=dt, device=dev)
         s["eps"] = 1e-6
-    elif case["op"] == "int8_gemm":
+    elif case["op"] == "byte_gemm":
         m, d, rows = case["m"], case["d"], case["rows"]
         s["x"] = normal(m, d, scale=36.0).round_().clamp_(-127, 127).to(torch.int8)
         s["x_scales"] = torch.rand(m, generator=gen, device=dev) * 0.02 + 0.01
@@ -258,9 +258,9 @@ def prepare(case, seed):
 def run(state):
     op = state["case"]["op"]
     if own:
-        return {"norm_quant": _own_norm_quant, "int8_gemm": _own_int8_gemm, "kv_append": _own_kv_append,
+        return {"norm_quant": _own_norm_quant, "byte_gemm": _own_byte_gemm, "kv_append": _own_kv_append,
                 "kv_attention": _own_kv_attention}[op](state)
-    return {"norm_quant": _plain_norm_quant, "int8_gemm": _plain_int8_gemm, "kv_append": _plain_kv_append,
+    return {"norm_quant": _plain_norm_quant, "byte_gemm": _plain_byte_gemm, "kv_append": _plain_kv_append,
             "kv_attention": _plain_kv_attention}[op](state)
 
 
@@ -278,9 +278,9 @@ def _own_norm_quant(s):
     return torch.mul(codes, scales[:, None], out=s["values"]), scales, total
 
 
-def _own_int8_gemm(s):
+def _own_byte_gemm(s):
     import post_weight_quantization_20_amd as g
-    return g.gptq_int8_gemm(s["x"], s["x_scales"], s["w"], s["w_scales"], zeros=s["zeros"], y=s["y"])
+    return g.gptq_byte_gemm(s["x"], s["x_scales"], s["w"], s["w_scales"], zeros=s["zeros"], y=s["y"])
 
 
 def _own_kv_append(s):
@@ -311,7 +311,7 @@ def _plain_norm_quant(s):
     return values, scales, h if s["residual"] is not None else None
 
 
-def _plain_int8_gemm(s):
+def _plain_byte_gemm(s):
     w = s["w"].float()
     if s["zeros"] is not None:
         w = w - s["zeros"].float()[:, None]
@@ -415,7 +415,7 @@ def _plain_kv_attention(s):
 
 def exact(case, seed):
     s = prepare(case, seed)
-    return {"norm_quant": _exact_norm_quant, "int8_gemm": _exact_int8_gemm, "kv_append": _exact_kv_append,
+    return {"norm_quant": _exact_norm_quant, "byte_gemm": _exact_byte_gemm, "kv_append": _exact_kv_append,
             "kv_attention": _exact_kv_attention}[case["op"]](s)
 
 
@@ -440,7 +440,7 @@ def _exact_norm_quant(s):
     return torch.cat(values), torch.cat(scales), torch.cat(sums) if s["residual"] is not None else None
 
 
-def _exact_int8_gemm(s):
+def _exact_byte_gemm(s):
     # whole numbers below 2^53 are exact
     zeros = torch.zeros(s["w"].shape[0], dtype=torch.float64, device=s["w"].device) if s["zeros"] is None \
         else s["zeros"].to(torch.float64)
