@@ -19,11 +19,18 @@
  *
  *   gptq_dequant_gemm        y = x W^T for a few input rows, read straight from the packed codes
  *   gptq_lora_gemm           low-rank adapters of many requests added beside it
+ *   gptq_byte_gemm           y = x W^T with 8-bit inputs and weights, scaled per token and per output
  *
  * and the attention half of a decoder block:
  *
  *   gptq_norm_rotate         per-head norm of queries and keys with the position rotation
  *   gptq_attention           attention over packed sequences: shared heads, masks, capped scores
+ *
+ * and serving in 8 bits around them:
+ *
+ *   gptq_norm_quant          residual addition and norm of whole rows, as int8 rows with a scale each
+ *   gptq_kv_append           keys (rotated) and values into a paged int8 cache
+ *   gptq_kv_attention        attention over that cache
  *
  * Sources (web pages on GPTQ): the GPTQ tools page at ozercemkelahmet.com ("How it works",
  * Steps 3-8, "Optional refinements", "A minimal Python sketch", "Memory arithmetic"); "GPTQ
@@ -456,6 +463,175 @@ gptq_status_t gptq_attention(const gptq_attention_t *a, const void *q, const voi
 
 /* Workspace bytes with which gptq_attention splits key ranges; 0 when it would not (or for invalid arguments). */
 size_t gptq_attention_workspace_bytes(const gptq_attention_t *a);
+
+/* Sizes, pitches and types of gptq_norm_quant. */
+typedef struct {
+  int64_t n;        /* rows (tokens), >= 0 (0: nothing is queued)                                 */
+  int64_t d;        /* columns, 1..65536                                                          */
+  int64_t x_ld, r_ld, sum_ld, y_ld, q_ld;   /* row pitches in elements, >= d (of arrays that are passed) */
+  double eps;       /* >= 0                                                                       */
+  int32_t dtype;    /* of x, residual, sum and y: GPTQ_F32, GPTQ_F16 or GPTQ_BF16                 */
+  int32_t w_dtype;  /* of weight                                                                  */
+} gptq_norm_quant_t;
+
+/*
+ * Residual addition, root-mean-square norm and 8-bit rows in one pass, the inputs of gptq_byte_gemm. For each
+ * row: h = x + residual (an fp32 sum rounded to dtype), y = weight * h / sqrt(mean(h^2) + eps), and with
+ * a = max |y|: scales = a / 127 and q = y * 127 / a, to the nearest whole number, ties to even.
+ *
+ *   x         device array [n x x_ld] of dtype.
+ *   residual  device array [n x r_ld] of dtype, or NULL: h = x.
+ *   weight    device array of w_dtype [d], or NULL: ones.
+ *   sum       device array [n x sum_ld] of dtype, output: h; or NULL. It may be x or residual itself with the
+ *             same pitch (in place), or be apart from both.
+ *   y         device array [n x y_ld] of dtype, output: the normed rows, or NULL.
+ *   q         device int8[n x q_ld], output, in [-127, 127]; or NULL (then scales is not used and y must be given).
+ *   scales    device float[n], output.
+ * Outputs must be apart from every other array (sum as above); anything else is GPTQ_EINVAL. The row's sum of
+ * squares, its largest element and the codes' rounding are computed in 64 bits: q is the rounding of the exact
+ * quotient of h's and weight's products, whatever their size, and scales and y are rounded once. A row of zeros
+ * has a scale and codes of zero. A row whose y is not finite everywhere (an infinity or NaN in h or weight) has a
+ * scale of NaN and codes of zero, so that products with it are NaN.
+ * d > 65536 is GPTQ_EUNSUPPORTED. Launches on `stream` alone; the call may be captured in a graph.
+ */
+gptq_status_t gptq_norm_quant(const gptq_norm_quant_t *a, const void *x, const void *residual, const void *weight,
+                              void *sum, void *y, int8_t *q, float *scales, void *stream);
+
+/*
+ * Product of 8-bit rows with 8-bit weights:
+ *   y[i, r] = x_scales[i] * w_scales[r] * sum_k x[i, k] * (w[r, k] - zeros[r]).
+ * The weights are signed bytes (zeros NULL), or the unsigned codes of a layer quantized with bits = 8 and one
+ * group per row: gptq_quantize_layer's codes, or gptq_pack's words of them (the same bytes), with its scales and
+ * zeros.
+ *
+ *   x         device int8[m x ld_x], one row per token; ld_x >= d. Not modified.
+ *   m         input rows, >= 0 (0: nothing is queued).
+ *   x_scales  device float[m] (gptq_norm_quant's), or NULL: 1.
+ *   w         device bytes [rows x ld_w], ld_w >= d: int8 with zeros NULL, else uint8. Not modified.
+ *   w_scales  device float[rows], or NULL: 1.
+ *   zeros     device int32[rows], any values, or NULL.
+ *   rows      outputs, 0..2^24 (0: nothing is queued); d input features, 1..131071 (beyond it a 32-bit sum could
+ *             overflow: GPTQ_EUNSUPPORTED).
+ *   y         device array [m x ld_y] of y_dtype (GPTQ_F32, GPTQ_F16 or GPTQ_BF16), output, ld_y >= rows; apart
+ *             from the other arrays.
+ *   work      device workspace of work_bytes bytes (16-byte aligned), or NULL. With at least
+ *             gptq_byte_gemm_workspace_bytes(m, rows, d) bytes, long sums are split across workgroups where there
+ *             are few outputs; with less they are not. The result is the same bit for bit. Not shared with a
+ *             concurrent call, two captured graphs included.
+ * Sums are exact whole numbers; the result is rounded to fp32 four times at most (the sum, each product with a
+ * scale, the difference for zeros is exact) and once to y_dtype. 16-byte accesses are used where pointers and
+ * pitches allow them. Launches on `stream` alone; the call may be captured in a graph.
+ */
+gptq_status_t gptq_byte_gemm(const int8_t *x, int64_t m, int64_t ld_x, const float *x_scales, const void *w,
+                             int64_t ld_w, const float *w_scales, const int32_t *zeros, int64_t rows, int64_t d,
+                             void *y, int32_t y_dtype, int64_t ld_y, void *work, size_t work_bytes, void *stream);
+
+/* Workspace bytes with which gptq_byte_gemm splits its sums; 0 when it would not (or for invalid arguments). */
+size_t gptq_byte_gemm_workspace_bytes(int64_t m, int64_t rows, int64_t d);
+
+/*
+ * A paged cache of keys and values in 8 bits. A page holds page_size tokens; a key or value stands for its code
+ * times the scale of its page and head. Code (page p, slot t, head h, column c) of keys is at
+ * p * k_page + t * k_tok + h * k_hp + c of k (values the same), and the scale at p * kv_heads + h of k_scales.
+ */
+typedef struct {
+  int8_t *k, *v;                    /* device                                                     */
+  float *k_scales, *v_scales;       /* device float[pages * kv_heads]                             */
+  int64_t pages;                    /* 0..2^31 - 1                                                */
+  int64_t k_page, k_tok, k_hp;      /* pitches of pages, tokens and heads, in bytes               */
+  int64_t v_page, v_tok, v_hp;
+  int32_t page_size;                /* a multiple of 16, 16..1024; others are GPTQ_EUNSUPPORTED   */
+  int32_t kv_heads;                 /* 1..65535                                                   */
+  int32_t head_dim;                 /* 1..1024                                                    */
+  int32_t max_pages;                /* pages of a sequence, the pitch of page tables, 1..2^26     */
+} gptq_kv_cache_t;
+
+/* Sizes, strides and settings of gptq_kv_append; pitches and rotation as in gptq_norm_rotate_t. */
+typedef struct {
+  int64_t seqs;        /* sequences, >= 0 (0: nothing is queued)                                  */
+  int64_t n;           /* rows of k and v, 0..2^30                                                */
+  int64_t k_ld, k_hp, v_ld, v_hp;
+  int32_t dtype;       /* of k and v: GPTQ_F32, GPTQ_F16 or GPTQ_BF16                             */
+  int32_t rotary_dim;  /* rotated columns of each key: even, 0..head_dim (0: none)                */
+  int32_t interleaved;
+  int32_t axes;        /* rows of positions, 1..64                                                */
+} gptq_kv_append_t;
+
+/*
+ * Appends keys and values to the cache. Sequence s holds rows [start[s], start[s + 1]) of k and v, and past[s]
+ * tokens in the cache already: its row i becomes token t = past[s] + i, slot t % page_size of page
+ * table[s * max_pages + t / page_size]. Keys are rotated on the way, as gptq_norm_rotate does without its norm.
+ *
+ * A page's scale of a head is m / 127 in fp32, m the largest magnitude it has held, as far as this call knows
+ * it: where the page holds earlier tokens of the sequence, the scale is the larger of theirs and of the new
+ * tokens'. When it grows, the earlier codes c become the nearest whole number to c * old / new. A new code is the
+ * nearest whole number to the value over the scale, ties to even, in [-127, 127]. A page whose first slot is
+ * written takes its scale from the new tokens alone. New tokens that hold an infinity or NaN make their page's
+ * scale of that head NaN, until its first slot is written again.
+ *
+ *   cache            its arrays are modified in place: slots of the new tokens, earlier slots of their pages
+ *                    where a scale grows, and scales of these pages. Nothing else is written.
+ *   k, v             device arrays [n x kv_heads x head_dim] of dtype. Not modified.
+ *   start            device int32[seqs + 1], ascending, or NULL: seqs equal ranges (n a multiple of seqs). Values are
+ *                    clamped into [0, n].
+ *   past             device int32[seqs], clamped to [0, max_pages * page_size].
+ *   table            device int32[seqs * max_pages]. A page outside [0, pages) and tokens past the table's end are
+ *                    left out. A page that this call writes must belong to one sequence and stand in its table
+ *                    once (pages before, a shared prefix, may belong to several).
+ *   positions        device int32[axes * n], or NULL: t (with axes = 1).
+ *   inv_freq, pair_axis  as in gptq_norm_rotate; not used with rotary_dim = 0.
+ * Rotation and rounding are computed in 64 bits. Launches on `stream` alone; the call may be captured in a graph.
+ */
+gptq_status_t gptq_kv_append(const gptq_kv_append_t *a, const gptq_kv_cache_t *cache, const void *k, const void *v,
+                             const int32_t *start, const int32_t *past, const int32_t *table,
+                             const int32_t *positions, const float *inv_freq, const int32_t *pair_axis, void *stream);
+
+/* Sizes, strides and settings of gptq_kv_attention; pitches as in gptq_norm_rotate_t. */
+typedef struct {
+  int64_t seqs;       /* sequences, >= 0 (0: nothing is queued)                                   */
+  int64_t n_q;        /* rows of q and out, 0..2^30                                               */
+  int64_t q_ld, q_hp, out_ld, out_hp;
+  double scale;       /* score scale, finite in fp32                                              */
+  double softcap;     /* c >= 1e-37: scores become c tanh(score / c); 0: no cap                   */
+  int32_t dtype;      /* of q and out: GPTQ_F32, GPTQ_F16 or GPTQ_BF16                            */
+  int32_t q_heads;    /* 1..65535, a multiple of the cache's kv_heads                             */
+  int32_t causal;     /* 1: a query sees the keys up to its own position; 0: all of its sequence's */
+  int32_t window;     /* w > 0: and of those only keys with position p - j < w; 0: no window      */
+} gptq_kv_attention_t;
+
+/*
+ * Softmax attention over the paged cache: gptq_attention's formula with keys and values read through page tables.
+ * Sequence s holds rows [q_start[s], q_start[s + 1]) of q, lq of them, and lens[s] tokens in the cache (the new
+ * ones included: append first). Query i has position p = i + lens[s] - lq.
+ *   score = scale * q . k_j, capped (softcap), minus slopes[head] * |p - j|
+ *   seen  = (j <= p or causal = 0) and (p - j < window or window = 0) and the page of j is in [0, pages)
+ *   out   = sum of v_j exp(score) / sum of exp(score) over the keys that are seen
+ * A query that sees no key gets zeros. Rows of out that belong to no sequence are left as they were. Slots behind a
+ * sequence's last token and pages it does not name take no part, whatever they and their scales hold.
+ *
+ *   q         device array [n_q x q_heads x head_dim] of dtype, not modified.
+ *   q_start   device int32[seqs + 1], ascending, or NULL: seqs equal ranges (n_q a multiple of seqs). Values are
+ *             clamped into [0, n_q].
+ *   lens      device int32[seqs], clamped to [0, max_pages * page_size].
+ *   table     device int32[seqs * max_pages]; sequences may share pages.
+ *   slopes    device float[q_heads], or NULL.
+ *   out       device array, output; apart from q, its heads and tokens from each other.
+ *   work      device workspace of work_bytes bytes (16-byte aligned), or NULL. With at least
+ *             gptq_kv_attention_workspace_bytes(a, cache) bytes, long key ranges are split across workgroups
+ *             where there are few queries; with less they are not. Not shared with a concurrent call, two
+ *             captured graphs included.
+ * Codes are exact in the matrix cores' 16-bit type. Scores, the softmax's maximum and sum and the output's sums are
+ * fp32. With fp16 and bf16 each query is used as it is and each probability (times its value's scale) is rounded
+ * once to 11 bits before it weighs a code, which moves the output by at most half a step (2^-11) of sum p |v|;
+ * with fp32 both are kept to 22 bits. Results do not
+ * depend on scheduling. Launches on `stream` alone; the call may be captured in a graph.
+ */
+gptq_status_t gptq_kv_attention(const gptq_kv_attention_t *a, const gptq_kv_cache_t *cache, const void *q,
+                                const int32_t *q_start, const int32_t *lens, const int32_t *table,
+                                const float *slopes, void *out, void *work, size_t work_bytes, void *stream);
+
+/* Workspace bytes with which gptq_kv_attention splits key ranges; 0 when it would not (or for invalid arguments). */
+size_t gptq_kv_attention_workspace_bytes(const gptq_kv_attention_t *a, const gptq_kv_cache_t *cache);
 
 /*
  * One pre-norm decoder block for gptq_quantize_block. The pages fix the order in which a block's

@@ -1,5 +1,6 @@
 """GPTQ layer-wise weight quantization solver for AMD Instinct MI355X (gfx950), with the operators of a decoder
-layer beside its stored layers (norm with rotation, attention, adapters).
+layer beside its stored layers (norm with rotation, attention, adapters) and of serving in 8 bits (norm with int8
+rows, 8-bit product, paged cache).
 
 The solver's steps are HIP kernels behind a C ABI (include/gptq.h, libgptq.so); this package is its
 Python binding. Build the library with `python -m post_weight_quantization_20_amd.build`.
@@ -11,6 +12,14 @@ from .attention import (  # noqa: F401
     gptq_lora_gemm,
     gptq_lora_workspace_bytes,
     gptq_norm_rotate,
+)
+from .serving import (  # noqa: F401
+    gptq_byte_gemm,
+    gptq_byte_gemm_workspace_bytes,
+    gptq_kv_append,
+    gptq_kv_attention,
+    gptq_kv_attention_workspace_bytes,
+    gptq_norm_quant,
 )
 from .solver import (  # noqa: F401
     BLOCK_LAYERS,

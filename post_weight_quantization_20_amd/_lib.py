@@ -59,6 +59,28 @@ class gptq_block_attn_t(ctypes.Structure):
                 [(f, c_int32) for f in ("qk_norm", "w_dtype", "rotary_dim", "interleaved", "axes", "causal")])
 
 
+class gptq_norm_quant_t(ctypes.Structure):
+    _fields_ = ([(f, c_int64) for f in ("n", "d", "x_ld", "r_ld", "sum_ld", "y_ld", "q_ld")] + [("eps", c_double)] +
+                [(f, c_int32) for f in ("dtype", "w_dtype")])
+
+
+class gptq_kv_cache_t(ctypes.Structure):
+    _fields_ = ([(f, c_void_p) for f in ("k", "v", "k_scales", "v_scales")] +
+                [(f, c_int64) for f in ("pages", "k_page", "k_tok", "k_hp", "v_page", "v_tok", "v_hp")] +
+                [(f, c_int32) for f in ("page_size", "kv_heads", "head_dim", "max_pages")])
+
+
+class gptq_kv_append_t(ctypes.Structure):
+    _fields_ = ([(f, c_int64) for f in ("seqs", "n", "k_ld", "k_hp", "v_ld", "v_hp")] +
+                [(f, c_int32) for f in ("dtype", "rotary_dim", "interleaved", "axes")])
+
+
+class gptq_kv_attention_t(ctypes.Structure):
+    _fields_ = ([(f, c_int64) for f in ("seqs", "n_q", "q_ld", "q_hp", "out_ld", "out_hp")] +
+                [("scale", c_double), ("softcap", c_double)] +
+                [(f, c_int32) for f in ("dtype", "q_heads", "causal", "window")])
+
+
 # name -> (restype, argtypes), mirroring include/gptq.h
 SIGNATURES = {
     "gptq_hessian_accumulate": (c_int32, [c_void_p, c_int64, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_size_t,
@@ -89,6 +111,15 @@ SIGNATURES = {
     "gptq_norm_rotate": (c_int32, [ctypes.POINTER(gptq_norm_rotate_t)] + [c_void_p] * 10),
     "gptq_attention": (c_int32, [ctypes.POINTER(gptq_attention_t)] + [c_void_p] * 11 + [c_size_t, c_void_p]),
     "gptq_attention_workspace_bytes": (c_size_t, [ctypes.POINTER(gptq_attention_t)]),
+    "gptq_norm_quant": (c_int32, [ctypes.POINTER(gptq_norm_quant_t)] + [c_void_p] * 8),
+    "gptq_byte_gemm": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64,
+                                 c_int64, c_void_p, c_int32, c_int64, c_void_p, c_size_t, c_void_p]),
+    "gptq_byte_gemm_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "gptq_kv_append": (c_int32, [ctypes.POINTER(gptq_kv_append_t), ctypes.POINTER(gptq_kv_cache_t)] + [c_void_p] * 9),
+    "gptq_kv_attention": (c_int32, [ctypes.POINTER(gptq_kv_attention_t), ctypes.POINTER(gptq_kv_cache_t)] +
+                          [c_void_p] * 7 + [c_size_t, c_void_p]),
+    "gptq_kv_attention_workspace_bytes": (c_size_t, [ctypes.POINTER(gptq_kv_attention_t),
+                                                     ctypes.POINTER(gptq_kv_cache_t)]),
     "gptq_block_workspace_bytes": (c_size_t, [ctypes.POINTER(gptq_block_shape_t), ctypes.POINTER(gptq_params_t)]),
     "gptq_quantize_block": (c_int32, [ctypes.POINTER(gptq_block_shape_t), c_void_p, c_int32,
                                       ctypes.POINTER(gptq_params_t), c_int32, ctypes.POINTER(gptq_block_layer_t),

@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgptq.so")
 SOURCES = ["abi.hip", "runtime.hip", "gemm_f32.hip", "hessian.hip", "factor.hip", "quant.hip", "dequant.hip", "block.hip",
-           "gemm_f16.hip", "noalloc.hip", "rotate.hip", "attention.hip", "lora.hip"]
+           "gemm_f16.hip", "noalloc.hip", "rotate.hip", "attention.hip", "lora.hip", "norm_quant.hip", "byte_gemm.hip",
+           "kv_cache.hip", "kv_attention.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -405,6 +405,213 @@ gptq_status_t gptq_attention(const gptq_attention_t* a, const void* q, const voi
 
 namespace {
 
+// Address ranges without a common byte (an empty one has none).
+bool ranges_apart(const void* a, int64_t na, const void* b, int64_t nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return !x || !y || na <= 0 || nb <= 0 || x + na <= y || y + nb <= x;
+}
+
+gptq_status_t norm_quant_ok(const gptq_norm_quant_t* a) {
+  if (!a || !dtype_ok(a->dtype) || !dtype_ok(a->w_dtype) || a->n < 0 || a->n >= kMaxDim || a->d < 1 || a->d > kMaxDim)
+    return GPTQ_EINVAL;
+  if (!std::isfinite(a->eps) || a->eps < 0.0) return GPTQ_EINVAL;
+  return a->d > 65536 ? GPTQ_EUNSUPPORTED : GPTQ_OK;
+}
+
+}  // namespace
+
+gptq_status_t gptq_norm_quant(const gptq_norm_quant_t* a, const void* x, const void* residual, const void* weight,
+                              void* sum, void* y, int8_t* q, float* scales, void* stream) {
+  const gptq_status_t st = norm_quant_ok(a);
+  if (st != GPTQ_OK) return st;
+  const int64_t esz = elem_bytes(a->dtype), n = a->n, d = a->d;
+  const Tensor3 tx{x, n, 1, d, a->x_ld, 0, esz}, tr{residual, n, 1, d, a->r_ld, 0, esz},
+      tw{weight, 1, 1, d, d, 0, elem_bytes(a->w_dtype)}, ts{sum, n, 1, d, a->sum_ld, 0, esz},
+      ty{y, n, 1, d, a->y_ld, 0, esz}, tq{q, n, 1, d, a->q_ld, 0, 1}, tc{q ? scales : nullptr, n, 1, 1, 1, 0, 4};
+  for (const Tensor3* t : {&tx, &tr, &ts, &ty, &tq})
+    if ((t->p || t == &tx) && (t->ld < d || !pitches_ok(*t))) return GPTQ_EINVAL;
+  if (n == 0) return GPTQ_OK;
+  if (!x || (!q && !y) || (q && !scales)) return GPTQ_EINVAL;
+  const Tensor3* out[] = {&ts, &ty, &tq, &tc};
+  for (int i = 0; i < 4; ++i) {
+    if (!out[i]->p) continue;
+    for (const Tensor3* in : {&tx, &tr, &tw})
+      if (in->p && !(i == 0 && in != &tw && same(ts, *in)) && !apart(*out[i], *in)) return GPTQ_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (out[j]->p && !apart(*out[i], *out[j])) return GPTQ_EINVAL;
+  }
+  return hip_status(gptq::norm_quant(*a, x, residual, weight, sum, y, q, scales, static_cast<hipStream_t>(stream)));
+}
+
+static constexpr int64_t kMaxInt8Sum = 131071;   // d * 128 * 128 < 2^31
+
+size_t gptq_byte_gemm_workspace_bytes(int64_t m, int64_t rows, int64_t d) {
+  if (m <= 0 || m > kMaxDim || rows <= 0 || rows > kMaxRows || d < 1 || d > kMaxInt8Sum) return 0;
+  return gptq::byte_gemm_workspace_bytes(m, rows, d);
+}
+
+gptq_status_t gptq_byte_gemm(const int8_t* x, int64_t m, int64_t ld_x, const float* x_scales, const void* w,
+                             int64_t ld_w, const float* w_scales, const int32_t* zeros, int64_t rows, int64_t d,
+                             void* y, int32_t y_dtype, int64_t ld_y, void* work, size_t work_bytes, void* stream) {
+  if (m < 0 || m > kMaxDim || rows < 0 || rows > kMaxRows || d < 1 || d > kMaxDim || !dtype_ok(y_dtype))
+    return GPTQ_EINVAL;
+  if (ld_x < d || ld_w < d || ld_y < rows) return GPTQ_EINVAL;
+  if (d > kMaxInt8Sum) return GPTQ_EUNSUPPORTED;
+  const Tensor3 tx{x, m, 1, d, ld_x, 0, 1}, tw{w, rows, 1, d, ld_w, 0, 1}, ty{y, m, 1, rows, ld_y, 0, elem_bytes(y_dtype)};
+  if (!pitches_ok(tx) || !pitches_ok(tw) || !pitches_ok(ty)) return GPTQ_EINVAL;
+  if (m == 0 || rows == 0) return GPTQ_OK;
+  if (!x || !w || !y) return GPTQ_EINVAL;
+  if (!apart(ty, tx) || !apart(ty, tw) || !ranges_apart(y, ty.bytes(), x_scales, 4 * m) ||
+      !ranges_apart(y, ty.bytes(), w_scales, 4 * rows) || !ranges_apart(y, ty.bytes(), zeros, 4 * rows))
+    return GPTQ_EINVAL;
+  if (reinterpret_cast<uintptr_t>(work) % 16 != 0) return GPTQ_EINVAL;
+  return hip_status(gptq::byte_gemm(x, m, ld_x, x_scales, w, ld_w, w_scales, zeros, rows, d, y, y_dtype, ld_y, work,
+                                    work ? work_bytes : 0, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+// One level of a cache's codes: so many blocks of one pitch.
+struct Level {
+  int64_t count, pitch;
+};
+
+// The codes of keys or of values, levels by ascending pitch.
+struct Codes {
+  const int8_t* p;
+  int64_t width;
+  Level level[3];
+  Codes(const int8_t* p, int64_t width, Level a, Level b, Level c) : p(p), width(width), level{a, b, c} {
+    std::sort(level, level + 3, [](const Level& x, const Level& y) { return x.pitch < y.pitch; });
+  }
+  // bytes that the blocks below level i span
+  int64_t extent(int i) const {
+    int64_t e = width;
+    for (int l = 0; l < i; ++l) e += (level[l].count - 1) * level[l].pitch;
+    return e;
+  }
+  static Codes keys(const gptq_kv_cache_t& c) {
+    return Codes(c.k, c.head_dim, {c.pages, c.k_page}, {c.page_size, c.k_tok}, {c.kv_heads, c.k_hp});
+  }
+  static Codes values(const gptq_kv_cache_t& c) {
+    return Codes(c.v, c.head_dim, {c.pages, c.v_page}, {c.page_size, c.v_tok}, {c.kv_heads, c.v_hp});
+  }
+  bool pitches_ok() const {
+    constexpr int64_t most = (int64_t)1 << 56;
+    __int128 span = width;
+    for (const Level& l : level) {
+      if (l.pitch < 0 || l.pitch > most) return false;
+      span += (__int128)l.count * l.pitch;
+    }
+    return span <= most;
+  }
+  bool elements_apart() const {
+    for (int i = 0; i < 3; ++i)
+      if (level[i].count > 1 && level[i].pitch < extent(i)) return false;
+    return true;
+  }
+};
+
+// Two arrays of codes that share no byte: address ranges apart, or the same pitches and every block of one in a
+// gap between blocks of the other.
+bool codes_apart(const Codes& a, const Codes& b) {
+  if (ranges_apart(a.p, a.extent(3), b.p, b.extent(3))) return true;
+  for (int i = 0; i < 3; ++i)
+    if (a.level[i].pitch != b.level[i].pitch || a.level[i].count != b.level[i].count) return false;
+  const int64_t diff = a.p < b.p ? b.p - a.p : a.p - b.p;
+  for (int i = 0; i < 3; ++i)
+    if (diff >= a.extent(i) && diff + a.extent(i) <= a.level[i].pitch) return true;
+  return false;
+}
+
+gptq_status_t cache_ok(const gptq_kv_cache_t* c) {
+  if (!c || c->pages < 0 || c->pages >= kMaxDim || c->page_size < 1 || c->kv_heads < 1 || c->kv_heads > 65535)
+    return GPTQ_EINVAL;
+  if (c->head_dim < 1 || c->head_dim > 1024 || c->max_pages < 1 || c->max_pages > (1 << 26)) return GPTQ_EINVAL;
+  if (!Codes::keys(*c).pitches_ok() || !Codes::values(*c).pitches_ok()) return GPTQ_EINVAL;
+  if (c->pages > 0 && (!c->k || !c->v || !c->k_scales || !c->v_scales)) return GPTQ_EINVAL;
+  return c->page_size % 16 != 0 || c->page_size > 1024 ? GPTQ_EUNSUPPORTED : GPTQ_OK;
+}
+
+gptq_status_t kv_attention_ok(const gptq_kv_attention_t* a, const gptq_kv_cache_t* c) {
+  const gptq_status_t st = cache_ok(c);
+  if (st == GPTQ_EINVAL || !a || !dtype_ok(a->dtype) || a->seqs < 0 || a->seqs >= kMaxDim) return GPTQ_EINVAL;
+  if (a->n_q < 0 || a->n_q > kMaxDim / 2) return GPTQ_EINVAL;
+  if (a->q_heads < 1 || a->q_heads > 65535 || a->q_heads % c->kv_heads != 0) return GPTQ_EINVAL;
+  if ((a->causal != 0 && a->causal != 1) || a->window < 0) return GPTQ_EINVAL;
+  const float scale = (float)a->scale, cap = (float)a->softcap;
+  if (!std::isfinite(scale) || !std::isfinite(cap) || a->softcap < 0.0 || (a->softcap > 0.0 && cap < 1e-37f))
+    return GPTQ_EINVAL;
+  return st;
+}
+
+}  // namespace
+
+gptq_status_t gptq_kv_append(const gptq_kv_append_t* a, const gptq_kv_cache_t* cache, const void* k, const void* v,
+                             const int32_t* start, const int32_t* past, const int32_t* table,
+                             const int32_t* positions, const float* inv_freq, const int32_t* pair_axis, void* stream) {
+  const gptq_status_t st = cache_ok(cache);
+  if (st == GPTQ_EINVAL || !a || !dtype_ok(a->dtype) || a->seqs < 0 || a->seqs >= kMaxDim || a->n < 0 ||
+      a->n > kMaxDim / 2)
+    return GPTQ_EINVAL;
+  if (a->rotary_dim < 0 || a->rotary_dim > cache->head_dim || a->rotary_dim % 2 ||
+      (a->interleaved != 0 && a->interleaved != 1) || a->axes < 1 || a->axes > 64)
+    return GPTQ_EINVAL;
+  if (st != GPTQ_OK) return st;
+  const int64_t esz = elem_bytes(a->dtype), heads = cache->kv_heads, dh = cache->head_dim;
+  const Tensor3 k3{k, a->n, heads, dh, a->k_ld, a->k_hp, esz}, v3{v, a->n, heads, dh, a->v_ld, a->v_hp, esz};
+  if (!pitches_ok(k3) || !pitches_ok(v3)) return GPTQ_EINVAL;
+  if (a->seqs == 0 || a->n == 0 || cache->pages == 0) return GPTQ_OK;
+  if (!start && a->n % a->seqs != 0) return GPTQ_EINVAL;
+  if (!k || !v || !past || !table) return GPTQ_EINVAL;
+  if (a->rotary_dim && (!inv_freq || (!positions && a->axes != 1))) return GPTQ_EINVAL;
+  const Codes kc = Codes::keys(*cache), vc = Codes::values(*cache);
+  const int64_t sb = 4 * cache->pages * heads;
+  if (!kc.elements_apart() || !vc.elements_apart() || !codes_apart(kc, vc)) return GPTQ_EINVAL;
+  if (!ranges_apart(cache->k_scales, sb, cache->v_scales, sb)) return GPTQ_EINVAL;
+  for (const Codes* c : {&kc, &vc})
+    for (const Tensor3* t : {&k3, &v3})
+      if (!ranges_apart(c->p, c->extent(3), t->p, t->bytes())) return GPTQ_EINVAL;
+  for (const float* sc : {cache->k_scales, cache->v_scales}) {
+    for (const Codes* c : {&kc, &vc})
+      if (!ranges_apart(sc, sb, c->p, c->extent(3))) return GPTQ_EINVAL;
+    for (const Tensor3* t : {&k3, &v3})
+      if (!ranges_apart(sc, sb, t->p, t->bytes())) return GPTQ_EINVAL;
+  }
+  return hip_status(gptq::kv_append(*a, *cache, k, v, start, past, table, positions, inv_freq, pair_axis,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+size_t gptq_kv_attention_workspace_bytes(const gptq_kv_attention_t* a, const gptq_kv_cache_t* cache) {
+  if (kv_attention_ok(a, cache) != GPTQ_OK || a->seqs == 0 || a->n_q == 0) return 0;
+  return gptq::kv_attention_workspace_bytes(*a, *cache);
+}
+
+gptq_status_t gptq_kv_attention(const gptq_kv_attention_t* a, const gptq_kv_cache_t* cache, const void* q,
+                                const int32_t* q_start, const int32_t* lens, const int32_t* table,
+                                const float* slopes, void* out, void* work, size_t work_bytes, void* stream) {
+  const gptq_status_t st = kv_attention_ok(a, cache);
+  if (st != GPTQ_OK) return st;
+  const int64_t esz = elem_bytes(a->dtype), dh = cache->head_dim, sb = 4 * cache->pages * cache->kv_heads;
+  const Tensor3 q3{q, a->n_q, a->q_heads, dh, a->q_ld, a->q_hp, esz}, o3{out, a->n_q, a->q_heads, dh, a->out_ld, a->out_hp, esz};
+  if (!pitches_ok(q3) || !pitches_ok(o3)) return GPTQ_EINVAL;
+  if (a->seqs == 0 || a->n_q == 0) return GPTQ_OK;
+  if (!q_start && a->n_q % a->seqs != 0) return GPTQ_EINVAL;
+  if (!q || !out || !lens || !table) return GPTQ_EINVAL;
+  if (!elements_apart(o3) || !apart(o3, q3)) return GPTQ_EINVAL;
+  if (cache->pages > 0) {
+    const Codes kc = Codes::keys(*cache), vc = Codes::values(*cache);
+    if (!ranges_apart(out, o3.bytes(), kc.p, kc.extent(3)) || !ranges_apart(out, o3.bytes(), vc.p, vc.extent(3)) ||
+        !ranges_apart(out, o3.bytes(), cache->k_scales, sb) || !ranges_apart(out, o3.bytes(), cache->v_scales, sb))
+      return GPTQ_EINVAL;
+  }
+  if (reinterpret_cast<uintptr_t>(work) % 16 != 0) return GPTQ_EINVAL;
+  return hip_status(gptq::kv_attention(*a, *cache, q, q_start, lens, table, slopes, out, work, work ? work_bytes : 0,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
 bool block_shape_ok(const gptq_block_shape_t* sh) {
   if (!sh) return false;
   if (sh->hidden < 8 || sh->hidden > kMaxDim || sh->inter < 8 || sh->inter > kMaxDim) return false;

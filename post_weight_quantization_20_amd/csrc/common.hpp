@@ -210,6 +210,25 @@ hipError_t attention(const gptq_attention_t& t, const void* q, const void* k, co
                      const int32_t* kv_start, const float* slopes, const int32_t* q_doc, const int32_t* kv_doc,
                      const int32_t* prefix, void* out, void* work, size_t work_bytes, hipStream_t s);
 
+// Residual addition, norm and int8 rows (norm_quant.hip).
+hipError_t norm_quant(const gptq_norm_quant_t& t, const void* x, const void* r, const void* w, void* sum, void* y,
+                      int8_t* q, float* scales, hipStream_t s);
+
+// y = xs ws (x (w - z)^T) for int8 rows and 8-bit weights (byte_gemm.hip). z may be null: signed weights.
+size_t byte_gemm_workspace_bytes(int64_t m, int64_t rows, int64_t d);
+hipError_t byte_gemm(const int8_t* x, int64_t m, int64_t ld_x, const float* xs, const void* w, int64_t ld_w,
+                     const float* ws, const int32_t* z, int64_t rows, int64_t d, void* y, int y_dtype, int64_t ld_y,
+                     void* work, size_t work_bytes, hipStream_t s);
+
+// Keys and values into a paged 8-bit cache (kv_cache.hip), and attention over it (kv_attention.hip).
+hipError_t kv_append(const gptq_kv_append_t& t, const gptq_kv_cache_t& c, const void* k, const void* v,
+                     const int32_t* start, const int32_t* past, const int32_t* table, const int32_t* pos,
+                     const float* inv_freq, const int32_t* pair_axis, hipStream_t s);
+size_t kv_attention_workspace_bytes(const gptq_kv_attention_t& t, const gptq_kv_cache_t& c);
+hipError_t kv_attention(const gptq_kv_attention_t& t, const gptq_kv_cache_t& c, const void* q, const int32_t* q_start,
+                        const int32_t* lens, const int32_t* table, const float* slopes, void* out, void* work,
+                        size_t work_bytes, hipStream_t s);
+
 // ------------------------------------------------------------------ fp16 products (gemm_f16.hip)
 // C[M x N] = alpha A B^T + beta C with A [M x K], B [N x K] fp16 row-major (k contiguous); K a
 // multiple of 64, lda and ldb multiples of 8, A and B 16-byte aligned. beta == 0 never reads C.

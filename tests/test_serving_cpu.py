@@ -1,0 +1,256 @@
+"""Refusals of gptq_norm_quant, gptq_byte_gemm, gptq_kv_append and gptq_kv_attention (C ABI and binding), and pins of
+their float64 oracle (CPU only: no call here launches a kernel)."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import serve_ref
+
+FAKE = 0x1000000          # never dereferenced: every call below is rejected or has nothing to do
+EINVAL, EUNSUPPORTED = -1, -3
+
+
+def _lib():
+    from test_abi_cpu import _lib as load
+    return load()
+
+
+# -------------------------------------------------------------------------------------- norm_quant
+
+def _norm(over=None, **kw):
+    L = _lib()
+    d = dict(n=4, d=64, x_ld=64, r_ld=64, sum_ld=64, y_ld=64, q_ld=64, eps=1e-6, dtype=1, w_dtype=0)
+    d.update(kw)
+    p = dict(x=FAKE, residual=2 * FAKE, weight=3 * FAKE, sum=4 * FAKE, y=5 * FAKE, q=6 * FAKE, scales=7 * FAKE)
+    p.update(over or {})
+    a = L.gptq_norm_quant_t(**d)
+    return L.lib().gptq_norm_quant(ctypes.byref(a), *[ctypes.c_void_p(v) for v in p.values()], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=-1), dict(n=1 << 31), dict(d=0), dict(d=-5), dict(dtype=3), dict(w_dtype=-1), dict(eps=-1.0),
+    dict(eps=float("inf")), dict(eps=float("nan")), dict(x_ld=63), dict(r_ld=1), dict(sum_ld=63), dict(y_ld=0),
+    dict(q_ld=63), dict(x_ld=1 << 58)], ids=str)
+def test_norm_quant_rejects_settings(kw):
+    assert _norm(**kw) == EINVAL
+
+
+def test_norm_quant_widest_row():
+    assert _norm(d=65537, x_ld=65537, r_ld=65537, sum_ld=65537, y_ld=65537, q_ld=65537) == EUNSUPPORTED
+
+
+@pytest.mark.parametrize("over", [
+    dict(x=0), dict(scales=0), dict(q=0, y=0), dict(sum=FAKE + 2), dict(y=FAKE), dict(y=2 * FAKE), dict(q=FAKE + 8),
+    dict(sum=5 * FAKE), dict(scales=6 * FAKE), dict(scales=3 * FAKE), dict(y=3 * FAKE + 4), dict(q=4 * FAKE),
+    dict(sum=3 * FAKE)], ids=str)
+def test_norm_quant_rejects_pointers(over):
+    assert _norm(over) == EINVAL
+
+
+def test_norm_quant_in_place_needs_one_pitch():
+    assert _norm(dict(sum=FAKE), sum_ld=80) == EINVAL
+    assert _norm(dict(sum=FAKE), n=0) == 0
+
+
+def test_norm_quant_null_and_empty():
+    assert _lib().lib().gptq_norm_quant(None, *[ctypes.c_void_p(FAKE)] * 7, None) == EINVAL
+    assert _norm(dict(x=0, q=0, y=0), n=0) == 0
+
+
+# --------------------------------------------------------------------------------------- byte_gemm
+
+def _gemm(**kw):
+    d = dict(x=FAKE, m=4, ld_x=64, xs=2 * FAKE, w=3 * FAKE, ld_w=64, ws=4 * FAKE, zeros=5 * FAKE, rows=32, d=64, y=6 * FAKE,
+             y_dtype=0, ld_y=32, work=7 * FAKE, work_bytes=0)
+    d.update(kw)
+    return _lib().lib().gptq_byte_gemm(*d.values(), None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(m=-1), dict(m=1 << 40), dict(rows=-1), dict(rows=(1 << 24) + 1, ld_y=1 << 25), dict(d=0), dict(ld_x=63), dict(ld_w=63),
+    dict(ld_y=31), dict(y_dtype=3), dict(x=0), dict(w=0), dict(y=0), dict(y=FAKE), dict(y=3 * FAKE + 100),
+    dict(y=2 * FAKE), dict(y=4 * FAKE), dict(y=5 * FAKE), dict(work=7 * FAKE + 8), dict(ld_x=1 << 60)], ids=str)
+def test_byte_gemm_rejects(kw):
+    assert _gemm(**kw) == EINVAL
+
+
+def test_byte_gemm_longest_sum_and_empty():
+    assert _gemm(d=131072, ld_x=131072, ld_w=131072) == EUNSUPPORTED
+    assert _gemm(m=0, x=0, y=0) == 0
+    assert _gemm(rows=0, w=0, y=0) == 0
+    f = _lib().lib().gptq_byte_gemm_workspace_bytes
+    assert f(0, 4, 4) == 0 and f(4, -1, 4) == 0 and f(4, 4, 131072) == 0 and f(4, 4, 0) == 0
+
+
+# -------------------------------------------------------------------------------------------- cache
+
+def _cache(**kw):
+    d = dict(k=FAKE, v=2 * FAKE, k_scales=3 * FAKE, v_scales=4 * FAKE, pages=10, k_page=16 * 2 * 32, k_tok=64, k_hp=32,
+             v_page=16 * 2 * 32, v_tok=64, v_hp=32, page_size=16, kv_heads=2, head_dim=32, max_pages=4)
+    d.update(kw)
+    return _lib().gptq_kv_cache_t(**d)
+
+
+CACHE_REFUSED = [
+    (dict(pages=-1), EINVAL), (dict(pages=1 << 31), EINVAL), (dict(page_size=0), EINVAL), (dict(page_size=24), EUNSUPPORTED),
+    (dict(page_size=8), EUNSUPPORTED), (dict(page_size=2048), EUNSUPPORTED), (dict(kv_heads=0), EINVAL),
+    (dict(kv_heads=65536), EINVAL), (dict(head_dim=0), EINVAL), (dict(head_dim=1025), EINVAL), (dict(max_pages=0), EINVAL),
+    (dict(max_pages=1 << 27), EINVAL), (dict(k=0), EINVAL), (dict(v=0), EINVAL), (dict(k_scales=0), EINVAL),
+    (dict(v_scales=0), EINVAL), (dict(k_page=-1), EINVAL), (dict(v_tok=1 << 60), EINVAL)]
+
+
+def _append(over=None, cache=None, **kw):
+    L = _lib()
+    d = dict(seqs=2, n=8, k_ld=64, k_hp=32, v_ld=64, v_hp=32, dtype=1, rotary_dim=32, interleaved=0, axes=1)
+    d.update(kw)
+    p = dict(k=5 * FAKE, v=6 * FAKE, start=7 * FAKE, past=8 * FAKE, table=9 * FAKE, positions=0, inv_freq=10 * FAKE, pair_axis=0)
+    p.update(over or {})
+    a = L.gptq_kv_append_t(**d)
+    c = cache if cache is not None else _cache()
+    return L.lib().gptq_kv_append(ctypes.byref(a), ctypes.byref(c), *[ctypes.c_void_p(v) for v in p.values()], None)
+
+
+@pytest.mark.parametrize("kw,status", CACHE_REFUSED, ids=str)
+def test_kv_append_rejects_caches(kw, status):
+    assert _append(cache=_cache(**kw)) == status
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k_hp=16),                          # heads of the cache overlap
+    dict(v_tok=32), dict(k_page=100), dict(v=FAKE), dict(v=FAKE + 100),
+    dict(v=FAKE + 16 * 64 * 9),             # begins in the last page of keys
+    dict(k_scales=FAKE + 64), dict(v_scales=2 * FAKE), dict(v_scales=3 * FAKE + 8), dict(k=5 * FAKE), dict(v_scales=6 * FAKE),
+], ids=str)
+def test_kv_append_rejects_overlaps(kw):
+    assert _append(cache=_cache(**kw)) == EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(seqs=-1), dict(seqs=1 << 31), dict(n=-1), dict(n=(1 << 30) + 1), dict(dtype=4), dict(rotary_dim=33), dict(rotary_dim=34),
+    dict(rotary_dim=-2), dict(interleaved=2), dict(axes=0), dict(axes=65), dict(k_ld=-1), dict(v_hp=1 << 60),
+    dict(axes=2)], ids=str)                 # several rows of positions, and none given
+def test_kv_append_rejects_settings(kw):
+    assert _append(**kw) == EINVAL
+
+
+@pytest.mark.parametrize("over", [dict(k=0), dict(v=0), dict(past=0), dict(table=0), dict(inv_freq=0)], ids=str)
+def test_kv_append_rejects_pointers(over):
+    assert _append(over) == EINVAL
+
+
+def test_kv_append_equal_ranges_need_a_multiple_and_empty():
+    assert _append(dict(start=0), seqs=3) == EINVAL
+    assert _append(dict(k=0), n=0) == 0
+    assert _append(dict(k=0), seqs=0) == 0
+    assert _append(dict(k=0), cache=_cache(pages=0, k=0, v=0, k_scales=0, v_scales=0)) == 0
+    L = _lib()
+    assert L.lib().gptq_kv_append(None, ctypes.byref(_cache()), *[ctypes.c_void_p(FAKE)] * 8, None) == EINVAL
+    a = L.gptq_kv_append_t(seqs=1, n=1, axes=1)
+    assert L.lib().gptq_kv_append(ctypes.byref(a), None, *[ctypes.c_void_p(FAKE)] * 8, None) == EINVAL
+
+
+# ------------------------------------------------------------------------------------ kv_attention
+
+def _attention(over=None, cache=None, **kw):
+    L = _lib()
+    d = dict(seqs=2, n_q=8, q_ld=128, q_hp=32, out_ld=128, out_hp=32, scale=0.25, softcap=0.0, dtype=1, q_heads=4, causal=1,
+             window=0)
+    d.update(kw)
+    p = dict(q=5 * FAKE, q_start=0, lens=6 * FAKE, table=7 * FAKE, slopes=0, out=8 * FAKE, work=0)
+    p.update(over or {})
+    a = L.gptq_kv_attention_t(**d)
+    c = cache if cache is not None else _cache()
+    return L.lib().gptq_kv_attention(ctypes.byref(a), ctypes.byref(c), *[ctypes.c_void_p(v) for v in p.values()], 0, None)
+
+
+@pytest.mark.parametrize("kw,status", CACHE_REFUSED, ids=str)
+def test_kv_attention_rejects_caches(kw, status):
+    assert _attention(cache=_cache(**kw)) == status
+    L = _lib()
+    a = L.gptq_kv_attention_t(seqs=2, n_q=8, q_heads=4, scale=1.0)
+    assert L.lib().gptq_kv_attention_workspace_bytes(ctypes.byref(a), ctypes.byref(_cache(**kw))) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(seqs=-1), dict(seqs=1 << 31), dict(n_q=-1), dict(n_q=(1 << 30) + 2), dict(dtype=9), dict(q_heads=0), dict(q_heads=3),
+    dict(causal=2), dict(window=-1), dict(scale=float("inf")), dict(scale=float("nan")), dict(scale=1e300),
+    dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=1e-300), dict(softcap=1e300), dict(q_ld=-1),
+    dict(out_hp=31), dict(out_ld=64), dict(seqs=3), dict(q_hp=1 << 60)], ids=str)
+def test_kv_attention_rejects_settings(kw):
+    assert _attention(**kw) == EINVAL
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=0), dict(lens=0), dict(table=0), dict(out=0), dict(out=5 * FAKE), dict(out=FAKE), dict(out=2 * FAKE + 64),
+    dict(out=3 * FAKE), dict(out=4 * FAKE), dict(work=9 * FAKE + 4)], ids=str)
+def test_kv_attention_rejects_pointers(over):
+    assert _attention(over) == EINVAL
+
+
+def test_kv_attention_empty():
+    assert _attention(dict(q=0, out=0), seqs=0) == 0
+    assert _attention(dict(q=0, out=0), n_q=0) == 0
+    L = _lib()
+    assert L.lib().gptq_kv_attention(None, ctypes.byref(_cache()), *[ctypes.c_void_p(FAKE)] * 7, 0, None) == EINVAL
+    assert L.lib().gptq_kv_attention_workspace_bytes(None, None) == 0
+
+
+# ------------------------------------------------------------------------------------------ binding
+
+def test_binding_refuses_host_tensors():
+    torch = pytest.importorskip("torch")
+    import post_weight_quantization_20_amd as g
+    x = torch.zeros(2, 32, dtype=torch.int8)
+    c, s = torch.zeros(1, 16, 1, 32, dtype=torch.int8), torch.zeros(1, 1)
+    t, n = torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    k = torch.zeros(1, 1, 32)
+    for call in (lambda: g.gptq_norm_quant(x.float()), lambda: g.gptq_byte_gemm(x, None, x, None),
+                 lambda: g.gptq_kv_append(k, k, c, c, s, s, t, n), lambda: g.gptq_kv_attention(k, c, c, s, s, t, n)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+# ------------------------------------------------------------------------------------------- oracle
+
+def test_oracle_norm_quant_by_hand():
+    codes, scales, y, quot = serve_ref.norm_quant([[3.0, 4.0]], [2.0, 1.0], 0.0)
+    rms = np.sqrt(12.5)
+    assert np.allclose(y, [[6 / rms, 4 / rms]]) and np.allclose(scales, 6 / rms / 127)
+    assert np.array_equal(codes, [[127, 85]]) and np.allclose(quot[0, 1], 84.6666666)
+
+
+def test_oracle_byte_gemm_by_hand():
+    whole, out = serve_ref.byte_gemm([[1, -2]], [0.5], [[3, 4]], [2.0], [1])
+    assert whole.tolist() == [[-4]] and out.tolist() == [[-4.0]]
+
+
+def test_oracle_append_by_hand():
+    """A page with one token of scale 1: a token twice as large halves its codes."""
+    cache = np.zeros((1, 16, 1, 2))
+    cache[0, 0, 0] = [100, 51]
+    got, sc, _ = serve_ref.kv_append([[[254.0, -127.0]]], cache, np.ones((1, 1)), np.array([[0]]), [0, 1], [1])
+    assert sc[0, 0] == 2.0 and got[0, 0, 0].tolist() == [50, 26] and got[0, 1, 0].tolist() == [127, -64]
+
+
+def test_oracle_attention_by_hand():
+    """Two keys with equal scores average their values; a page outside the pool is not seen."""
+    k = np.zeros((1, 16, 1, 1))
+    v = np.arange(16.0).reshape(1, 16, 1, 1)
+    s = np.ones((1, 1))
+    out, mag, _, written = serve_ref.kv_attention(np.ones((2, 1, 1)), k, v, s, s, np.array([[0]]), [0, 1], [2], 1.0)
+    assert out[0, 0, 0] == 0.5 and written.tolist() == [True, False]
+    out, *_ = serve_ref.kv_attention(np.ones((1, 1, 1)), k, v, s, s, np.array([[3]]), [0, 1], [2], 1.0)
+    assert out[0, 0, 0] == 0.0
+    out, *_ = serve_ref.kv_attention(np.ones((1, 1, 1)), k, v, s, s, np.array([[0]]), [0, 1], [9], 1.0, window=2)
+    assert out[0, 0, 0] == 7.5
+
+
+def test_oracle_rotation_is_complex_multiplication():
+    r = np.random.default_rng(0)
+    x = r.standard_normal((3, 2, 6))
+    f = np.array([1.0, 0.1], dtype=np.float32)
+    got = serve_ref.rotate(x, np.array([[1, 5, 9]]), f)
+    z = (x[..., :2] + 1j * x[..., 2:4]) * np.exp(1j * np.array([1, 5, 9])[:, None] * f.astype(np.float64))[:, None]
+    assert np.allclose(got[..., :2], z.real) and np.allclose(got[..., 2:4], z.imag) and np.array_equal(got[..., 4:], x[..., 4:])
