@@ -574,7 +574,8 @@ typedef struct {
  *   k, v             device arrays [n x kv_heads x head_dim] of dtype. Not modified.
  *   start            device int32[seqs + 1], ascending, or NULL: seqs equal ranges (n a multiple of seqs). Values are
  *                    clamped into [0, n].
- *   past             device int32[seqs], clamped to [0, max_pages * page_size].
+ *   past             device int32[seqs], clamped to [0, max_pages * page_size]. A sequence has at most 2^31 - 1024
+ *                    tokens; those beyond are left out.
  *   table            device int32[seqs * max_pages]. A page outside [0, pages) and tokens past the table's end are
  *                    left out. A page that this call writes must belong to one sequence and stand in its table
  *                    once (pages before, a shared prefix, may belong to several).
@@ -612,7 +613,7 @@ typedef struct {
  *   q         device array [n_q x q_heads x head_dim] of dtype, not modified.
  *   q_start   device int32[seqs + 1], ascending, or NULL: seqs equal ranges (n_q a multiple of seqs). Values are
  *             clamped into [0, n_q].
- *   lens      device int32[seqs], clamped to [0, max_pages * page_size].
+ *   lens      device int32[seqs], clamped to [0, max_pages * page_size] and 2^31 - 1024.
  *   table     device int32[seqs * max_pages]; sequences may share pages.
  *   slopes    device float[q_heads], or NULL.
  *   out       device array, output; apart from q, its heads and tokens from each other.

@@ -44,7 +44,7 @@ GPTQ_DEV int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo
 
 GPTQ_DEV Unit find_unit(const AppendArgs& a, int64_t u, int lane) {
   Unit r{-1, 0, 0, 0, 0};
-  const int64_t cap = min((int64_t)a.c.max_pages * a.c.page_size, (int64_t)0x7fffffff);
+  const int64_t cap = min((int64_t)a.c.max_pages * a.c.page_size, (int64_t)0x7ffffc00);
   int64_t before = 0;
   for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
     const int64_t s = s0 + lane;
