@@ -156,7 +156,8 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 
 constexpr int kRowTile = 16, kKeyTile = 32;
 constexpr int kParts = 512;        // workgroups: two a CU
-constexpr int kMinTiles = 8;       // key tiles that a workgroup takes at least
+constexpr int kMinTiles = 4;       // key tiles that a workgroup takes at least
+constexpr int kJoinRows = 1;       // rows of a unit that a workgroup joins
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kShift = 7.0f, kRaise = 8.0f;
 
@@ -164,7 +165,14 @@ struct FewArgs {
   KvArgs a;
   int parts;                       // > 0: workgroups that share the list by key tiles; 0: by whole units
   int64_t each;                    // parts = 0: units of a workgroup
+  struct Head* head;               // [parts]: the unit that a part leaves to the next ones
   float *part_ml, *part_o;         // [parts][2][16][2] and [parts][2][16][dh]
+};
+
+// A unit that part w began and part `last` ends: its sequence's queries, its rows and key head.
+struct Head {
+  int64_t q0, lq, row0;
+  int32_t kvh, last;               // last: -1 where part w leaves no unit
 };
 
 GPTQ_DEV int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -189,35 +197,66 @@ GPTQ_DEV Span span_of(const KvArgs& a, const Seq& q) {
   return r;
 }
 
-// Sum of the list's entries before sequence s, for s given or, with at >= 0, for the sequence that holds entry
-// `at` (s = -1: none does). One lane a sequence, 64 at a time.
-GPTQ_DEV int64_t before_seq(const KvArgs& a, bool whole, int64_t at, int64_t& s, int lane) {
-  int64_t before = 0;
-  const int64_t stop = s;
-  for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
-    const int64_t mine = s0 + lane;
-    int64_t w = 0;
-    if (mine < a.seqs && (at >= 0 || mine < stop)) w = span_of(a, sequence(a, mine)).work(whole);
-    int64_t sum = w;
+// The list's total, and for an entry the sequence that holds it (at.s = -1: none does) with the entries before it.
+// One lane a sequence, 64 at a time.
+struct At {
+  int64_t s, before;
+  Seq sq;
+};
+
+GPTQ_DEV int64_t prefix_sum(int64_t v, int lane) {
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t v = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += v;
-    }
-    if (at >= 0) {
-      const uint64_t past = __ballot(before + sum > at);
-      if (past) {
-        const int l = __builtin_ctzll(past);
-        s = s0 + l;
-        return before + uniform(__shfl(sum, l, 64) - __shfl(w, l, 64));
-      }
-    } else if (s0 + 64 >= stop) {
-      return before + uniform(__shfl(sum, 63, 64));
-    }
-    before += uniform(__shfl(sum, 63, 64));
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t x = __shfl_up(v, o, 64);
+    if (lane >= o) v += x;
   }
-  if (at >= 0) s = -1;
-  return before;
+  return v;
+}
+
+GPTQ_DEV int64_t lane_value(int64_t v, int l) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, l) |
+                   (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32);
+}
+
+// entry(total) names the entry.
+template <typename F>
+GPTQ_DEV At find_entry(const KvArgs& a, bool whole, int lane, F&& entry) {
+  At r{-1, 0, {}};
+  Seq q{};
+  int64_t w = 0, sum = 0, total = 0;
+  for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
+    q = Seq{};
+    w = 0;
+    if (s0 + lane < a.seqs) {
+      q = sequence(a, s0 + lane);
+      w = span_of(a, q).work(whole);
+    }
+    sum = prefix_sum(w, lane);
+    total += lane_value(sum, 63);
+  }
+  const int64_t at = entry(total);
+  if (at < 0 || at >= total) return r;
+  for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
+    if (a.seqs > 64) {   // else what the lanes hold is the list
+      q = Seq{};
+      w = 0;
+      if (s0 + lane < a.seqs) {
+        q = sequence(a, s0 + lane);
+        w = span_of(a, q).work(whole);
+      }
+      sum = prefix_sum(w, lane);
+    }
+    const uint64_t past = __ballot(r.before + sum > at);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      r.s = s0 + l;
+      r.before += lane_value(sum, l) - lane_value(w, l);
+      r.sq = Seq{lane_value(q.q0, l), lane_value(q.lq, l), lane_value(q.len, l)};
+      return r;
+    }
+    r.before += lane_value(sum, 63);
+  }
+  return r;
 }
 
 // Entries of each workgroup's part.
@@ -264,37 +303,43 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
   constexpr int VB = DHP == 64 ? 4 : 8, NU = DHP == 256 ? 2 : 1, NT = VB * NU;
   typedef uint32_t KUnit __attribute__((ext_vector_type(KB / 4), aligned(1)));
   typedef uint32_t VUnit __attribute__((ext_vector_type(VB / 4), aligned(1)));
-  __shared__ float merge[2][4 * NT + 3][64];
+  __shared__ float merge[4][4][VB][64], stats[4][3][64];
   const KvArgs& a = f.a;
   const int lane = threadIdx.x & 63, wave = uniform((int32_t)(threadIdx.x >> 6));
   const int n = lane & 15, g = lane >> 4;
   const bool whole = f.parts == 0;
   const int dh = a.dh;
 
-  int64_t s = a.seqs, pos, end;
-  if (whole) {
-    pos = (int64_t)blockIdx.x * f.each;
-    end = pos + f.each;
-  } else {
-    const int64_t total = before_seq(a, false, -1, s, lane);
-    const int64_t size = part_size(total, f.parts);
+  int64_t pos = 0, end = 0, size = 0;
+  At at = find_entry(a, whole, lane, [&](int64_t total) {
+    size = whole ? f.each : part_size(total, f.parts);
     pos = (int64_t)blockIdx.x * size;
     end = min(total, pos + size);
+    return pos;
+  });
+  Head left{0, 0, 0, 0, -1};
+
+  // the lane's columns in a key tile's rows (those past the head read the first ones, which meet zeros in Q)
+  int64_t k_lane[KL];
+#pragma unroll
+  for (int j = 0; j < KL; ++j) {
+    const int c = 4 * KB * j + KB * g;
+    k_lane[j] = n * a.c.k_tok + (c < dh ? c : 0);
   }
-  if (pos >= end) return;
-  int64_t before = before_seq(a, whole, pos, s, lane);
-  if (s < 0) return;
+  int64_t v_lane[NU];
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int c = 128 * u + VB * n;               // past the head: columns of the output that are not stored
+    v_lane[u] = 4 * g * a.c.v_tok + (c < dh ? c : 0);
+  }
 
-  // the lane's place in a key tile and in its rows
-  const int kcol = KB * g;                        // of 4 KB columns a load
-  const int64_t k_lane = n * a.c.k_tok + kcol, v_lane = 4 * g * a.c.v_tok + VB * n;
-
-  while (true) {
-    const Seq sq = sequence(a, s);
+  while (at.s >= 0) {
+    const int64_t s = at.s;
+    const Seq sq = at.sq;
     const Span sp = span_of(a, sq);
-    const int64_t at = pos - before;              // within the sequence's entries
-    const int64_t unit = whole ? at : at / sp.tiles;
-    const int64_t t0 = whole ? 0 : at - unit * sp.tiles;
+    const int64_t in = pos - at.before;           // within the sequence's entries
+    const int64_t unit = whole ? in : in / sp.tiles;
+    const int64_t t0 = whole ? 0 : in - unit * sp.tiles;
     const int64_t t1 = whole ? sp.tiles : min(sp.tiles, t0 + (end - pos));
     const int kvh = uniform((int32_t)(unit / sp.rows));
     const int64_t row0 = uniform((unit - kvh * sp.rows) * kRowTile);
@@ -318,41 +363,118 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
     lim_max = uniform(lim_max);
     lo_max = uniform(lo_max);
 
-    // Q^T: 8 columns of the row for each product, in the order in which the keys' bytes lie
+    // Q^T: 8 columns of the row for each product, in the order in which the keys' bytes lie. Its loads, the pages'
+    // and the first tile's are on their way together.
+    constexpr int QW = TERMS == 2 ? 8 : 4;        // words of 8 columns: two terms are for fp32 alone
+    typedef uint32_t QWords __attribute__((ext_vector_type(QW), aligned(TERMS == 2 ? 4 : 2)));
+    QWords qw[NK];
+    auto q_column = [&](int ks) { return KB == 16 ? 64 * (ks / 2) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g; };
+    {
+      const char* base = static_cast<const char*>(a.q) + ((sq.q0 + qi) * a.q_ld + h * a.q_hp) * (QW / 2);
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        const int c0 = q_column(ks);
+        qw[ks] = *reinterpret_cast<const QWords*>(base + (c0 < dh ? c0 : 0) * (QW / 2));
+      }
+    }
+    const float slope = ANY && a.slopes ? a.slopes[h] : 0.f;
+
+    // this wave's tiles: t0 + wave, + 4, ..., of which 32 at a time have their pages and scales in lanes
+    const int32_t tfirst = (int32_t)(sp.tlo + t0) + wave,
+                  tend = min((int32_t)(sp.tlo + t1), (int32_t)(((int64_t)lim_max + kKeyTile - 1) / kKeyTile));
+    const uint32_t per_page = (uint32_t)a.ps >> 4;
+    uint64_t valid = 0;
+    int64_t k_at = 0, v_at = 0;
+    float ks = 0.f, vs = 0.f;
+    int count = 0;
+    auto open = [&](int32_t tb) {
+      // lane 2 i + e: subtile e (16 keys) of the batch's tile i
+      const int32_t tile = tb + 4 * (lane >> 1);
+      const uint32_t sub = 2 * (uint32_t)tile + (lane & 1), at_page = sub / per_page;
+      int64_t page = -1;
+      if (tile < tend && 16 * (int64_t)sub < sq.len) {
+        page = a.table[s * a.c.max_pages + at_page];
+        if (page >= a.c.pages) page = -1;
+      }
+      valid = __ballot(page >= 0);
+      ks = vs = 0.f;
+      if (page >= 0) {
+        ks = a.c.k_scales[page * a.hk + kvh];
+        vs = a.c.v_scales[page * a.hk + kvh];
+      }
+      // where one half of a tile has no page, the other's is read in its place; without both there is no tile
+      const int64_t slot = (sub - at_page * per_page) * 16;
+      k_at = page * a.c.k_page + slot * a.c.k_tok + kvh * a.c.k_hp;
+      v_at = page * a.c.v_page + slot * a.c.v_tok + kvh * a.c.v_hp;
+      const int64_t ko = __shfl_xor(k_at, 1, 64), vo = __shfl_xor(v_at, 1, 64);
+      if (page < 0) {
+        k_at = ko;
+        v_at = vo;
+      }
+      count = min(32, (tend - tb + 3) / 4);
+    };
+    // Two tiles' bytes in registers: one on its way while the other is used.
+    struct Tile {
+      KUnit k[2][KL];
+      VUnit v[8][NU];
+    };
+    auto load = [&](int i, Tile& x) {
+      if (i >= count || !((int)(valid >> (2 * i)) & 3)) return;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int8_t* kp = a.c.k + lane_value(k_at, 2 * i + e);
+        const int8_t* vp = a.c.v + lane_value(v_at, 2 * i + e);
+#pragma unroll
+        for (int j = 0; j < KL; ++j) x.k[e][j] = *reinterpret_cast<const KUnit*>(kp + k_lane[j]);
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) x.v[4 * e + b][u] = *reinterpret_cast<const VUnit*>(vp + b * a.c.v_tok + v_lane[u]);
+      }
+    };
+    Tile even, odd;
+    if (tfirst < tend) {
+      open(tfirst);
+      load(0, even);
+    }
+
     half8 q[TERMS][NK];
     int qe = 0;                                   // queries are 2^qe larger than q
     {
-      const int64_t q_at = (sq.q0 + qi) * a.q_ld + h * a.q_hp;
       float v[NK][8], top = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        const int c0 = KB == 16 ? 64 * (ks / 2) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g;
+      for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          v[ks][e] = live && c0 + e < dh ? load_q(a, dtype, q_at + c0 + e) : 0.f;
-          top = fmaxf(top, fabsf(v[ks][e]));
+          float x;
+          if constexpr (TERMS == 2) {
+            x = __builtin_bit_cast(float, (uint32_t)qw[k][e]);
+          } else {
+            const uint16_t w = (uint16_t)(qw[k][e / 2] >> (16 * (e & 1)));
+            x = dtype == F16 ? (float)__builtin_bit_cast(_Float16, w) : bf16_bits_to_f32(w);
+          }
+          v[k][e] = live && q_column(k) < dh ? x : 0.f;
+          top = fmaxf(top, fabsf(v[k][e]));
         }
-      }
-      if (dtype != F16) {
+      if (TERMS == 2 || dtype != F16) {
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         if (top > 0.f && top < INFINITY) {
           qe = ilogbf(top);
 #pragma unroll
-          for (int ks = 0; ks < NK; ++ks)
+          for (int k = 0; k < NK; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[ks][i] = ldexpf(v[ks][i], -qe);
+            for (int i = 0; i < 8; ++i) v[k][i] = ldexpf(v[k][i], -qe);
         }
       }
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks)
+      for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          q[0][ks][i] = (_Float16)v[ks][i];
-          if constexpr (TERMS == 2) q[1][ks][i] = (_Float16)(v[ks][i] - (float)q[0][ks][i]);
+          q[0][k][i] = (_Float16)v[k][i];
+          if constexpr (TERMS == 2) q[1][k][i] = (_Float16)(v[k][i] - (float)q[0][k][i]);
         }
     }
-    const float slope = ANY && a.slopes ? a.slopes[h] : 0.f;
 
     floatx4 acc[NT];
 #pragma unroll
@@ -360,27 +482,9 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
     float m = -INFINITY, l = 0.f;
     int ve = -200;                                // value scales are below 2^ve
 
-    // this wave's tiles: t0 + wave, + 4, ..., of which 32 at a time have their pages and scales in lanes
-    const int64_t tfirst = sp.tlo + t0 + wave, tend = min(sp.tlo + t1, (int64_t)(lim_max + kKeyTile - 1) / kKeyTile);
-    const int per_page = a.ps >> 4;
-    for (int64_t tb = tfirst; tb < tend; tb += 4 * 32) {
-      // lane 2 i + e: subtile e (16 keys) of the batch's tile i
-      const int64_t sub = 2 * (tb + 4 * (lane >> 1)) + (lane & 1);
-      int64_t page = -1;
-      if (tb + 4 * (lane >> 1) < tend && 16 * sub < sq.len) {
-        page = a.table[s * a.c.max_pages + sub / per_page];
-        if (page >= a.c.pages) page = -1;
-      }
-      const uint64_t valid = __ballot(page >= 0);
-      float ks = 0.f, vs = 0.f;
-      if (page >= 0) {
-        ks = a.c.k_scales[page * a.hk + kvh];
-        vs = a.c.v_scales[page * a.hk + kvh];
-      }
-      const int32_t slot = (int32_t)(sub % per_page) * 16;
+    for (int32_t tb = tfirst; tb < tend;) {
       {
-        float top = fabsf(vs) < INFINITY ? fabsf(vs) : 0.f;
-        top = wave_max(top);
+        const float top = wave_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.f);
         if (top > 0.f) {
           const int e = uniform((int32_t)ilogbf(top)) + 1;
           if (e > ve) {
@@ -392,62 +496,21 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
         }
         if (fabsf(vs) < INFINITY) vs = ldexpf(vs, -ve);
       }
-      const int count = (int)min((int64_t)32, (tend - tb + 3) / 4);
-
-      KUnit kx[2][KL];
-      VUnit vx[8][NU];
-      auto load = [&](int i) {
-        // where one half of a tile has no page, the other's is read in its place; without both there is no tile
+      auto compute = [&](int i, const Tile& x) {
         const int both = (int)(valid >> (2 * i)) & 3;
-        if (!both) return;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int from = 2 * i + ((both >> e) & 1 ? e : 1 - e);
-          const int64_t pg = __builtin_amdgcn_readlane((int)page, from);
-          const int64_t sl = __builtin_amdgcn_readlane(slot, from);
-          const int8_t* kp = a.c.k + (pg * a.c.k_page + sl * a.c.k_tok + kvh * a.c.k_hp) + k_lane;
-          const int8_t* vp = a.c.v + (pg * a.c.v_page + sl * a.c.v_tok + kvh * a.c.v_hp) + v_lane;
-#pragma unroll
-          for (int j = 0; j < KL; ++j)
-            kx[e][j] = 4 * KB * j + kcol < dh ? *reinterpret_cast<const KUnit*>(kp + 4 * KB * j) : KUnit{};
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int u = 0; u < NU; ++u)
-              vx[4 * e + b][u] = 128 * u + VB * n < dh
-                                     ? *reinterpret_cast<const VUnit*>(vp + b * a.c.v_tok + 128 * u)
-                                     : VUnit{};
-        }
-      };
-      load(0);
-      for (int i = 0; i < count; ++i) {
-        const int both = (int)(valid >> (2 * i)) & 3;
-        if (!both) {
-          if (i + 1 < count) load(i + 1);
-          continue;
-        }
-        // this tile's operands out of the way of the next one's loads
+        if (i >= count || !both) return;
         floatx4 S[2];
-        uint32_t vw[8][NU][VB / 4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           S[e] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < NK; ++k) {
-            const half8 kf = KB == 16 ? widen8(kx[e][k / 2][2 * (k & 1)], kx[e][k / 2][2 * (k & 1) + 1])
-                                      : widen8(kx[e][k][0], kx[e][k][1]);
+            const half8 kf = KB == 16 ? widen8(x.k[e][k / 2][2 * (k & 1)], x.k[e][k / 2][2 * (k & 1) + 1])
+                                      : widen8(x.k[e][k][0], x.k[e][k][1]);
 #pragma unroll
             for (int t = 0; t < TERMS; ++t) S[e] = mfma32(kf, q[t][k], S[e]);
           }
         }
-#pragma unroll
-        for (int b = 0; b < 8; ++b)
-#pragma unroll
-          for (int u = 0; u < NU; ++u)
-#pragma unroll
-            for (int c = 0; c < VB / 4; ++c) vw[b][u][c] = vx[b][u][c];
-        if (i + 1 < count) load(i + 1);
-
         const int32_t j0 = (int32_t)((tb + 4 * i) * kKeyTile);
         const int32_t jl = j0 + 4 * g;            // the key of register c of half e: jl + 16 e + c
         float mx = -INFINITY;
@@ -496,9 +559,9 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
           for (int c = 0; c < 4; ++c) {
             const float pr = __builtin_amdgcn_exp2f(S[e][c] + off);
             l += pr;
-            const float x = S[e][c] == -INFINITY ? 0.f : pr * sv;   // a scale that is not a number stays unseen
-            w[0][4 * e + c] = (_Float16)x;
-            if constexpr (TERMS == 2) w[1][4 * e + c] = (_Float16)(x - (float)w[0][4 * e + c]);
+            const float y = S[e][c] == -INFINITY ? 0.f : pr * sv;   // a scale that is not a number stays unseen
+            w[0][4 * e + c] = (_Float16)y;
+            if constexpr (TERMS == 2) w[1][4 * e + c] = (_Float16)(y - (float)w[0][4 * e + c]);
           }
         }
 #pragma unroll
@@ -508,168 +571,196 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
             half8 vf;
 #pragma unroll
             for (int pr = 0; pr < 4; ++pr) {
-              const half2v x = widen_pair<B % 4>(vw[2 * pr][u][B / 4], vw[2 * pr + 1][u][B / 4]);
-              vf[2 * pr] = x[0];
-              vf[2 * pr + 1] = x[1];
+              const half2v y = widen_pair<B % 4>(x.v[2 * pr][u][B / 4], x.v[2 * pr + 1][u][B / 4]);
+              vf[2 * pr] = y[0];
+              vf[2 * pr + 1] = y[1];
             }
 #pragma unroll
             for (int t = 0; t < TERMS; ++t) acc[u * VB + B] = mfma32(vf, w[t], acc[u * VB + B]);
           });
+      };
+      for (int i = 0; i < count; i += 2) {
+        load(i + 1, odd);
+        compute(i, even);
+        load(i + 2, even);
+        compute(i + 1, odd);
+      }
+      tb += 4 * 32;
+      if (tb < tend) {
+        open(tb);
+        load(0, even);
       }
     }
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
 
-    // the four waves' results into the first: 2 and 3 into 0 and 1, then 1 into 0
+    // The four waves' results together, wave c taking register c of every product: columns VB (4 g + c) .. + VB - 1
+    // of the lane's row.
     __syncthreads();                              // the area may still be read from the segment before
+    stats[wave][0][lane] = m;
+    stats[wave][1][lane] = l;
+    stats[wave][2][lane] = __builtin_bit_cast(float, ve);
+    float part[NT], give[4], lsum = 0.f;
 #pragma unroll
-    for (int step = 0; step < 2; ++step) {
-      const int from = 2 >> step;                 // waves from .. 2 from - 1 give
-      if (wave >= from && wave < 2 * from) {
-        float(*o)[64] = merge[wave - from];
+    for (int u = 0; u < NU; ++u) {
+      if (u) __syncthreads();
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) o[4 * t + c][lane] = acc[t][c];
-        o[4 * NT][lane] = m;
-        o[4 * NT + 1][lane] = l;
-        o[4 * NT + 2][lane] = __builtin_bit_cast(float, ve);
-      }
+        for (int b = 0; b < VB; ++b) merge[wave][c][b][lane] = acc[u * VB + b][c];
       __syncthreads();
-      if (wave < from) {
-        float(*o)[64] = merge[wave];
-        const float m1 = o[4 * NT][lane], m2 = fmaxf(m, m1);
-        const int e1 = __builtin_bit_cast(int, o[4 * NT + 2][lane]), e2 = max(ve, e1);
-        const float f0 = m == -INFINITY && l == 0.f ? 0.f : __builtin_amdgcn_exp2f(m - m2);
-        const float f1 = m1 == -INFINITY && o[4 * NT + 1][lane] == 0.f ? 0.f : __builtin_amdgcn_exp2f(m1 - m2);
-        const float g0 = f0 * ldexpf(1.0f, max(ve - e2, -200)), g1 = f1 * ldexpf(1.0f, max(e1 - e2, -200));
+      if (u == 0) {
+        float mw[4];
+        int ew[4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int w = 0; w < 4; ++w) {
+          mw[w] = stats[w][0][lane];
+          ew[w] = __builtin_bit_cast(int, stats[w][2][lane]);
+        }
+        m = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
+        ve = max(max(ew[0], ew[1]), max(ew[2], ew[3]));
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[t][c] = acc[t][c] * g0 + o[4 * t + c][lane] * g1;
-        l = l * f0 + o[4 * NT + 1][lane] * f1;
-        m = m2;
-        ve = e2;
+        for (int w = 0; w < 4; ++w) {
+          const float lw = stats[w][1][lane];
+          const float fw = lw == 0.f ? 0.f : __builtin_amdgcn_exp2f(mw[w] - m);
+          lsum += lw * fw;
+          give[w] = fw * ldexpf(1.0f, max(ew[w] - ve, -200));
+        }
       }
-      if (step == 0) __syncthreads();
+#pragma unroll
+      for (int b = 0; b < VB; ++b) {
+        part[u * VB + b] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          part[u * VB + b] = __builtin_fmaf(merge[w][wave][b][lane], give[w], part[u * VB + b]);
+      }
     }
-    if (wave == 0 && live) {
-      const float inv = l == 0.f ? 0.f : 1.0f / l;
-      const bool complete = t0 == 0 && t1 == sp.tiles;
+    if (live) {
+      const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
       float* po = nullptr;
-      if (!complete) {
+      if (t0 != 0 || t1 != sp.tiles) {
         // one part has at most one unit that it did not begin, and one more that it does not end
         const int64_t slot = ((int64_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kRowTile + n;
-        if (g == 0) {
+        if (g == 0 && wave == 0) {
           f.part_ml[2 * slot] = m;
-          f.part_ml[2 * slot + 1] = l;
+          f.part_ml[2 * slot + 1] = lsum;
         }
         po = f.part_o + slot * dh;
       }
       const int64_t o_at = (sq.q0 + qi) * a.o_ld + h * a.o_hp;
 #pragma unroll
-      for (int u = 0; u < NU; ++u)
+      for (int u = 0; u < NU; ++u) {
+        const int c0 = 128 * u + VB * (4 * g + wave);
+        if (c0 >= dh) continue;
+        auto put = [&](auto* dst) {
+          typedef typename std::remove_pointer<decltype(dst)>::type T;
+          typedef T Vec __attribute__((ext_vector_type(VB), aligned(sizeof(T))));
+          Vec x;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int c0 = 128 * u + VB * (4 * g + c);
-          if (c0 >= dh) continue;
-          float o[VB];
-#pragma unroll
-          for (int b = 0; b < VB; ++b) o[b] = ldexpf(acc[u * VB + b][c] * inv, ve);
-          auto put = [&](auto* dst) {
-            typedef typename std::remove_pointer<decltype(dst)>::type T;
-            typedef T Vec __attribute__((ext_vector_type(VB), aligned(sizeof(T))));
-            Vec x;
-#pragma unroll
-            for (int b = 0; b < VB; ++b) x[b] = (T)o[b];
-            *reinterpret_cast<Vec*>(dst) = x;
-          };
-          if (po) put(po + c0);
-          else if (dtype == F32) put(static_cast<float*>(a.out) + o_at + c0);
-          else if (dtype == F16) put(static_cast<_Float16*>(a.out) + o_at + c0);
-          else put(static_cast<__bf16*>(a.out) + o_at + c0);
-        }
+          for (int b = 0; b < VB; ++b) x[b] = (T)ldexpf(part[u * VB + b] * inv, ve);
+          *reinterpret_cast<Vec*>(dst) = x;
+        };
+        if (po) put(po + c0);
+        else if (dtype == F32) put(static_cast<float*>(a.out) + o_at + c0);
+        else if (dtype == F16) put(static_cast<_Float16*>(a.out) + o_at + c0);
+        else put(static_cast<__bf16*>(a.out) + o_at + c0);
+      }
     }
+    if (t0 == 0 && t1 < sp.tiles) left = Head{sq.q0, sq.lq, row0, kvh, (int32_t)((pos + sp.tiles - 1) / size)};
+
     // on to the next unit, in this sequence or the next that has any
     pos += whole ? 1 : t1 - t0;
     if (pos >= end) break;
-    if (pos >= before + sp.work(whole)) {
-      before += sp.work(whole);
+    if (pos >= at.before + sp.work(whole)) {
+      at.before += sp.work(whole);
       do {
-        ++s;
-      } while (s < a.seqs && span_of(a, sequence(a, s)).units == 0);
-      if (s >= a.seqs) break;
+        ++at.s;
+        if (at.s < a.seqs) at.sq = sequence(a, at.s);
+      } while (at.s < a.seqs && span_of(a, at.sq).units == 0);
+      if (at.s >= a.seqs) break;
     }
   }
+  if (!whole && threadIdx.x == 0) f.head[blockIdx.x] = left;
 }
 
-// Joins the partial results of each unit that several workgroups shared: a workgroup a (query, head).
+// Joins the partial results of a unit that several workgroups shared, in their order: workgroup w the unit that
+// part w began and did not end.
 __global__ __launch_bounds__(256) void kv_join_kernel(FewArgs f, int dtype) {
   const KvArgs& a = f.a;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __shared__ float part[4][256];
-  int64_t all = a.seqs;
-  const int64_t size = part_size(before_seq(a, false, -1, all, lane), f.parts);
-  const int64_t total = a.nq * a.hq;
-  for (int64_t it = blockIdx.x; it < total; it += gridDim.x) {
-    const int64_t row = it / a.hq;
-    const int h = (int)(it - row * a.hq), kvh = h / a.group;
-    // the sequence that holds the row
-    int64_t s = -1;
-    if (!a.q_start) {
-      s = row / a.lq_even;
-    } else {
-      for (int64_t s0 = 0; s0 < a.seqs && s < 0; s0 += 64) {
-        bool in = false;
-        if (s0 + lane < a.seqs) {
-          const Seq q = sequence(a, s0 + lane);
-          in = row >= q.q0 && row < q.q0 + q.lq;
-        }
-        const uint64_t b = __ballot(in);
-        if (b) s = s0 + __builtin_ctzll(b);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w0 = blockIdx.x;
+  const Head hd = f.head[w0];
+  if (hd.last < 0) return;
+  const int parts = hd.last - w0 + 1, dh = a.dh;
+  // rows n0 .. n0 + rows - 1 of the unit
+  const int n0 = kJoinRows * blockIdx.y, rows = (int)min((int64_t)kJoinRows, hd.lq * a.group - hd.row0 - n0);
+  if (rows <= 0) return;
+  __shared__ float share[kJoinRows][kParts];
+  __shared__ floatx4 sums[256];
+  auto slot = [&](int w, int n) { return ((int64_t)2 * (w0 + w) + (w == 0 ? 1 : 0)) * kRowTile + n0 + n; };
+  for (int n = wave; n < rows; n += 4) {
+    float m = -INFINITY, l = 0.f, mw[kParts / 64], lw[kParts / 64];
+#pragma unroll
+    for (int i = 0; i < kParts / 64; ++i) {
+      const int w = 64 * i + lane;
+      mw[i] = -INFINITY;
+      lw[i] = 0.f;
+      if (w < parts) {
+        const float2 ml = *reinterpret_cast<const float2*>(f.part_ml + 2 * slot(w, n));
+        lw[i] = ml.y;
+        if (ml.y != 0.f) mw[i] = ml.x;
       }
+      m = fmaxf(m, mw[i]);
     }
-    if (s < 0) continue;
-    const Seq sq = sequence(a, s);
-    const Span sp = span_of(a, sq);
-    const int64_t before = before_seq(a, false, -1, s, lane);
-    const int64_t r = (row - sq.q0) * a.group + (h - kvh * a.group);
-    const int64_t u0 = before + (kvh * sp.rows + r / kRowTile) * sp.tiles, u1 = u0 + sp.tiles;
-    const int64_t w0 = u0 / size, w1 = (u1 - 1) / size;
-    if (w0 == w1) continue;                       // written by its one workgroup
-    const int n = (int)(r % kRowTile);
-    auto slot = [&](int64_t w) { return (2 * w + (w == w0 ? 1 : 0)) * kRowTile + n; };
-    float m = -INFINITY;
-    for (int64_t w = w0 + lane; w <= w1; w += 64)
-      if (f.part_ml[2 * slot(w) + 1] != 0.f) m = fmaxf(m, f.part_ml[2 * slot(w)]);
     m = wave_max(m);
-    float l = 0.f;
-    for (int64_t w = w0 + lane; w <= w1; w += 64) {
-      const float lw = f.part_ml[2 * slot(w) + 1];
-      if (lw != 0.f) l += lw * __builtin_amdgcn_exp2f(f.part_ml[2 * slot(w)] - m);
+#pragma unroll
+    for (int i = 0; i < kParts / 64; ++i) {
+      lw[i] = lw[i] == 0.f ? 0.f : lw[i] * __builtin_amdgcn_exp2f(mw[i] - m);
+      l += lw[i];
     }
     l = wave_add(l);
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t w = w0 + wave; w <= w1; w += 4) {
-      const float lw = f.part_ml[2 * slot(w) + 1];
-      if (lw == 0.f) continue;
-      const float share = lw * __builtin_amdgcn_exp2f(f.part_ml[2 * slot(w)] - m) / l;
-      const float* po = f.part_o + slot(w) * a.dh;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (64 * c + lane < a.dh) o[c] = __builtin_fmaf(po[64 * c + lane], share, o[c]);
+    for (int i = 0; i < kParts / 64; ++i)
+      if (64 * i + lane < parts) share[n][64 * i + lane] = lw[i] == 0.f ? 0.f : lw[i] / l;
+  }
+  __syncthreads();
+  // four columns a thread, and where that leaves threads over, the parts shared among them
+  const int quads = dh >> 2, items = rows * quads, split = max(1, 256 / items);
+  for (int i0 = 0; i0 < items; i0 += 256) {
+    const int it = split > 1 ? (int)threadIdx.x % items : i0 + (int)threadIdx.x;
+    const int z = split > 1 ? (int)threadIdx.x / items : 0;
+    const int n = it / quads, c = 4 * (it - n * quads);
+    floatx4 o = {0.f, 0.f, 0.f, 0.f};
+    if (it < items && z < split) {
+      for (int w = z; w < parts; w += 4 * split) {
+        floatx4 x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int u = w + e * split;
+          x[e] = floatx4{0.f, 0.f, 0.f, 0.f};
+          if (u < parts && share[n][u] != 0.f)
+            x[e] = *reinterpret_cast<const floatx4*>(f.part_o + slot(u, n) * dh + c) * share[n][u];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o += x[e];
+      }
     }
-    __syncthreads();
+    if (split > 1) {
+      sums[threadIdx.x] = o;
+      __syncthreads();
+      if (z == 0)
+        for (int e = 1; e < split; ++e) o += sums[threadIdx.x + e * items];
+    }
+    if (it < items && z == 0) {
+      const int64_t r = hd.row0 + n0 + n, qi = r / a.group;
+      const int64_t o_at = (hd.q0 + qi) * a.o_ld + (hd.kvh * a.group + (r - qi * a.group)) * a.o_hp + c;
+      auto put = [&](auto* dst) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) part[wave][64 * c + lane] = o[c];
-    __syncthreads();
-    const int c = threadIdx.x;
-    if (c < a.dh) {
-      const float v = (part[0][c] + part[1][c]) + (part[2][c] + part[3][c]);
-      const int64_t o_at = row * a.o_ld + h * a.o_hp + c;
-      if (dtype == F32) static_cast<float*>(a.out)[o_at] = v;
-      else if (dtype == F16) static_cast<_Float16*>(a.out)[o_at] = (_Float16)v;
-      else static_cast<__bf16*>(a.out)[o_at] = (__bf16)v;
+        for (int e = 0; e < 4; ++e)
+          dst[e] = (typename std::remove_reference<decltype(*dst)>::type)o[e];
+      };
+      if (dtype == F32) put(static_cast<float*>(a.out) + o_at);
+      else if (dtype == F16) put(static_cast<_Float16*>(a.out) + o_at);
+      else put(static_cast<__bf16*>(a.out) + o_at);
     }
   }
 }
@@ -706,7 +797,7 @@ Plan plan(const gptq_kv_attention_t& t, const gptq_kv_cache_t& c) {
 
 size_t kv_attention_workspace_bytes(const gptq_kv_attention_t& t, const gptq_kv_cache_t& c) {
   const Plan p = plan(t, c);
-  return (size_t)p.parts * 2 * kRowTile * (c.head_dim + 2) * sizeof(float);
+  return (size_t)p.parts * (2 * kRowTile * (c.head_dim + 2) * sizeof(float) + sizeof(Head));
 }
 
 hipError_t kv_attention(const gptq_kv_attention_t& t, const gptq_kv_cache_t& c, const void* q, const int32_t* q_start,
@@ -721,10 +812,11 @@ hipError_t kv_attention(const gptq_kv_attention_t& t, const gptq_kv_cache_t& c, 
   a.q_start = q_start; a.lens = lens; a.table = table; a.slopes = slopes;
   const Plan p = plan(t, c);
   if (p.few) {
-    FewArgs f{a, 0, 1, nullptr, nullptr};
+    FewArgs f{a, 0, 1, nullptr, nullptr, nullptr};
     if (p.parts && work && work_bytes >= kv_attention_workspace_bytes(t, c)) {
       f.parts = p.parts;
-      f.part_ml = static_cast<float*>(work);
+      f.head = static_cast<Head*>(work);
+      f.part_ml = reinterpret_cast<float*>(f.head + p.parts);
       f.part_o = f.part_ml + (size_t)p.parts * 2 * kRowTile * 2;
     }
     // a grid holds fewer than 2^32 threads
@@ -736,7 +828,7 @@ hipError_t kv_attention(const gptq_kv_attention_t& t, const gptq_kv_cache_t& c, 
                    : a.dh <= 128 ? (two ? launch_few<128, 2>(f, t.dtype, grid, s) : launch_few<128, 1>(f, t.dtype, grid, s))
                                  : (two ? launch_few<256, 2>(f, t.dtype, grid, s) : launch_few<256, 1>(f, t.dtype, grid, s));
     if (e != hipSuccess || !f.parts) return e;
-    hipLaunchKernelGGL(kv_join_kernel, dim3((unsigned)std::min<int64_t>(a.nq * a.hq, 65536)), dim3(256), 0, s, f, t.dtype);
+    hipLaunchKernelGGL(kv_join_kernel, dim3((unsigned)f.parts, kRowTile / kJoinRows), dim3(256), 0, s, f, t.dtype);
     return hipGetLastError();
   }
   const int64_t waves = a.nq * a.hq;
