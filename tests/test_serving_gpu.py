@@ -276,7 +276,7 @@ def test_byte_gemm_largest_sums(m):
     _check_gemm(x, None, w, None, None, y)
     wu = torch.full((rows, d), 255, dtype=torch.uint8, device="cuda:0")
     wu[::2] = 0
-    z = _ints([0, 255, -1000000, 1000000] * 5)
+    z = _ints([0, 255, -1000000, 1000000, 2 ** 31 - 1, -2 ** 31, 128, 1 << 28, 1, 254] * 2)
     y = _g().gptq_byte_gemm(x, None, wu, None, z)
     torch.cuda.synchronize()
     _check_gemm(x, None, wu, None, z, y)
