@@ -122,7 +122,7 @@ GPTQ_DEV bool tile_of(const GemmI8& a, uint32_t b, uint32_t& tm, uint32_t& tn) {
   return true;
 }
 
-template <int KB, int NST, bool DMA, bool CODES>
+template <int KB, int NST, bool DMA, bool CODES, int YT>
 __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
   constexpr int UN = KB / 16, KS = KB / 32;       // units of a row, products of 32 columns
   constexpr int OPB = BT * KB, STAGEB = 2 * OPB;  // bytes of an operand and of a stage
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
 #pragma unroll
     for (int i = i0; i < i1; ++i) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xv[i], wv[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[j], xv[i], acc[i][j], 0, 0, 0);
       if constexpr (CODES) xsum[i] = add_bytes(xv[i], xsum[i]);
     }
   };
@@ -276,52 +276,53 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
     __syncthreads();
   }
 
-  // Outputs leave through LDS, 32 rows of a wave's 128 columns at a time, so that a row's come side by side.
-  // Register e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32 of its block.
-  float ws[4];
-  int zero[4];
-  const int64_t nc = n0 + 128 * wn;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t r = min(nc + 32 * j + col, a.rows - 1);
-    ws[j] = a.ws ? a.ws[r] : 1.0f;
-    zero[j] = CODES ? a.z[r] : 128;
+  // Register e of lane l: output 8 (e / 4) + 4 (l / 32) + e % 4 of block j, token l % 32 of block i. Outputs leave
+  // through LDS, 32 tokens by the wave's 128 outputs at a time, so that a token's come side by side.
+  typedef typename ElemOf<YT>::T T;
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  constexpr int ESZ = sizeof(T), PITCH = 128 * ESZ + 16, UR = 8 * ESZ;   // UR: 16-byte units of a row
+  GPTQ_LDS char* area = lds + wave * 32 * (128 * 4 + 16);
+  GPTQ_LDS float* ws = (GPTQ_LDS float*)(lds + 4 * 32 * (128 * 4 + 16));
+  GPTQ_LDS int32_t* zs = (GPTQ_LDS int32_t*)(ws + BT);
+  {
+    const int64_t r = min(n0 + tid, a.rows - 1);
+    ws[tid] = a.ws ? a.ws[r] : 1.0f;
+    if constexpr (CODES) zs[tid] = a.z[r];
   }
-  GPTQ_LDS char* area = lds + wave * 32 * 528;
-  const int esz = a.y_dtype == F32 ? 4 : 2, pitch = 128 * esz + 16;
+  float xs[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) xs[i] = a.xs ? a.xs[min(m0 + 128 * wm + 32 * i + col, a.m - 1)] : 1.0f;
+  __syncthreads();
+  const int64_t nc = n0 + 128 * wn;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t mr = m0 + 128 * wm + 32 * i;
     if constexpr (CODES) xsum[i] += __shfl_xor(xsum[i], 32, 64);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int row = 8 * (e >> 2) + 4 * half + (e & 3);
-      const float xs = a.xs ? a.xs[min(mr + row, a.m - 1)] : 1.0f;
-      const int xsm = CODES ? __shfl(xsum[i], row, 64) : 0;
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v = output<CODES>(acc[i][j][e], xsm, zero[j], xs, ws[j]);
-        GPTQ_LDS char* o = area + row * pitch + (32 * j + col) * esz;
-        if (a.y_dtype == F32) *(GPTQ_LDS float*)o = v;
-        else if (a.y_dtype == F16) *(GPTQ_LDS _Float16*)o = (_Float16)v;
-        else *(GPTQ_LDS __bf16*)o = (__bf16)v;
+      for (int b = 0; b < 4; ++b) {
+        const int c = 32 * j + 8 * b + 4 * half;
+        const floatx4 w4 = *(GPTQ_LDS floatx4*)(ws + 128 * wn + c);
+        i32x4 z4 = {};
+        if constexpr (CODES) z4 = *(GPTQ_LDS i32x4*)(zs + 128 * wn + c);
+        T4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (T)output<CODES>(acc[i][j][4 * b + e], xsum[i], z4[e], xs[i], w4[e]);
+        *(GPTQ_LDS T4*)(area + col * PITCH + c * ESZ) = o;
       }
-    }
     __builtin_amdgcn_wave_barrier();
-    const int ur = 8 * esz;                       // 16-byte units of a row
-    for (int u = lane; u < 32 * ur; u += 64) {
-      const int row = u / ur, c = (u - row * ur) * 16 / esz;
+#pragma unroll
+    for (int q = 0; q < UR / 2; ++q) {
+      const int u = 64 * q + lane, row = u / UR, c = u % UR * 16 / ESZ;
       if (mr + row >= a.m || nc + c >= a.rows) continue;
-      GPTQ_LDS char* o = area + row * pitch + c * esz;
-      char* dst = static_cast<char*>(a.y) + ((mr + row) * a.ld_y + nc + c) * esz;
-      if (a.y_vec && nc + c + 16 / esz <= a.rows) {
+      GPTQ_LDS char* o = area + row * PITCH + c * ESZ;
+      T* dst = static_cast<T*>(a.y) + (mr + row) * a.ld_y + nc + c;
+      if (a.y_vec && nc + c + 16 / ESZ <= a.rows) {
         *reinterpret_cast<i32x4*>(dst) = *(GPTQ_LDS i32x4*)o;
       } else {
-        for (int e = 0; e < 16 / esz; ++e)
-          if (nc + c + e < a.rows) {
-            if (esz == 4) reinterpret_cast<int32_t*>(dst)[e] = ((GPTQ_LDS int32_t*)o)[e];
-            else reinterpret_cast<int16_t*>(dst)[e] = ((GPTQ_LDS int16_t*)o)[e];
-          }
+        for (int e = 0; e < 16 / ESZ; ++e)
+          if (nc + c + e < a.rows) dst[e] = ((GPTQ_LDS T*)o)[e];
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -378,11 +379,11 @@ hipError_t ask_lds(K kernel, size_t lds, std::atomic<uint64_t>& asked) {
 
 constexpr int kKB = 128, kNST = 2;
 
-template <bool DMA, bool CODES>
+template <bool DMA, bool CODES, int YT>
 hipError_t launch_tile(const GemmI8& a, hipStream_t s) {
   static std::atomic<uint64_t> asked{0};
   constexpr size_t lds = (size_t)kNST * 2 * BT * kKB;
-  auto f = tile_kernel<kKB, kNST, DMA, CODES>;
+  auto f = tile_kernel<kKB, kNST, DMA, CODES, YT>;
   const hipError_t e = ask_lds(f, lds, asked);
   if (e != hipSuccess) return e;
   const uint32_t per = (a.tiles_m * a.tiles_n + 7) / 8;
@@ -390,13 +391,20 @@ hipError_t launch_tile(const GemmI8& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool DMA, bool CODES>
+hipError_t tile_type(const GemmI8& a, hipStream_t s) {
+  return a.y_dtype == F32   ? launch_tile<DMA, CODES, F32>(a, s)
+         : a.y_dtype == F16 ? launch_tile<DMA, CODES, F16>(a, s)
+                            : launch_tile<DMA, CODES, BF16>(a, s);
+}
+
 hipError_t one(const GemmI8& a, hipStream_t s) {
   if (a.m > 128) {
     // 16-byte units inside rows, and a tile inside 31-bit offsets
     const bool dma = a.d % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 &&
                      a.ld_x % 16 == 0 && a.ld_w % 16 == 0 && std::max(a.ld_x, a.ld_w) < ((int64_t)1 << 22);
-    if (dma) return a.z ? launch_tile<true, true>(a, s) : launch_tile<true, false>(a, s);
-    return a.z ? launch_tile<false, true>(a, s) : launch_tile<false, false>(a, s);
+    if (dma) return a.z ? tile_type<true, true>(a, s) : tile_type<true, false>(a, s);
+    return a.z ? tile_type<false, true>(a, s) : tile_type<false, false>(a, s);
   }
   hipLaunchKernelGGL(byte_gemm_kernel, dim3((unsigned)((a.m + 63) / 64), (unsigned)((a.rows + 63) / 64)), dim3(256), 0, s, a);
   return hipGetLastError();
