@@ -137,7 +137,8 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
   const int nst = (a.d + KB - 1) / KB;
 
   // unit q of a thread: LDS unit 256 q + tid, row / UN, in which column unit (u ^ swizzle) of the row lies
-  auto swizzle = [](int row) { return UN == 8 ? (row & 7) : ((row >> 1) & 3); };
+  // (an operand read takes 16 lanes a cycle, rows r .. r + 15 of one unit, over 64 banks: 256 bytes)
+  auto swizzle = [](int row) { return UN == 8 ? ((row >> 1) & 7) : ((row >> 2) & 3); };
   constexpr uint32_t OOB = 0x80000000u;           // beyond any descriptor's range: reads as zero
   const int64_t mrows = min((int64_t)BT, a.m - m0), nrows = min((int64_t)BT, a.rows - n0);
   const int8_t* xb = a.x + m0 * a.ld_x;
