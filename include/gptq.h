@@ -518,8 +518,8 @@ gptq_status_t gptq_norm_quant(const gptq_norm_quant_t *a, const void *x, const v
  *             gptq_byte_gemm_workspace_bytes(m, rows, d) bytes, long sums are split across workgroups where there
  *             are few outputs; with less they are not. The result is the same bit for bit. Not shared with a
  *             concurrent call, two captured graphs included.
- * Sums are exact whole numbers; the result is rounded to fp32 four times at most (the sum, each product with a
- * scale, the difference for zeros is exact) and once to y_dtype. 16-byte accesses are used where pointers and
+ * Sums are exact whole numbers (rounded to 53 bits where a zero beyond 2^28 takes them past that); the result is
+ * rounded to fp32 three times (the sum, each product with a scale) and once to y_dtype. 16-byte accesses are used where pointers and
  * pitches allow them. Launches on `stream` alone; the call may be captured in a graph.
  */
 gptq_status_t gptq_byte_gemm(const int8_t *x, int64_t m, int64_t ld_x, const float *x_scales, const void *w,

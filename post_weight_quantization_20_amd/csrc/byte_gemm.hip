@@ -35,16 +35,10 @@ struct GemmI8 {
 };
 
 // One output from its whole sum and its row's sum of x: fp32 roundings of the sum and of two products. The whole
-// number is exact in a double below 2^53 (|xsum| is below 2^24), and in 64 bits for any zero.
+// number is exact in a double below 2^53, which only zeros beyond 2^28 (|xsum| is below 2^24) can pass.
 template <bool CODES>
 GPTQ_DEV float output(int sum, int xsum, int zero, float xs, float ws) {
-  float v = (float)sum;
-  if constexpr (CODES) {
-    if (__builtin_expect(zero > -(1 << 28) && zero < (1 << 28), 1))
-      v = (float)__builtin_fma((double)(128 - zero), (double)xsum, (double)sum);
-    else
-      v = (float)((int64_t)sum + (128 - (int64_t)zero) * xsum);
-  }
+  const float v = CODES ? (float)__builtin_fma(128.0 - (double)zero, (double)xsum, (double)sum) : (float)sum;
   return v * xs * ws;
 }
 
@@ -59,12 +53,9 @@ GPTQ_DEV i32x4 bytes16(const void* row, int k, int d) {
   return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
 }
 
-template <bool CODES>
-GPTQ_DEV i32x4 as_signed(i32x4 v) {
-  if constexpr (CODES) {
+GPTQ_DEV i32x4 flip(i32x4 v) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] ^= (int)0x80808080;
-  }
+  for (int e = 0; e < 4; ++e) v[e] ^= (int)0x80808080;
   return v;
 }
 
@@ -83,31 +74,18 @@ GPTQ_DEV void store_one(const GemmI8& a, int64_t i, int64_t r, float v) {
 
 // ------------------------------------------------------------------ tiles
 //
-// Stages of KB columns of 256 rows of each operand stream into LDS 16 bytes a lane (buffer_load ... lds), through a
-// ring of NST stages; units of a row are XOR-swizzled so that the 32 rows of an operand read fall in distinct
-// banks. Columns past d and rows past the last read as zeros through the descriptor's range. Rows that are not
-// 16-byte aligned, or whose width is not a multiple of 16, are staged through registers instead.
-constexpr int BT = 256;        // tile edge
-constexpr int GROUP = 8;       // row tiles that run side by side
-
-GPTQ_DEV void dma16(i32x4 rsrc, uint32_t voff, uint32_t lds_addr) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds_addr)
-               : "memory");
-}
-
-// Waits until at most N of this thread's loads into LDS are in flight and all its LDS reads are done, then meets
-// the workgroup. The builtin tells the compiler that no LDS read is pending; the loads it does not track.
-template <int N>
-GPTQ_DEV void stage_barrier() {
-  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-GPTQ_DEV i32x4 descriptor(const void* base, int64_t bytes) {
-  const uint64_t b = (uint64_t)(uintptr_t)base;
-  return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)b), __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)),
-               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
-}
+// Stages of 128 columns of 256 rows of each operand go to LDS by way of registers: a thread loads 16 units of 16 bytes
+// of stage s + 2 while stage s is multiplied, and each is written to LDS a whole stage later, so that every load has
+// that long to arrive and neither loads nor writes come in bursts that matrix instructions would queue behind (loads
+// straight into LDS have to wait for their buffer: 4096 x 4096 x 65536 in 1030 us with them). Units of a row are
+// XOR-swizzled so that the 16 rows of an operand read's cycle fall in distinct banks. Columns past d and rows past
+// the last read as zeros through the descriptor's range; where rows are not 4-byte aligned or d is no multiple of 16
+// the loads are ordinary ones with masks. Codes are flipped, and the rows of x summed, on their way through registers.
+constexpr int BT = 256;                 // tile edge
+constexpr int KB = 128;                 // columns of a stage
+constexpr int OPB = BT * KB;            // bytes of an operand's stage
+constexpr int STAGEB = 2 * OPB;
+constexpr int GROUP = 8;                // row tiles that run side by side
 
 // Tile of a workgroup: XCD b % 8 takes a contiguous run of an order in which GROUP row tiles run side by side
 // through the column tiles, so that what its L2 holds is shared.
@@ -122,11 +100,8 @@ GPTQ_DEV bool tile_of(const GemmI8& a, uint32_t b, uint32_t& tm, uint32_t& tn) {
   return true;
 }
 
-template <int KB, int NST, bool DMA, bool CODES, int YT>
+template <bool WHOLE, bool CODES, int YT>
 __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
-  constexpr int UN = KB / 16, KS = KB / 32;       // units of a row, products of 32 columns
-  constexpr int OPB = BT * KB, STAGEB = 2 * OPB;  // bytes of an operand and of a stage
-  constexpr int LOADS = OPB / 16 / 256;           // units a thread stages of each operand
   extern __shared__ __align__(16) char smem_raw[];
   GPTQ_LDS char* lds = (GPTQ_LDS char*)smem_raw;
   uint32_t tm, tn;
@@ -136,64 +111,53 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
   const int wm = wave >> 1, wn = wave & 1, col = lane & 31, half = lane >> 5;
   const int nst = (a.d + KB - 1) / KB;
 
-  // unit q of a thread: LDS unit 256 q + tid, row / UN, in which column unit (u ^ swizzle) of the row lies
-  // (an operand read takes 16 lanes a cycle, rows r .. r + 15 of one unit, over 64 banks: 256 bytes)
-  auto swizzle = [](int row) { return UN == 8 ? ((row >> 1) & 7) : ((row >> 2) & 3); };
-  constexpr uint32_t OOB = 0x80000000u;           // beyond any descriptor's range: reads as zero
+  // staging: unit q of a thread is row 32 q + tid / 8 of the tile, LDS unit tid % 8 of that row, which holds column
+  // unit (tid % 8) ^ swizzle(row)
   const int64_t mrows = min((int64_t)BT, a.m - m0), nrows = min((int64_t)BT, a.rows - n0);
   const int8_t* xb = a.x + m0 * a.ld_x;
   const uint8_t* wb = a.w + n0 * a.ld_w;
-  int srow[LOADS], scol[LOADS];
-  uint32_t xo[LOADS], wo[LOADS];
-#pragma unroll
-  for (int q = 0; q < LOADS; ++q) {
-    const int u = 256 * q + tid;
-    srow[q] = u / UN;
-    scol[q] = 16 * ((u % UN) ^ swizzle(u / UN));
-    xo[q] = (uint32_t)(srow[q] * a.ld_x + scol[q]);
-    wo[q] = (uint32_t)(srow[q] * a.ld_w + scol[q]);
-    if (srow[q] >= mrows) xo[q] = OOB;
-    if (srow[q] >= nrows) wo[q] = OOB;
-  }
-  auto issue = [&](int s) {
-    const int k0 = s * KB;
-    GPTQ_LDS char* dst = lds + (s % NST) * STAGEB;
-    if constexpr (DMA) {
-      const i32x4 xr = descriptor(xb + k0, (mrows - 1) * a.ld_x + a.d - k0),
-                  wr = descriptor(wb + k0, (nrows - 1) * a.ld_w + a.d - k0);
-      const uint32_t base = (uint32_t)(uintptr_t)dst + 1024 * wave;
-      const bool last = k0 + KB > a.d;            // columns past d would be the next row's
-#pragma unroll
-      for (int q = 0; q < LOADS; ++q) dma16(xr, last && k0 + scol[q] >= a.d ? OOB : xo[q], base + 4096 * q);
-#pragma unroll
-      for (int q = 0; q < LOADS; ++q) dma16(wr, last && k0 + scol[q] >= a.d ? OOB : wo[q], base + OPB + 4096 * q);
+  const int srow = tid >> 3, scol = 16 * ((tid & 7) ^ ((srow >> 1) & 7));
+  i32x4 st[16];                                   // 8 units of x, 8 of w
+  auto fetch = [&](int s, int q) {
+    const int k0 = s * KB, e = q & 7;
+    const bool isx = q < 8;
+    const int64_t ld = isx ? a.ld_x : a.ld_w, rows = isx ? mrows : nrows;
+    const char* base = (isx ? reinterpret_cast<const char*>(xb) : reinterpret_cast<const char*>(wb)) + k0;
+    if constexpr (WHOLE) {
+      // past d: beyond the descriptor's range, as rows past the last are (ld >= d)
+      const int bytes = s < nst ? (int)((rows - 1) * ld + a.d - k0) : 0;
+      const uint32_t off = k0 + scol < a.d ? (uint32_t)((srow + 32 * e) * (int)ld + scol) : 0x80000000u;
+      st[q] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bytes, 0x00020000), off, 0, 0));
     } else {
-      i32x4 xv[LOADS], wv[LOADS];
-#pragma unroll
-      for (int q = 0; q < LOADS; ++q) {
-        xv[q] = wv[q] = i32x4{0, 0, 0, 0};
-        if (k0 + scol[q] < a.d) {
-          if (srow[q] < mrows) xv[q] = bytes16(xb + srow[q] * a.ld_x, k0 + scol[q], a.d);
-          if (srow[q] < nrows) wv[q] = bytes16(wb + srow[q] * a.ld_w, k0 + scol[q], a.d);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < LOADS; ++q) {
-        *(GPTQ_LDS i32x4*)(dst + 4096 * q + 16 * tid) = xv[q];
-        *(GPTQ_LDS i32x4*)(dst + OPB + 4096 * q + 16 * tid) = wv[q];
-      }
+      const int row = srow + 32 * e;
+      st[q] = i32x4{0, 0, 0, 0};
+      if (k0 + scol < a.d && row < rows) st[q] = bytes16(base - k0 + row * ld, k0 + scol, a.d);
     }
+  };
+  int xsum[8] = {0, 0, 0, 0, 0, 0, 0, 0};         // of rows 32 q + tid / 8: this thread's columns
+  auto put = [&](int s, int q) {
+    i32x4 v = st[q];
+    if constexpr (CODES) {
+      if (q < 8) xsum[q] = add_bytes(v, xsum[q]);
+      else v = flip(v);
+    }
+    *(GPTQ_LDS i32x4*)(lds + (s & 1) * STAGEB + 4096 * q + 16 * tid) = v;
   };
 
   // operand reads: row 32 i + col of the wave's 128, unit 2 ks + half
-  const int xrow = (128 * wm + col) * KB, wrow = OPB + (128 * wn + col) * KB;
-  const int sw = swizzle(col);
-  auto read = [&](int s, int ks, i32x4 (&xv)[4], i32x4 (&wv)[4], int i0, int i1) {
-    GPTQ_LDS char* b = lds + (s % NST) * STAGEB + (((2 * ks + half) ^ sw) << 4);
+  const int xrow = (128 * wm + col) * KB, wrow = OPB + (128 * wn + col) * KB, sw = (col >> 1) & 7;
+  struct Step {
+    i32x4 x[4], w[4];
+  };
+  // a quarter of a step's operands: two blocks of w, the others of w, two of x, the others of x
+  auto read = [&](int s, int ks, Step& o, int quarter) {
+    GPTQ_LDS char* b = lds + (s & 1) * STAGEB + (((2 * ks + half) ^ sw) << 4);
 #pragma unroll
-    for (int i = i0; i < i1; ++i) {
-      xv[i] = *(GPTQ_LDS i32x4*)(b + xrow + 32 * KB * i);
-      wv[i] = *(GPTQ_LDS i32x4*)(b + wrow + 32 * KB * i);
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * (quarter & 1) + e;
+      if (quarter < 2) o.w[i] = *(GPTQ_LDS i32x4*)(b + wrow + 32 * KB * i);
+      else o.x[i] = *(GPTQ_LDS i32x4*)(b + xrow + 32 * KB * i);
     }
   };
   i32x16 acc[4][4];
@@ -201,81 +165,48 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
-  int xsum[4] = {0, 0, 0, 0};
-  auto multiply = [&](const i32x4 (&xv)[4], i32x4 (&wv)[4], int i0, int i1) {   // from i0 = 0 on, in order
-    if (i0 == 0) {
+
+  // A step multiplies operands that are in registers while the next step's are read, in quarters; with each quarter a
+  // unit of stage s goes to LDS and its register takes one of stage s + 1. The barrier before a stage's last step
+  // says that every wave has read that stage to its end and written the next one.
+  auto step = [&](Step& cur, Step& next, int s, int ks, int to, int q0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wv[j] = as_signed<CODES>(wv[j]);
-    }
+    for (int i = 0; i < 4; ++i) {
+      read(s, ks, next, i);
+      put(to, q0 + i);
+      fetch(to + 1, q0 + i);
 #pragma unroll
-    for (int i = i0; i < i1; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[j], xv[i], acc[i][j], 0, 0, 0);
-      if constexpr (CODES) xsum[i] = add_bytes(xv[i], xsum[i]);
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(cur.w[j], cur.x[i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-
-  if constexpr (DMA) {
-    constexpr int L = 2 * LOADS;                  // loads of a thread a stage
-    for (int s = 0; s < NST && s < nst; ++s) issue(s);
-    if (nst >= NST) stage_barrier<(NST - 1) * L>();
-    else stage_barrier<0>();
-    i32x4 x0[4], w0[4], x1[4], w1[4];
-    read(0, 0, x0, w0, 0, 4);
-    for (int it = 0; it < nst; ++it) {
-      // All steps of the stage but the last, each under the reads of the next one's operands.
 #pragma unroll
-      for (int ks = 0; ks + 1 < KS; ++ks) {
-        __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0): this step's operands, read a step ago
-        if (ks & 1) {
-          read(it, ks + 1, x0, w0, 0, 4);
-          multiply(x1, w1, 0, 4);
-        } else {
-          read(it, ks + 1, x1, w1, 0, 4);
-          multiply(x0, w0, 0, 4);
-        }
+  for (int q = 0; q < 16; ++q) fetch(0, q);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // two MFMAs
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
-        }
-      }
-      // The last step (its operands are in x1, w1): stage it is read to the end by every wave and stage it + 1 has
-      // arrived behind the barrier, so the loads of stage it + NST go out and the first operands of stage it + 1
-      // are read while it multiplies (after the last stage those reads are stale and not used).
-      if (it + NST <= nst) stage_barrier<(NST - 2) * L>();
-      else stage_barrier<0>();
-      read(it + 1, 0, x0, w0, 0, 2);
-      multiply(x1, w1, 0, 2);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 1);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
-      }
-      if (it + NST < nst) issue(it + NST);
-      read(it + 1, 0, x0, w0, 2, 4);
-      multiply(x1, w1, 2, 4);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 2);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 2);
-      }
-    }
-    stage_barrier<0>();
-  } else {
-    issue(0);
-    for (int it = 0; it < nst; ++it) {
-      __syncthreads();
-      if (it + 1 < nst) issue(it + 1);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        i32x4 xv[4], wv[4];
-        read(it, ks, xv, wv, 0, 4);
-        multiply(xv, wv, 0, 4);
-      }
-    }
-    __syncthreads();
+  for (int q = 0; q < 16; ++q) {
+    put(0, q);
+    fetch(1, q);
   }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    put(1, q);
+    fetch(2, q);
+  }
+  __syncthreads();
+  Step even, odd;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) read(0, 0, even, q);
+  for (int it = 0; it < nst; ++it) {
+    step(even, odd, it, 1, it + 1, 4);
+    step(odd, even, it, 2, it + 1, 8);
+    step(even, odd, it, 3, it + 1, 12);
+    // LDS reads and writes done, loads still on their way
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_barrier" ::: "memory");
+    step(odd, even, it + 1, 0, it + 2, 0);        // what this reads after the last stage is not used
+  }
+  __syncthreads();
 
   // Register e of lane l: output 8 (e / 4) + 4 (l / 32) + e % 4 of block j, token l % 32 of block i. Outputs leave
   // through LDS, 32 tokens by the wave's 128 outputs at a time, so that a token's come side by side.
@@ -285,10 +216,19 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
   GPTQ_LDS char* area = lds + wave * 32 * (128 * 4 + 16);
   GPTQ_LDS float* ws = (GPTQ_LDS float*)(lds + 4 * 32 * (128 * 4 + 16));
   GPTQ_LDS int32_t* zs = (GPTQ_LDS int32_t*)(ws + BT);
+  GPTQ_LDS int32_t* sums = zs + BT;
   {
     const int64_t r = min(n0 + tid, a.rows - 1);
     ws[tid] = a.ws ? a.ws[r] : 1.0f;
-    if constexpr (CODES) zs[tid] = a.z[r];
+    if constexpr (CODES) {
+      zs[tid] = a.z[r];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) xsum[q] += __shfl_xor(xsum[q], o, 64);
+        if ((tid & 7) == 0) sums[32 * q + srow] = xsum[q];
+      }
+    }
   }
   float xs[4];
 #pragma unroll
@@ -298,7 +238,7 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t mr = m0 + 128 * wm + 32 * i;
-    if constexpr (CODES) xsum[i] += __shfl_xor(xsum[i], 32, 64);
+    const int xsm = CODES ? sums[128 * wm + 32 * i + col] : 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -309,7 +249,7 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
         if constexpr (CODES) z4 = *(GPTQ_LDS i32x4*)(zs + 128 * wn + c);
         T4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = (T)output<CODES>(acc[i][j][4 * b + e], xsum[i], z4[e], xs[i], w4[e]);
+        for (int e = 0; e < 4; ++e) o[e] = (T)output<CODES>(acc[i][j][4 * b + e], xsm, z4[e], xs[i], w4[e]);
         *(GPTQ_LDS T4*)(area + col * PITCH + c * ESZ) = o;
       }
     __builtin_amdgcn_wave_barrier();
@@ -343,12 +283,10 @@ __global__ __launch_bounds__(256) void byte_gemm_kernel(GemmI8 a) {
   const uint8_t* w = a.w + r * a.ld_w;
   i32x16 acc = {};
   int xsum = 0;
-  const int flip = a.z ? (int)0x80808080 : 0;
   for (int k = 0; k < a.d; k += 32) {
     const i32x4 xf = bytes16(x, k + 16 * half, a.d);
     i32x4 wf = bytes16(w, k + 16 * half, a.d);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) wf[e] ^= flip;   // past the last column the row of x is zero
+    if (a.z) wf = flip(wf);   // past the last column the row of x is zero
     xsum = add_bytes(xf, xsum);
     acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(xf, wf, acc, 0, 0, 0);
   }
@@ -378,13 +316,11 @@ hipError_t ask_lds(K kernel, size_t lds, std::atomic<uint64_t>& asked) {
   return hipSuccess;
 }
 
-constexpr int kKB = 128, kNST = 2;
-
-template <bool DMA, bool CODES, int YT>
+template <bool WHOLE, bool CODES, int YT>
 hipError_t launch_tile(const GemmI8& a, hipStream_t s) {
   static std::atomic<uint64_t> asked{0};
-  constexpr size_t lds = (size_t)kNST * 2 * BT * kKB;
-  auto f = tile_kernel<kKB, kNST, DMA, CODES, YT>;
+  constexpr size_t lds = 2 * STAGEB;
+  auto f = tile_kernel<WHOLE, CODES, YT>;
   const hipError_t e = ask_lds(f, lds, asked);
   if (e != hipSuccess) return e;
   const uint32_t per = (a.tiles_m * a.tiles_n + 7) / 8;
@@ -392,19 +328,20 @@ hipError_t launch_tile(const GemmI8& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool DMA, bool CODES>
+template <bool WHOLE, bool CODES>
 hipError_t tile_type(const GemmI8& a, hipStream_t s) {
-  return a.y_dtype == F32   ? launch_tile<DMA, CODES, F32>(a, s)
-         : a.y_dtype == F16 ? launch_tile<DMA, CODES, F16>(a, s)
-                            : launch_tile<DMA, CODES, BF16>(a, s);
+  return a.y_dtype == F32   ? launch_tile<WHOLE, CODES, F32>(a, s)
+         : a.y_dtype == F16 ? launch_tile<WHOLE, CODES, F16>(a, s)
+                            : launch_tile<WHOLE, CODES, BF16>(a, s);
 }
 
 hipError_t one(const GemmI8& a, hipStream_t s) {
   if (a.m > 128) {
-    // 16-byte units inside rows, and a tile inside 31-bit offsets
-    const bool dma = a.d % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 &&
-                     a.ld_x % 16 == 0 && a.ld_w % 16 == 0 && std::max(a.ld_x, a.ld_w) < ((int64_t)1 << 22);
-    if (dma) return a.z ? tile_type<true, true>(a, s) : tile_type<true, false>(a, s);
+    // 16-byte units inside rows of whole words, and a tile inside 31-bit offsets
+    const bool whole = a.d % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 4 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.w) % 4 == 0 && a.ld_x % 4 == 0 && a.ld_w % 4 == 0 &&
+                       std::max(a.ld_x, a.ld_w) < ((int64_t)1 << 22);
+    if (whole) return a.z ? tile_type<true, true>(a, s) : tile_type<true, false>(a, s);
     return a.z ? tile_type<false, true>(a, s) : tile_type<false, false>(a, s);
   }
   hipLaunchKernelGGL(byte_gemm_kernel, dim3((unsigned)((a.m + 63) / 64), (unsigned)((a.rows + 63) / 64)), dim3(256), 0, s, a);
