@@ -514,20 +514,13 @@ gptq_status_t gptq_norm_quant(const gptq_norm_quant_t *a, const void *x, const v
  *             overflow: GPTQ_EUNSUPPORTED).
  *   y         device array [m x ld_y] of y_dtype (GPTQ_F32, GPTQ_F16 or GPTQ_BF16), output, ld_y >= rows; apart
  *             from the other arrays.
- *   work      device workspace of work_bytes bytes (16-byte aligned), or NULL. With at least
- *             gptq_byte_gemm_workspace_bytes(m, rows, d) bytes, long sums are split across workgroups where there
- *             are few outputs; with less they are not. The result is the same bit for bit. Not shared with a
- *             concurrent call, two captured graphs included.
  * Sums are exact whole numbers (rounded to 53 bits where a zero beyond 2^28 takes them past that); the result is
  * rounded to fp32 three times (the sum, each product with a scale) and once to y_dtype. 16-byte accesses are used where pointers and
  * pitches allow them. Launches on `stream` alone; the call may be captured in a graph.
  */
 gptq_status_t gptq_byte_gemm(const int8_t *x, int64_t m, int64_t ld_x, const float *x_scales, const void *w,
                              int64_t ld_w, const float *w_scales, const int32_t *zeros, int64_t rows, int64_t d,
-                             void *y, int32_t y_dtype, int64_t ld_y, void *work, size_t work_bytes, void *stream);
-
-/* Workspace bytes with which gptq_byte_gemm splits its sums; 0 when it would not (or for invalid arguments). */
-size_t gptq_byte_gemm_workspace_bytes(int64_t m, int64_t rows, int64_t d);
+                             void *y, int32_t y_dtype, int64_t ld_y, void *stream);
 
 /*
  * A paged cache of keys and values in 8 bits. A page holds page_size tokens; a key or value stands for its code

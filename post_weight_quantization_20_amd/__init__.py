@@ -15,7 +15,6 @@ from .attention import (  # noqa: F401
 )
 from .serving import (  # noqa: F401
     gptq_byte_gemm,
-    gptq_byte_gemm_workspace_bytes,
     gptq_kv_append,
     gptq_kv_attention,
     gptq_kv_attention_workspace_bytes,

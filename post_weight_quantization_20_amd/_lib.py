@@ -113,8 +113,7 @@ SIGNATURES = {
     "gptq_attention_workspace_bytes": (c_size_t, [ctypes.POINTER(gptq_attention_t)]),
     "gptq_norm_quant": (c_int32, [ctypes.POINTER(gptq_norm_quant_t)] + [c_void_p] * 8),
     "gptq_byte_gemm": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64,
-                                 c_int64, c_void_p, c_int32, c_int64, c_void_p, c_size_t, c_void_p]),
-    "gptq_byte_gemm_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+                                 c_int64, c_void_p, c_int32, c_int64, c_void_p]),
     "gptq_kv_append": (c_int32, [ctypes.POINTER(gptq_kv_append_t), ctypes.POINTER(gptq_kv_cache_t)] + [c_void_p] * 9),
     "gptq_kv_attention": (c_int32, [ctypes.POINTER(gptq_kv_attention_t), ctypes.POINTER(gptq_kv_cache_t)] +
                           [c_void_p] * 7 + [c_size_t, c_void_p]),

@@ -445,14 +445,9 @@ gptq_status_t gptq_norm_quant(const gptq_norm_quant_t* a, const void* x, const v
 
 static constexpr int64_t kMaxInt8Sum = 131071;   // d * 128 * 128 < 2^31
 
-size_t gptq_byte_gemm_workspace_bytes(int64_t m, int64_t rows, int64_t d) {
-  if (m <= 0 || m > kMaxDim || rows <= 0 || rows > kMaxRows || d < 1 || d > kMaxInt8Sum) return 0;
-  return gptq::byte_gemm_workspace_bytes(m, rows, d);
-}
-
 gptq_status_t gptq_byte_gemm(const int8_t* x, int64_t m, int64_t ld_x, const float* x_scales, const void* w,
                              int64_t ld_w, const float* w_scales, const int32_t* zeros, int64_t rows, int64_t d,
-                             void* y, int32_t y_dtype, int64_t ld_y, void* work, size_t work_bytes, void* stream) {
+                             void* y, int32_t y_dtype, int64_t ld_y, void* stream) {
   if (m < 0 || m > kMaxDim || rows < 0 || rows > kMaxRows || d < 1 || d > kMaxDim || !dtype_ok(y_dtype))
     return GPTQ_EINVAL;
   if (ld_x < d || ld_w < d || ld_y < rows) return GPTQ_EINVAL;
@@ -464,9 +459,8 @@ gptq_status_t gptq_byte_gemm(const int8_t* x, int64_t m, int64_t ld_x, const flo
   if (!apart(ty, tx) || !apart(ty, tw) || !ranges_apart(y, ty.bytes(), x_scales, 4 * m) ||
       !ranges_apart(y, ty.bytes(), w_scales, 4 * rows) || !ranges_apart(y, ty.bytes(), zeros, 4 * rows))
     return GPTQ_EINVAL;
-  if (reinterpret_cast<uintptr_t>(work) % 16 != 0) return GPTQ_EINVAL;
-  return hip_status(gptq::byte_gemm(x, m, ld_x, x_scales, w, ld_w, w_scales, zeros, rows, d, y, y_dtype, ld_y, work,
-                                    work ? work_bytes : 0, static_cast<hipStream_t>(stream)));
+  return hip_status(gptq::byte_gemm(x, m, ld_x, x_scales, w, ld_w, w_scales, zeros, rows, d, y, y_dtype, ld_y,
+                                    static_cast<hipStream_t>(stream)));
 }
 
 namespace {

@@ -5,11 +5,10 @@
 // formed beside the product. All sums are exact whole numbers in 32 bits for d <= 131071 (each product is at most
 // 2^14), so any order and any split gives the same bits.
 //
-// Three kernels, by the number of tokens:
+// Two kernels:
 //   tile    256 x 256 outputs a workgroup (4 waves of 128 x 128, v_mfma_i32_32x32x32_i8), operands through LDS
-//   strip   up to 128 tokens x 64 outputs a workgroup, whose waves share the sum over k and read both operands
-//           straight from memory: each byte of w is used by one wave
-//   token   up to 16 tokens x 16 outputs (v_mfma_i32_16x16x64_i8), eight waves sharing the sum
+//   strip   up to 128 tokens and as many outputs as give each CU a workgroup, whose waves share the sum over k and read
+//           both operands straight from memory
 #include "common.hpp"
 
 #include <atomic>
@@ -32,6 +31,7 @@ struct GemmI8 {
   int d, y_dtype;
   int y_vec;              // rows of y take 16-byte stores
   uint32_t tiles_m, tiles_n;
+  uint32_t whole_tiles, cut;   // tiles of whole rounds; parts of each other tile
 };
 
 // One output from its whole sum and its row's sum of x: fp32 roundings of the sum and of two products. The whole
@@ -65,13 +65,6 @@ GPTQ_DEV int add_bytes(i32x4 v, int sum) {
   return sum;
 }
 
-GPTQ_DEV void store_one(const GemmI8& a, int64_t i, int64_t r, float v) {
-  const int64_t at = i * a.ld_y + r;
-  if (a.y_dtype == F32) static_cast<float*>(a.y)[at] = v;
-  else if (a.y_dtype == F16) static_cast<_Float16*>(a.y)[at] = (_Float16)v;
-  else static_cast<__bf16*>(a.y)[at] = (__bf16)v;
-}
-
 // ------------------------------------------------------------------ tiles
 //
 // Stages of 128 columns of 256 rows of each operand go to LDS by way of registers: a thread loads 16 units of 16 bytes
@@ -83,44 +76,36 @@ GPTQ_DEV void store_one(const GemmI8& a, int64_t i, int64_t r, float v) {
 // the loads are ordinary ones with masks. Codes are flipped, and the rows of x summed, on their way through registers.
 constexpr int BT = 256;                 // tile edge
 constexpr int KB = 128;                 // columns of a stage
-constexpr int OPB = BT * KB;            // bytes of an operand's stage
-constexpr int STAGEB = 2 * OPB;
 constexpr int GROUP = 8;                // row tiles that run side by side
+constexpr uint32_t kStripTiles = 96;    // fewer quarter tiles than this: strips
 
-// Tile of a workgroup: XCD b % 8 takes a contiguous run of an order in which GROUP row tiles run side by side
-// through the column tiles, so that what its L2 holds is shared.
-GPTQ_DEV bool tile_of(const GemmI8& a, uint32_t b, uint32_t& tm, uint32_t& tn) {
-  const uint32_t total = a.tiles_m * a.tiles_n, per = (total + 7) / 8;
-  const uint32_t slot = (b & 7) * per + (b >> 3);
-  if ((b >> 3) >= per || slot >= total) return false;
+// Tile `slot` of an order in which GROUP row tiles run side by side through the column tiles.
+GPTQ_DEV void tile_at(const GemmI8& a, uint32_t slot, uint32_t& tm, uint32_t& tn) {
   const uint32_t span = GROUP * a.tiles_n, grp = slot / span, in = slot - grp * span;
   const uint32_t height = min((uint32_t)GROUP, a.tiles_m - grp * GROUP);
   tm = grp * GROUP + in % height;
   tn = in / height;
-  return true;
 }
 
-template <bool WHOLE, bool CODES, int YT>
-__global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
-  extern __shared__ __align__(16) char smem_raw[];
-  GPTQ_LDS char* lds = (GPTQ_LDS char*)smem_raw;
-  uint32_t tm, tn;
-  if (!tile_of(a, blockIdx.x, tm, tn)) return;
-  const int64_t m0 = (int64_t)tm * BT, n0 = (int64_t)tn * BT;
+// One tile of 64 XI tokens by 64 WJ outputs from (m0, n0) on, by 2 x 2 waves of XI x WJ blocks of 32 x 32.
+template <int XI, int WJ, bool WHOLE, bool CODES, int YT>
+GPTQ_DEV void tile(const GemmI8& a, int64_t m0, int64_t n0, GPTQ_LDS char* lds) {
+  constexpr int BM = 64 * XI, BN = 64 * WJ, STAGE = (BM + BN) * KB;
+  constexpr int QX = 2 * XI, NQ = QX + 2 * WJ;    // units that a thread stages of x, and in all
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, col = lane & 31, half = lane >> 5;
   const int nst = (a.d + KB - 1) / KB;
 
-  // staging: unit q of a thread is row 32 q + tid / 8 of the tile, LDS unit tid % 8 of that row, which holds column
-  // unit (tid % 8) ^ swizzle(row)
-  const int64_t mrows = min((int64_t)BT, a.m - m0), nrows = min((int64_t)BT, a.rows - n0);
+  // staging: unit q of a thread is row 32 q + tid / 8 of an operand's tile, LDS unit tid % 8 of that row, which holds
+  // column unit (tid % 8) ^ swizzle(row)
+  const int64_t mrows = min((int64_t)BM, a.m - m0), nrows = min((int64_t)BN, a.rows - n0);
   const int8_t* xb = a.x + m0 * a.ld_x;
   const uint8_t* wb = a.w + n0 * a.ld_w;
   const int srow = tid >> 3, scol = 16 * ((tid & 7) ^ ((srow >> 1) & 7));
-  i32x4 st[16];                                   // 8 units of x, 8 of w
+  i32x4 st[NQ];
   auto fetch = [&](int s, int q) {
-    const int k0 = s * KB, e = q & 7;
-    const bool isx = q < 8;
+    const int k0 = s * KB, e = q < QX ? q : q - QX;
+    const bool isx = q < QX;
     const int64_t ld = isx ? a.ld_x : a.ld_w, rows = isx ? mrows : nrows;
     const char* base = (isx ? reinterpret_cast<const char*>(xb) : reinterpret_cast<const char*>(wb)) + k0;
     if constexpr (WHOLE) {
@@ -135,72 +120,74 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
       if (k0 + scol < a.d && row < rows) st[q] = bytes16(base - k0 + row * ld, k0 + scol, a.d);
     }
   };
-  int xsum[8] = {0, 0, 0, 0, 0, 0, 0, 0};         // of rows 32 q + tid / 8: this thread's columns
+  int xsum[QX] = {};                              // of rows 32 q + tid / 8: this thread's columns
   auto put = [&](int s, int q) {
     i32x4 v = st[q];
     if constexpr (CODES) {
-      if (q < 8) xsum[q] = add_bytes(v, xsum[q]);
+      if (q < QX) xsum[q] = add_bytes(v, xsum[q]);
       else v = flip(v);
     }
-    *(GPTQ_LDS i32x4*)(lds + (s & 1) * STAGEB + 4096 * q + 16 * tid) = v;
+    *(GPTQ_LDS i32x4*)(lds + (s & 1) * STAGE + 4096 * q + 16 * tid) = v;
   };
 
-  // operand reads: row 32 i + col of the wave's 128, unit 2 ks + half
-  const int xrow = (128 * wm + col) * KB, wrow = OPB + (128 * wn + col) * KB, sw = (col >> 1) & 7;
+  // operand reads: row 32 i + col of the wave's, unit 2 ks + half
+  const int xrow = (32 * XI * wm + col) * KB, wrow = BM * KB + (32 * WJ * wn + col) * KB, sw = (col >> 1) & 7;
   struct Step {
-    i32x4 x[4], w[4];
+    i32x4 x[XI], w[WJ];
   };
-  // a quarter of a step's operands: two blocks of w, the others of w, two of x, the others of x
-  auto read = [&](int s, int ks, Step& o, int quarter) {
-    GPTQ_LDS char* b = lds + (s & 1) * STAGEB + (((2 * ks + half) ^ sw) << 4);
+  // part i of XI of a step's operands, those of w first
+  auto read = [&](int s, int ks, Step& o, int i) {
+    GPTQ_LDS char* b = lds + (s & 1) * STAGE + (((2 * ks + half) ^ sw) << 4);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = 2 * (quarter & 1) + e;
-      if (quarter < 2) o.w[i] = *(GPTQ_LDS i32x4*)(b + wrow + 32 * KB * i);
-      else o.x[i] = *(GPTQ_LDS i32x4*)(b + xrow + 32 * KB * i);
+    for (int e = i * (XI + WJ) / XI; e < (i + 1) * (XI + WJ) / XI; ++e) {
+      if (e < WJ) o.w[e] = *(GPTQ_LDS i32x4*)(b + wrow + 32 * KB * e);
+      else o.x[e - WJ] = *(GPTQ_LDS i32x4*)(b + xrow + 32 * KB * (e - WJ));
     }
   };
-  i32x16 acc[4][4];
+  i32x16 acc[XI][WJ];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < XI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
+    for (int j = 0; j < WJ; ++j) acc[i][j] = i32x16{};
 
-  // A step multiplies operands that are in registers while the next step's are read, in quarters; with each quarter a
-  // unit of stage s goes to LDS and its register takes one of stage s + 1. The barrier before a stage's last step
-  // says that every wave has read that stage to its end and written the next one.
-  auto step = [&](Step& cur, Step& next, int s, int ks, int to, int q0) {
+  // A step multiplies operands that are in registers while the next step's are read, in parts; with each part some
+  // units of stage `to` go to LDS and their registers take those of stage to + 1. The barrier before a stage's last
+  // step says that every wave has read that stage to its end and written the next one.
+  auto step = [&](Step& cur, Step& next, int s, int ks, int to, int part0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < XI; ++i) {
       read(s, ks, next, i);
-      put(to, q0 + i);
-      fetch(to + 1, q0 + i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int q = (part0 + i) * NQ / (4 * XI); q < (part0 + i + 1) * NQ / (4 * XI); ++q) {
+        put(to, q);
+        fetch(to + 1, q);
+      }
+#pragma unroll
+      for (int j = 0; j < WJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(cur.w[j], cur.x[i], acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 #pragma unroll
-  for (int q = 0; q < 16; ++q) fetch(0, q);
+  for (int q = 0; q < NQ; ++q) fetch(0, q);
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
+  for (int q = 0; q < NQ; ++q) {
     put(0, q);
     fetch(1, q);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < NQ / 4; ++q) {
     put(1, q);
     fetch(2, q);
   }
   __syncthreads();
   Step even, odd;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) read(0, 0, even, q);
+  for (int i = 0; i < XI; ++i) read(0, 0, even, i);
   for (int it = 0; it < nst; ++it) {
-    step(even, odd, it, 1, it + 1, 4);
-    step(odd, even, it, 2, it + 1, 8);
-    step(even, odd, it, 3, it + 1, 12);
+    step(even, odd, it, 1, it + 1, XI);
+    step(odd, even, it, 2, it + 1, 2 * XI);
+    step(even, odd, it, 3, it + 1, 3 * XI);
     // LDS reads and writes done, loads still on their way
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("s_barrier" ::: "memory");
@@ -209,44 +196,44 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
   __syncthreads();
 
   // Register e of lane l: output 8 (e / 4) + 4 (l / 32) + e % 4 of block j, token l % 32 of block i. Outputs leave
-  // through LDS, 32 tokens by the wave's 128 outputs at a time, so that a token's come side by side.
+  // through LDS, 32 tokens by the wave's outputs at a time, so that a token's come side by side.
   typedef typename ElemOf<YT>::T T;
   typedef T T4 __attribute__((ext_vector_type(4)));
-  constexpr int ESZ = sizeof(T), PITCH = 128 * ESZ + 16, UR = 8 * ESZ;   // UR: 16-byte units of a row
-  GPTQ_LDS char* area = lds + wave * 32 * (128 * 4 + 16);
-  GPTQ_LDS float* ws = (GPTQ_LDS float*)(lds + 4 * 32 * (128 * 4 + 16));
-  GPTQ_LDS int32_t* zs = (GPTQ_LDS int32_t*)(ws + BT);
-  GPTQ_LDS int32_t* sums = zs + BT;
-  {
+  constexpr int ESZ = sizeof(T), WC = 32 * WJ, PITCH = WC * ESZ + 16, UR = WC * ESZ / 16;   // UR: 16-byte units of a row
+  GPTQ_LDS char* area = lds + wave * 32 * PITCH;
+  GPTQ_LDS float* ws = (GPTQ_LDS float*)(lds + 4 * 32 * PITCH);
+  GPTQ_LDS int32_t* zs = (GPTQ_LDS int32_t*)(ws + BN);
+  GPTQ_LDS int32_t* sums = zs + BN;
+  if (tid < BN) {
     const int64_t r = min(n0 + tid, a.rows - 1);
     ws[tid] = a.ws ? a.ws[r] : 1.0f;
-    if constexpr (CODES) {
-      zs[tid] = a.z[r];
+    if constexpr (CODES) zs[tid] = a.z[r];
+  }
+  if constexpr (CODES) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < QX; ++q) {
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) xsum[q] += __shfl_xor(xsum[q], o, 64);
-        if ((tid & 7) == 0) sums[32 * q + srow] = xsum[q];
-      }
+      for (int o = 1; o < 8; o <<= 1) xsum[q] += __shfl_xor(xsum[q], o, 64);
+      if ((tid & 7) == 0) sums[32 * q + srow] = xsum[q];
     }
   }
-  float xs[4];
+  float xs[XI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) xs[i] = a.xs ? a.xs[min(m0 + 128 * wm + 32 * i + col, a.m - 1)] : 1.0f;
+  for (int i = 0; i < XI; ++i) xs[i] = a.xs ? a.xs[min(m0 + 32 * (XI * wm + i) + col, a.m - 1)] : 1.0f;
   __syncthreads();
-  const int64_t nc = n0 + 128 * wn;
+  const int64_t nc = n0 + WC * wn;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t mr = m0 + 128 * wm + 32 * i;
-    const int xsm = CODES ? sums[128 * wm + 32 * i + col] : 0;
+  for (int i = 0; i < XI; ++i) {
+    const int64_t mr = m0 + 32 * (XI * wm + i);
+    const int xsm = CODES ? sums[32 * (XI * wm + i) + col] : 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < WJ; ++j)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int c = 32 * j + 8 * b + 4 * half;
-        const floatx4 w4 = *(GPTQ_LDS floatx4*)(ws + 128 * wn + c);
+        const floatx4 w4 = *(GPTQ_LDS floatx4*)(ws + WC * wn + c);
         i32x4 z4 = {};
-        if constexpr (CODES) z4 = *(GPTQ_LDS i32x4*)(zs + 128 * wn + c);
+        if constexpr (CODES) z4 = *(GPTQ_LDS i32x4*)(zs + WC * wn + c);
         T4 o;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = (T)output<CODES>(acc[i][j][4 * b + e], xsm, z4[e], xs[i], w4[e]);
@@ -270,34 +257,156 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
   }
 }
 
-// ------------------------------------------------------------------ strips
-
-// A wave owns 32 x 32 outputs; operands come straight from memory, 16 bytes a lane (v_mfma_i32_32x32x32_i8: lane l
-// holds row l % 32, columns 16 (l / 32) .. + 15 of 32).
-__global__ __launch_bounds__(256) void byte_gemm_kernel(GemmI8 a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = lane & 31, half = lane >> 5;
-  const int64_t i0 = (int64_t)blockIdx.x * 64 + 32 * (wave & 1), r0 = (int64_t)blockIdx.y * 64 + 32 * (wave >> 1);
-  const int64_t i = min(i0 + col, a.m - 1), r = min(r0 + col, a.rows - 1);
-  const int8_t* x = a.x + i * a.ld_x;
-  const uint8_t* w = a.w + r * a.ld_w;
-  i32x16 acc = {};
-  int xsum = 0;
-  for (int k = 0; k < a.d; k += 32) {
-    const i32x4 xf = bytes16(x, k + 16 * half, a.d);
-    i32x4 wf = bytes16(w, k + 16 * half, a.d);
-    if (a.z) wf = flip(wf);   // past the last column the row of x is zero
-    xsum = add_bytes(xf, xsum);
-    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(xf, wf, acc, 0, 0, 0);
+// Workgroups of whole rounds of the 256 CUs take a tile each, XCD b % 8 a contiguous run of them, so that what its L2
+// holds is shared. The tiles of the last round are cut into `cut` parts where that many more workgroups still run at
+// once: 256 x 128 (cut = 2) or 128 x 128 (cut = 4).
+template <bool WHOLE, bool CODES, int YT>
+__global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
+  extern __shared__ __align__(16) char smem_raw[];
+  GPTQ_LDS char* lds = (GPTQ_LDS char*)smem_raw;
+  const uint32_t b = blockIdx.x;
+  uint32_t tm, tn;
+  if (b < a.whole_tiles) {
+    tile_at(a, (b & 7) * (a.whole_tiles >> 3) + (b >> 3), tm, tn);
+    tile<4, 4, WHOLE, CODES, YT>(a, (int64_t)tm * BT, (int64_t)tn * BT, lds);
+    return;
   }
-  xsum += __shfl_xor(xsum, 32, 64);
+  const uint32_t rest = b - a.whole_tiles, t = rest / a.cut, part = rest - t * a.cut;
+  tile_at(a, a.whole_tiles + t, tm, tn);
+  const int64_t m0 = (int64_t)tm * BT, n0 = (int64_t)tn * BT;
+  if (a.cut == 1) {
+    tile<4, 4, WHOLE, CODES, YT>(a, m0, n0, lds);
+  } else if (a.cut == 2) {
+    if (n0 + 128 * part < a.rows) tile<4, 2, WHOLE, CODES, YT>(a, m0, n0 + 128 * part, lds);
+  } else {
+    const int64_t m1 = m0 + 128 * (part >> 1), n1 = n0 + 128 * (part & 1);
+    if (m1 < a.m && n1 < a.rows) tile<2, 2, WHOLE, CODES, YT>(a, m1, n1, lds);
+  }
+}
+
+// ------------------------------------------------------------------ strips
+//
+// 16 MB tokens by 16 NB outputs a workgroup (v_mfma_i32_16x16x64_i8: lane l holds row l % 16 and 16 columns of each 64).
+// The waves share the sum over k in blocks of 128 columns and add their sums up in LDS. Both operands come straight
+// from memory, the next block's while one is multiplied: a byte of w is read by one wave, a line of it by four lanes
+// twice in a row. Few tokens are bound by reading w.
+template <int MB, int NB, int WAVES, bool CODES>
+__global__ __launch_bounds__(64 * WAVES) void strip_kernel(GemmI8 a) {
+  __shared__ int part[WAVES][NB][4][64];
+  __shared__ int sums[WAVES][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int64_t r0 = (int64_t)blockIdx.x * 16 * NB, i0 = (int64_t)blockIdx.y * 16 * MB;
+  const uint8_t* w[NB];
+  const int8_t* x[MB];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int mine = 8 * (e >> 2) + 4 * half + (e & 3);
-    const int xsm = __shfl(xsum, mine, 64);
-    if (i0 + mine < a.m && r0 + col < a.rows)
-      store_one(a, i0 + mine, r0 + col, output<true>(acc[e], xsm, a.z ? a.z[r0 + col] : 128, a.xs ? a.xs[i0 + mine] : 1.0f,
-                                                     a.ws ? a.ws[r0 + col] : 1.0f));
+  for (int j = 0; j < NB; ++j) w[j] = a.w + min(r0 + 16 * j + n, a.rows - 1) * a.ld_w + 16 * g;
+#pragma unroll
+  for (int i = 0; i < MB; ++i) x[i] = a.x + min(i0 + 16 * i + n, a.m - 1) * a.ld_x + 16 * g;
+  i32x4 acc[MB][NB];
+  int xsum[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    xsum[i] = 0;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  }
+  struct Block {
+    i32x4 x[2][MB], w[2][NB];
+  };
+  const int blocks = a.d >> 7;                    // whole ones
+  auto load = [&](int b, Block& o) {
+    if (b >= blocks) return;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) o.w[e][j] = *reinterpret_cast<const Unit*>(w[j] + 128 * b + 64 * e);
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) o.x[e][i] = *reinterpret_cast<const Unit*>(x[i] + 128 * b + 64 * e);
+  };
+  auto multiply = [&](Block& o) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if constexpr (CODES) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) o.w[e][j] = flip(o.w[e][j]);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) xsum[i] = add_bytes(o.x[e][i], xsum[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(o.w[e][j], o.x[e][i], acc[i][j], 0, 0, 0);
+    }
+  };
+  Block even, odd;
+  load(wave, even);
+  for (int b = wave; b < blocks; b += 2 * WAVES) {
+    load(b + WAVES, odd);
+    multiply(even);
+    load(b + 2 * WAVES, even);
+    if (b + WAVES < blocks) multiply(odd);
+  }
+  if ((a.d & 127) && wave == blocks % WAVES) {    // the last, partial block
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = 128 * blocks + 64 * e + 16 * g;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) even.w[e][j] = k < a.d ? bytes16(w[j] - 16 * g, k, a.d) : i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < MB; ++i) even.x[e][i] = k < a.d ? bytes16(x[i] - 16 * g, k, a.d) : i32x4{0, 0, 0, 0};
+    }
+    multiply(even);
+  }
+  // register e of lane l: output 4 (l / 16) + e of block j, token l % 16
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    if (i) __syncthreads();
+    if constexpr (CODES) {
+      xsum[i] += __shfl_xor(xsum[i], 16, 64);
+      xsum[i] += __shfl_xor(xsum[i], 32, 64);
+      if (g == 0) sums[wave][n] = xsum[i];
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[wave][j][e][lane] = acc[i][j][e];
+    __syncthreads();
+    const int64_t t = i0 + 16 * i + n;
+    for (int j = wave; j < NB; j += WAVES) {
+      const int64_t r = r0 + 16 * j + 4 * g;
+      if (t >= a.m || r >= a.rows) continue;
+      int sum[4] = {0, 0, 0, 0}, xsm = 0;
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += part[v][j][e][lane];
+        if constexpr (CODES) xsm += sums[v][n];
+      }
+      const float xs = a.xs ? a.xs[t] : 1.0f;
+      float o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t c = min(r + e, a.rows - 1);
+        o[e] = output<CODES>(sum[e], xsm, CODES ? a.z[c] : 0, xs, a.ws ? a.ws[c] : 1.0f);
+      }
+      auto put = [&](auto* y) {
+        typedef typename std::remove_pointer<decltype(y)>::type T;
+        typedef T T4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+        y += t * a.ld_y + r;
+        if (r + 4 <= a.rows) {
+          *reinterpret_cast<T4*>(y) = T4{(T)o[0], (T)o[1], (T)o[2], (T)o[3]};
+        } else {
+          for (int e = 0; e < 3; ++e)
+            if (r + e < a.rows) y[e] = (T)o[e];
+        }
+      };
+      if (a.y_dtype == F32) put(static_cast<float*>(a.y));
+      else if (a.y_dtype == F16) put(static_cast<_Float16*>(a.y));
+      else put(static_cast<__bf16*>(a.y));
+    }
   }
 }
 
@@ -319,12 +428,12 @@ hipError_t ask_lds(K kernel, size_t lds, std::atomic<uint64_t>& asked) {
 template <bool WHOLE, bool CODES, int YT>
 hipError_t launch_tile(const GemmI8& a, hipStream_t s) {
   static std::atomic<uint64_t> asked{0};
-  constexpr size_t lds = 2 * STAGEB;
+  constexpr size_t lds = 2 * 2 * BT * KB + 6144;   // two stages; the epilogue of fp32 outputs takes as much
   auto f = tile_kernel<WHOLE, CODES, YT>;
   const hipError_t e = ask_lds(f, lds, asked);
   if (e != hipSuccess) return e;
-  const uint32_t per = (a.tiles_m * a.tiles_n + 7) / 8;
-  hipLaunchKernelGGL(f, dim3(8 * per), dim3(256), lds, s, a);
+  const uint32_t rest = a.tiles_m * a.tiles_n - a.whole_tiles;
+  hipLaunchKernelGGL(f, dim3(a.whole_tiles + rest * a.cut), dim3(256), lds, s, a);
   return hipGetLastError();
 }
 
@@ -335,8 +444,32 @@ hipError_t tile_type(const GemmI8& a, hipStream_t s) {
                             : launch_tile<WHOLE, CODES, BF16>(a, s);
 }
 
-hipError_t one(const GemmI8& a, hipStream_t s) {
-  if (a.m > 128) {
+template <int MB, int NB>
+hipError_t launch_strip(const GemmI8& a, hipStream_t s) {
+  constexpr int WAVES = MB * NB <= 4 ? 8 : 4;
+  const dim3 grid((unsigned)((a.rows + 16 * NB - 1) / (16 * NB)), (unsigned)((a.m + 16 * MB - 1) / (16 * MB)));
+  if (a.z) hipLaunchKernelGGL((strip_kernel<MB, NB, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a);
+  else hipLaunchKernelGGL((strip_kernel<MB, NB, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int MB>
+hipError_t strip(const GemmI8& a, int nb, hipStream_t s) {
+  switch (nb) {
+    case 1: return launch_strip<MB, 1>(a, s);
+    case 2: return launch_strip<MB, 2>(a, s);
+    case 3: return launch_strip<MB, 3>(a, s);
+    default: return launch_strip<MB, 4>(a, s);
+  }
+}
+
+hipError_t one(GemmI8 a, hipStream_t s) {
+  // Whole rounds of 256 tiles, and the last round's tiles cut as long as it stays one round.
+  const uint32_t tiles = a.tiles_m * a.tiles_n;
+  a.whole_tiles = tiles / 256 * 256;
+  const uint32_t rest = tiles - a.whole_tiles;
+  a.cut = rest > 128 ? 1 : rest > 64 ? 2 : 4;
+  if (a.m > 128 && tiles * 4 >= kStripTiles) {
     // 16-byte units inside rows of whole words, and a tile inside 31-bit offsets
     const bool whole = a.d % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 4 == 0 &&
                        reinterpret_cast<uintptr_t>(a.w) % 4 == 0 && a.ld_x % 4 == 0 && a.ld_w % 4 == 0 &&
@@ -344,18 +477,22 @@ hipError_t one(const GemmI8& a, hipStream_t s) {
     if (whole) return a.z ? tile_type<true, true>(a, s) : tile_type<true, false>(a, s);
     return a.z ? tile_type<false, true>(a, s) : tile_type<false, false>(a, s);
   }
-  hipLaunchKernelGGL(byte_gemm_kernel, dim3((unsigned)((a.m + 63) / 64), (unsigned)((a.rows + 63) / 64)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  // Strips as wide as leaves a workgroup to each CU: 16 NB outputs.
+  const int64_t mb = (std::min<int64_t>(a.m, 128) + 15) / 16, chunks = (a.m + 127) / 128;
+  const int nb = (int)std::min<int64_t>(4, std::max<int64_t>(1, ((a.rows + 15) / 16 * chunks + 255) / 256));
+  if (mb <= 1) return strip<1>(a, nb, s);
+  if (mb <= 2) return strip<2>(a, nb, s);
+  if (mb <= 4) return strip<4>(a, nb, s);
+  if (mb <= 6 && chunks == 1) return strip<6>(a, nb, s);
+  return strip<8>(a, nb, s);
 }
 
 }  // namespace
 
-size_t byte_gemm_workspace_bytes(int64_t m, int64_t rows, int64_t d) { return 0; }
-
 hipError_t byte_gemm(const int8_t* x, int64_t m, int64_t ld_x, const float* xs, const void* w, int64_t ld_w,
                      const float* ws, const int32_t* z, int64_t rows, int64_t d, void* y, int y_dtype, int64_t ld_y,
-                     void* work, size_t work_bytes, hipStream_t s) {
-  GemmI8 a{x, static_cast<const uint8_t*>(w), xs, ws, z, y, m, rows, ld_x, ld_w, ld_y, (int)d, y_dtype, 0, 0, 0};
+                     hipStream_t s) {
+  GemmI8 a{x, static_cast<const uint8_t*>(w), xs, ws, z, y, m, rows, ld_x, ld_w, ld_y, (int)d, y_dtype, 0, 0, 0, 0, 0};
   const int64_t esz = y_dtype == F32 ? 4 : 2;
   a.y_vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ld_y * esz % 16 == 0;
   // a launch takes at most 2^20 tokens by 2^18 outputs (2^22 tiles)

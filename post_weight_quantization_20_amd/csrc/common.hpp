@@ -215,10 +215,9 @@ hipError_t norm_quant(const gptq_norm_quant_t& t, const void* x, const void* r, 
                       int8_t* q, float* scales, hipStream_t s);
 
 // y = xs ws (x (w - z)^T) for int8 rows and 8-bit weights (byte_gemm.hip). z may be null: signed weights.
-size_t byte_gemm_workspace_bytes(int64_t m, int64_t rows, int64_t d);
 hipError_t byte_gemm(const int8_t* x, int64_t m, int64_t ld_x, const float* xs, const void* w, int64_t ld_w,
                      const float* ws, const int32_t* z, int64_t rows, int64_t d, void* y, int y_dtype, int64_t ld_y,
-                     void* work, size_t work_bytes, hipStream_t s);
+                     hipStream_t s);
 
 // Keys and values into a paged 8-bit cache (kv_cache.hip), and attention over it (kv_attention.hip).
 hipError_t kv_append(const gptq_kv_append_t& t, const gptq_kv_cache_t& c, const void* k, const void* v,

@@ -63,20 +63,14 @@ def gptq_norm_quant(x: torch.Tensor, residual: Optional[torch.Tensor] = None, we
     return codes, scales, sum_out
 
 
-def gptq_byte_gemm_workspace_bytes(m: int, rows: int, d: int) -> int:
-    """Workspace bytes of gptq_byte_gemm for these sizes."""
-    return int(_lib.lib().gptq_byte_gemm_workspace_bytes(m, rows, d))
-
-
 def gptq_byte_gemm(x: torch.Tensor, x_scales: Optional[torch.Tensor], w: torch.Tensor,
                    w_scales: Optional[torch.Tensor], zeros: Optional[torch.Tensor] = None,
-                   y: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
-                   work: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                   y: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """y[i, r] = x_scales[i] * w_scales[r] * sum_k x[i, k] * (w[r, k] - zeros[r]) for int8 x [m, d]. w is int8
     [rows, d] (zeros None), or a layer stored with bits = 8 and one group per row: its codes, uint8 [rows, d], or
     gptq_pack's words, int32 [rows, d / 4], with its int32 zeros [rows] ([rows, 1] too, as are w_scales). y is fp32,
     fp16 or bf16 [m, rows] (a new one: of `dtype`)."""
-    dev = _device(x, x_scales, w, w_scales, zeros, y, work)
+    dev = _device(x, x_scales, w, w_scales, zeros, y)
     if x.dim() != 2:
         raise ValueError("x must be int8 [m, d]")
     m, d = x.shape
@@ -106,14 +100,8 @@ def gptq_byte_gemm(x: torch.Tensor, x_scales: Optional[torch.Tensor], w: torch.T
         if y.dtype not in _DTYPE:
             raise ValueError("y must be fp32/fp16/bf16")
         y_ld = _rows(y, (m, rows), y.dtype, "y")
-        L = _lib.lib()
-        if work is None:
-            nb = int(L.gptq_byte_gemm_workspace_bytes(m, rows, d))
-            work = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-        else:
-            work = _scratch(work, 0, dev)
-        _check(L.gptq_byte_gemm(_ptr(x), m, x_ld, _ptr(x_scales), _ptr(w), w_ld, _ptr(w_scales), _ptr(zeros), rows, d,
-                                _ptr(y), _DTYPE[y.dtype], y_ld, _ptr(work), 0 if work is None else work.numel(), s))
+        _check(_lib.lib().gptq_byte_gemm(_ptr(x), m, x_ld, _ptr(x_scales), _ptr(w), w_ld, _ptr(w_scales), _ptr(zeros),
+                                         rows, d, _ptr(y), _DTYPE[y.dtype], y_ld, s))
     return y
 
 

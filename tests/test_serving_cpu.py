@@ -63,7 +63,7 @@ def test_norm_quant_null_and_empty():
 
 def _gemm(**kw):
     d = dict(x=FAKE, m=4, ld_x=64, xs=2 * FAKE, w=3 * FAKE, ld_w=64, ws=4 * FAKE, zeros=5 * FAKE, rows=32, d=64, y=6 * FAKE,
-             y_dtype=0, ld_y=32, work=7 * FAKE, work_bytes=0)
+             y_dtype=0, ld_y=32)
     d.update(kw)
     return _lib().lib().gptq_byte_gemm(*d.values(), None)
 
@@ -71,7 +71,7 @@ def _gemm(**kw):
 @pytest.mark.parametrize("kw", [
     dict(m=-1), dict(m=1 << 40), dict(rows=-1), dict(rows=(1 << 24) + 1, ld_y=1 << 25), dict(d=0), dict(ld_x=63), dict(ld_w=63),
     dict(ld_y=31), dict(y_dtype=3), dict(x=0), dict(w=0), dict(y=0), dict(y=FAKE), dict(y=3 * FAKE + 100),
-    dict(y=2 * FAKE), dict(y=4 * FAKE), dict(y=5 * FAKE), dict(work=7 * FAKE + 8), dict(ld_x=1 << 60)], ids=str)
+    dict(y=2 * FAKE), dict(y=4 * FAKE), dict(y=5 * FAKE), dict(ld_x=1 << 60)], ids=str)
 def test_byte_gemm_rejects(kw):
     assert _gemm(**kw) == EINVAL
 
@@ -80,8 +80,6 @@ def test_byte_gemm_longest_sum_and_empty():
     assert _gemm(d=131072, ld_x=131072, ld_w=131072) == EUNSUPPORTED
     assert _gemm(m=0, x=0, y=0) == 0
     assert _gemm(rows=0, w=0, y=0) == 0
-    f = _lib().lib().gptq_byte_gemm_workspace_bytes
-    assert f(0, 4, 4) == 0 and f(4, -1, 4) == 0 and f(4, 4, 131072) == 0 and f(4, 4, 0) == 0
 
 
 # -------------------------------------------------------------------------------------------- cache

@@ -228,10 +228,8 @@ def test_byte_gemm_sizes(m, d, rows, stored, dtype):
     torch.cuda.synchronize()
     _check_gemm(x, xs, w, ws, z, y)
     if dtype == "f32":
-        none = _g().gptq_byte_gemm(x, xs, w, ws, z, work=torch.empty(0, dtype=torch.uint8, device="cuda:0"))
         plain = _g().gptq_byte_gemm(x, None, w, None, z)
         torch.cuda.synchronize()
-        assert torch.equal(none, y)
         _check_gemm(x, None, w, None, z, plain)
 
 
