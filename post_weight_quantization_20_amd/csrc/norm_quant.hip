@@ -34,6 +34,33 @@ GPTQ_DEV int code_of(double p, double a, double inv) {
   return (int)k;
 }
 
+// Weights of V columns from c on; ones past the last.
+template <int V>
+GPTQ_DEV void load_weights(const NormArgs& a, int c, float (&w)[V]) {
+  auto read = [&](const auto* p) {
+    typedef typename std::remove_cv<typename std::remove_pointer<decltype(p)>::type>::type E;
+    typedef E Vec __attribute__((ext_vector_type(V), aligned(sizeof(E))));
+    if (c + V <= a.d) {
+      const Vec v = *reinterpret_cast<const Vec*>(p + c);
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = (float)v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = c + e < a.d ? (float)p[c + e] : 1.0f;
+    }
+  };
+  if (!a.w) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = 1.0f;
+  } else if (a.w_dtype == F32) {
+    read(static_cast<const float*>(a.w));
+  } else if (a.w_dtype == F16) {
+    read(static_cast<const _Float16*>(a.w));
+  } else {
+    read(static_cast<const __bf16*>(a.w));
+  }
+}
+
 // T lanes take a row (256 / T rows a workgroup of 256 lanes, one of 1024), a lane C chunks of V elements.
 template <int DT, int V, int T, int C>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_quant_kernel(NormArgs a) {
@@ -69,7 +96,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_quant_kernel(NormArgs 
     }
   }
   double ss = 0.0, top = 0.0, odd = 0.0;   // odd: zero, unless a product is not finite
-  auto weight = [&](int c) { return a.w && c < a.d ? (double)load_as_f32(a.w, a.w_dtype, c) : 1.0; };
+  float w[C][V];
+#pragma unroll
+  for (int i = 0; i < C; ++i) load_weights<V>(a, V * (sub + i * T), w[i]);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int c = V * (sub + i * T);
@@ -78,7 +107,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_quant_kernel(NormArgs 
     for (int e = 0; e < V; ++e) {
       s[e] = r ? (E)((float)xv[i][e] + (float)rv[i][e]) : xv[i][e];
       h[i][e] = (float)s[e];
-      const double p = (double)h[i][e] * weight(c + e);
+      const double p = (double)h[i][e] * (double)w[i][e];
       ss = __builtin_fma((double)h[i][e], (double)h[i][e], ss);
       top = fmax(top, fabs(p));
       odd = __builtin_fma(p, 0.0, odd);
@@ -129,7 +158,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_quant_kernel(NormArgs 
     Vec yv;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const double p = (double)h[i][e] * weight(c + e);
+      const double p = (double)h[i][e] * (double)w[i][e];
       k[e] = (int8_t)(some ? code_of(p, top, inv) : 0);
       yv[e] = (E)(float)(p * rho);
     }
