@@ -25,29 +25,37 @@ struct NormArgs {
   double eps;
 };
 
-// The nearest whole number to 127 p / a, ties to even, for |p| <= a, with inv = 127 / a. The product with inv is
-// within 2^-50 of the quotient, so only quotients that near a half are formed exactly.
-GPTQ_DEV int code_of(double p, double a, double inv) {
-  const double t = p * inv;
-  double k = rint(t);
-  if (__builtin_expect(fabs(fabs(t - k) - 0.5) < 1e-12, 0)) k = rint(p * 127.0 / a);
-  return (int)k;
+constexpr int64_t kNormGroups = 2048;   // workgroups of 256 lanes
+
+// The nearest whole number to 127 p / top, ties to even, for |p| <= top with inv near 127 / top: of the whole numbers k and
+// k + 1 around the quotient, the nearer one by the sign of 254 |p| - (2 k + 1) top.
+GPTQ_DEV int exact_code(double p, double top, double inv) {
+  const double k = floor(fabs(p) * inv);
+  const double side = __builtin_fma(-(2.0 * k + 1.0), top, 254.0 * fabs(p));
+  const bool up = side > 0.0 || (side == 0.0 && ((int)k & 1));
+  const int c = min((int)k + (up ? 1 : 0), 127);
+  return p < 0.0 ? -c : c;
 }
 
-// Weights of V columns from c on; ones past the last.
+// Hides where a value comes from, so that what was formed from it before is not kept for later.
+#define GPTQ_OPAQUE(x) \
+  if constexpr (sizeof(x) >= 8) asm volatile("" : "+v"(x))
+
+// A weight in 64 bits, formed where it is used.
+GPTQ_DEV double wide(float w) {
+  asm volatile("" : "+v"(w));
+  return (double)w;
+}
+
+// Weights of V columns from c on.
 template <int V>
 GPTQ_DEV void load_weights(const NormArgs& a, int c, float (&w)[V]) {
   auto read = [&](const auto* p) {
     typedef typename std::remove_cv<typename std::remove_pointer<decltype(p)>::type>::type E;
     typedef E Vec __attribute__((ext_vector_type(V), aligned(sizeof(E))));
-    if (c + V <= a.d) {
-      const Vec v = *reinterpret_cast<const Vec*>(p + c);
+    const Vec v = *reinterpret_cast<const Vec*>(p + c);
 #pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = (float)v[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = c + e < a.d ? (float)p[c + e] : 1.0f;
-    }
+    for (int e = 0; e < V; ++e) w[e] = (float)v[e];
   };
   if (!a.w) {
 #pragma unroll
@@ -61,8 +69,12 @@ GPTQ_DEV void load_weights(const NormArgs& a, int c, float (&w)[V]) {
   }
 }
 
-// T lanes take a row (256 / T rows a workgroup of 256 lanes, one of 1024), a lane C chunks of V elements.
-template <int DT, int V, int T, int C>
+// T lanes take a row (256 / T rows a workgroup of 256 lanes), a lane C chunks of V elements. A workgroup goes through
+// rows gridDim.x apart and loads the next one's while it works on one. A chunk that passes the row's end (d >= V) is
+// read V columns before it, and its first elements, which the chunk before holds, count as zeros. KEEP: the weights stay in registers between
+// rows; else they are read again, from the caches, for each sum and each rounding. SHORT: 16-bit weights with 16-bit
+// elements, whose products fp32 holds exactly within its range.
+template <int DT, int V, int T, int C, bool KEEP, bool SHORT>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_quant_kernel(NormArgs a) {
   typedef typename ElemOf<DT>::T E;
   // accesses need no more than the element's alignment
@@ -70,108 +82,161 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_quant_kernel(NormArgs 
   typedef int8_t Codes __attribute__((ext_vector_type(V), aligned(1)));
   constexpr int RPW = T < 256 ? 256 / T : 1, WAVES = T / 64;
   const int sub = threadIdx.x % T;
-  const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / T;
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / T;
   if (T < 256 && row >= a.n) return;   // no barrier follows for T = 64
-  const E* x = static_cast<const E*>(a.x) + row * a.x_ld;
-  const E* r = a.r ? static_cast<const E*>(a.r) + row * a.r_ld : nullptr;
-  E* sum = a.sum ? static_cast<E*>(a.sum) + row * a.sum_ld : nullptr;
 
-  float h[C][V];
   Vec xv[C], rv[C];
+  auto column = [&](int i) { return min(V * (sub + i * T), a.d - V); };   // the first that is read
+  auto load = [&](int64_t at) {
+    const E* x = static_cast<const E*>(a.x) + at * a.x_ld;
+    const E* r = a.r ? static_cast<const E*>(a.r) + at * a.r_ld : x;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int c = V * (sub + i * T);
-    xv[i] = Vec{};
-    rv[i] = Vec{};
-    if (c + V <= a.d) {
-      xv[i] = *reinterpret_cast<const Vec*>(x + c);
-      if (r) rv[i] = *reinterpret_cast<const Vec*>(r + c);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (c + e < a.d) {
-          xv[i][e] = x[c + e];
-          if (r) rv[i][e] = r[c + e];
-        }
+    for (int i = 0; i < C; ++i) {
+      xv[i] = *reinterpret_cast<const Vec*>(x + column(i));
+      rv[i] = *reinterpret_cast<const Vec*>(r + column(i));
     }
+  };
+  // stores chunk i of a row: whole, or the elements that no other chunk holds
+  auto store = [&](auto* row_p, int i, const auto& v) {
+    int skip = V * (sub + i * T) - column(i);
+    if (skip == 0) {
+      __builtin_memcpy(row_p + column(i), &v, V * sizeof(*row_p));
+    } else if (skip < V) {
+      asm volatile("" : "+v"(skip));   // its comparisons belong here, not in registers over all rows
+#pragma unroll
+      for (int e = 1; e < V; ++e)
+        if (e >= skip) row_p[column(i) + e] = v[e];
+    }
+  };
+  float w[KEEP ? C : 1][V];
+  load(row);
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) load_weights<V>(a, column(i), w[i]);
   }
-  double ss = 0.0, top = 0.0, odd = 0.0;   // odd: zero, unless a product is not finite
-  float w[C][V];
+  __shared__ double part[3][2][WAVES];   // by rows in turn: one barrier a row
+  int turn = 0;
+  for (; row < a.n; row += step) {
+    E* sum = a.sum ? static_cast<E*>(a.sum) + row * a.sum_ld : nullptr;
+    Vec h[C];
+    double ss = 0.0, top = 0.0, odd = 0.0;   // odd: zero, unless a product is not finite
+    float top32 = 0.f, odd32 = 0.f;
 #pragma unroll
-  for (int i = 0; i < C; ++i) load_weights<V>(a, V * (sub + i * T), w[i]);
+    for (int i = 0; i < C; ++i) {
+      if constexpr (!KEEP) load_weights<V>(a, column(i), w[0]);
+      const float(&wi)[V] = w[KEEP ? i : 0];
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int c = V * (sub + i * T);
-    Vec s;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      s[e] = r ? (E)((float)xv[i][e] + (float)rv[i][e]) : xv[i][e];
-      h[i][e] = (float)s[e];
-      const double p = (double)h[i][e] * (double)w[i][e];
-      ss = __builtin_fma((double)h[i][e], (double)h[i][e], ss);
-      top = fmax(top, fabs(p));
-      odd = __builtin_fma(p, 0.0, odd);
-    }
-    if (sum) {
-      if (c + V <= a.d) {
-        *reinterpret_cast<Vec*>(sum + c) = s;
-      } else {
+      for (int e = 0; e < V; ++e) h[i][e] = a.r ? (E)((float)xv[i][e] + (float)rv[i][e]) : xv[i][e];
+      if (sum) store(sum, i, h[i]);
+      int skip = V * (sub + i * T) - column(i);
+      if (skip) {
+        asm volatile("" : "+v"(skip));
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          if (c + e < a.d) sum[c + e] = s[e];
+          if (e < skip) h[i][e] = (E)0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float hf = (float)h[i][e];
+        const double hd = (double)hf;
+        ss = __builtin_fma(hd, hd, ss);
+        if constexpr (SHORT) {
+          const float p = hf * wi[e];
+          top32 = fmaxf(top32, fabsf(p));
+          odd32 = __builtin_fmaf(p, 0.f, odd32);
+        } else {
+          const double p = hd * wide(wi[e]);
+          top = fmax(top, fabs(p));
+          odd = __builtin_fma(p, 0.0, odd);
+        }
       }
     }
-  }
-  if (!(odd == 0.0)) top = INFINITY;
+    if (row + step < a.n) load(row + step);
+    // the row's sum and maximum
+    auto reduce = [&](double& sum2, double& most) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    ss += __shfl_xor(ss, o, 64);
-    top = fmax(top, __shfl_xor(top, o, 64));
-  }
-  if constexpr (WAVES > 1) {
-    __shared__ double part[2][WAVES];
-    if ((threadIdx.x & 63) == 0) {
-      part[0][threadIdx.x >> 6] = ss;
-      part[1][threadIdx.x >> 6] = top;
-    }
-    __syncthreads();
-    ss = part[0][0];
-    top = part[1][0];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) {
-      ss += part[0][w];
-      top = fmax(top, part[1][w]);
-    }
-  }
-  const bool finite = ss < INFINITY && top < INFINITY;   // false for NaN
-  const double ms = ss / a.d + a.eps;
-  const double rho = ms == 0.0 ? 0.0 : 1.0 / sqrt(ms);
-  const bool some = finite && top > 0.0;
-  const double inv = some ? 127.0 / top : 0.0;
-  if (a.q && sub == 0) a.scales[row] = finite ? (float)(top * rho / 127.0) : NAN;
-  E* y = a.y ? static_cast<E*>(a.y) + row * a.y_ld : nullptr;
-  int8_t* q = a.q ? a.q + row * a.q_ld : nullptr;
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int c = V * (sub + i * T);
-    Codes k;
-    Vec yv;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const double p = (double)h[i][e] * (double)w[i][e];
-      k[e] = (int8_t)(some ? code_of(p, top, inv) : 0);
-      yv[e] = (E)(float)(p * rho);
-    }
-    if (c + V <= a.d) {
-      if (q) *reinterpret_cast<Codes*>(q + c) = k;
-      if (y) *reinterpret_cast<Vec*>(y + c) = yv;
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (c + e < a.d) {
-          if (q) q[c + e] = k[e];
-          if (y) y[c + e] = yv[e];
+      for (int o = 32; o > 0; o >>= 1) {
+        sum2 += __shfl_xor(sum2, o, 64);
+        most = fmax(most, __shfl_xor(most, o, 64));
+      }
+      if constexpr (WAVES > 1) {
+        if ((threadIdx.x & 63) == 0) {
+          part[turn][0][threadIdx.x >> 6] = sum2;
+          part[turn][1][threadIdx.x >> 6] = most;
         }
+        // LDS alone: the next row's loads stay on their way
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        sum2 = part[turn][0][0];
+        most = part[turn][1][0];
+#pragma unroll
+        for (int v = 1; v < WAVES; ++v) {
+          sum2 += part[turn][0][v];
+          most = fmax(most, part[turn][1][v]);
+        }
+        turn = turn == 2 ? 0 : turn + 1;
+      }
+    };
+    if (SHORT ? !(odd32 == 0.f) : !(odd == 0.0)) top = INFINITY;
+    else if (SHORT) top = (double)top32;
+    reduce(ss, top);
+    bool fast = top >= 0x1p-60 && top <= 0x1p60;   // products and quotients in fp32's range
+    if (SHORT && !fast) {
+      // products that fp32 does not hold, a row of zeros, or one that is not finite
+      double none = 0.0;
+      top = odd = 0.0;
+#pragma unroll
+      for (int i = 0; i < C; ++i) GPTQ_OPAQUE(h[i]);
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        if constexpr (!KEEP) load_weights<V>(a, column(i), w[0]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const double p = (double)(float)h[i][e] * wide(w[KEEP ? i : 0][e]);
+          top = fmax(top, fabs(p));
+          odd = __builtin_fma(p, 0.0, odd);
+        }
+      }
+      if (!(odd == 0.0)) top = INFINITY;
+      reduce(none, top);
+    }
+    // what follows forms its products anew: kept from above they would fill the registers
+#pragma unroll
+    for (int i = 0; i < C; ++i) GPTQ_OPAQUE(h[i]);
+    const bool finite = ss < INFINITY && top < INFINITY;   // false for NaN
+    const double ms = ss / a.d + a.eps;
+    const double rho = ms == 0.0 ? 0.0 : 1.0 / sqrt(ms);
+    const bool some = finite && top > 0.0;
+    const double inv = some ? 127.0 / top : 0.0;
+    const float inv32 = (float)inv;
+    if (a.q && sub == 0) a.scales[row] = finite ? (float)(top * rho / 127.0) : NAN;
+    E* y = a.y ? static_cast<E*>(a.y) + row * a.y_ld : nullptr;
+    int8_t* q = a.q ? a.q + row * a.q_ld : nullptr;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if constexpr (!KEEP) load_weights<V>(a, column(i), w[0]);
+      const float(&wi)[V] = w[KEEP ? i : 0];
+      // in fp32, whose three roundings are within 2.3e-5 of the quotient; exactly where that is near a half
+      Codes k = {};
+      bool near = some && !fast;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float t = (float)h[i][e] * wi[e] * inv32, n = rintf(t);
+        near |= fabsf(t - n) > 0.4999f;
+        k[e] = (int8_t)(int)(fast ? n : 0.f);
+      }
+      if (near) {
+        GPTQ_OPAQUE(h[i]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) k[e] = (int8_t)exact_code((double)(float)h[i][e] * wide(wi[e]), top, inv);
+      }
+      if (q) store(q, i, k);
+      if (y) {
+        Vec yv;
+#pragma unroll
+        for (int e = 0; e < V; ++e) yv[e] = (E)(float)((double)(float)h[i][e] * wide(wi[e]) * rho);
+        store(y, i, yv);
+      }
     }
   }
 }
@@ -179,39 +244,32 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_quant_kernel(NormArgs 
 template <int DT, int V, int T, int C>
 hipError_t launch(const NormArgs& a, hipStream_t s) {
   constexpr int RPW = T < 256 ? 256 / T : 1;
-  // a launch takes at most 2^20 workgroups
-  const int64_t step = (int64_t)RPW << 20;
-  for (int64_t t = 0; t < a.n; t += step) {
-    NormArgs b = a;
-    b.n = std::min(step, a.n - t);
-    constexpr int64_t esz = DT == F32 ? 4 : 2;
-    b.x = static_cast<const char*>(a.x) + t * a.x_ld * esz;
-    if (a.r) b.r = static_cast<const char*>(a.r) + t * a.r_ld * esz;
-    if (a.sum) b.sum = static_cast<char*>(a.sum) + t * a.sum_ld * esz;
-    if (a.y) b.y = static_cast<char*>(a.y) + t * a.y_ld * esz;
-    if (a.q) {
-      b.q = a.q + t * a.q_ld;
-      b.scales = a.scales + t;
-    }
-    hipLaunchKernelGGL((norm_quant_kernel<DT, V, T, C>), dim3((unsigned)((b.n + RPW - 1) / RPW)),
-                       dim3(T < 256 ? 256 : T), 0, s, b);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  // as many workgroups as run at once
+  const int64_t groups = (a.n + RPW - 1) / RPW, most = kNormGroups * 256 / (T < 256 ? 256 : T);
+  const dim3 grid((unsigned)std::min(groups, most)), wg(T < 256 ? 256 : T);
+  constexpr bool KEEP = C * V <= 16;
+  if (DT != F32 && (!a.w || a.w_dtype != F32))
+    hipLaunchKernelGGL((norm_quant_kernel<DT, V, T, C, KEEP, DT != F32>), grid, wg, 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_quant_kernel<DT, V, T, C, KEEP, false>), grid, wg, 0, s, a);
+  return hipGetLastError();
 }
 
-// A wave a row up to 16 elements a lane, then 256 lanes up to 32, then 1024.
+// A wave a row up to 16 elements a lane, then 256 lanes up to 16 (fp32) or 32, then 512 and 1024.
 template <int DT>
 hipError_t by_width(const NormArgs& a, hipStream_t s) {
   constexpr int V = DT == F32 ? 4 : 8;
   const int chunks = (a.d + V - 1) / V;
+  if (a.d < V) return launch<DT, 1, 64, 1>(a, s);
   if (chunks <= 64) return launch<DT, V, 64, 1>(a, s);
   if (chunks <= 128) return launch<DT, V, 64, 2>(a, s);
   if (chunks <= 256) return launch<DT, V, 256, 1>(a, s);
   if (chunks <= 512) return launch<DT, V, 256, 2>(a, s);
+  if (chunks <= 768) return launch<DT, V, 256, 3>(a, s);
   if (chunks <= 1024) return launch<DT, V, 256, 4>(a, s);
-  if (chunks <= 2048) return launch<DT, V, 1024, 2>(a, s);
+  if (chunks <= 1536) return launch<DT, V, 512, 3>(a, s);
+  if (chunks <= 2048) return launch<DT, V, 512, 4>(a, s);
+  if (chunks <= 3072) return launch<DT, V, 512, 6>(a, s);
   if (chunks <= 4096) return launch<DT, V, 1024, 4>(a, s);
   if (chunks <= 8192) return launch<DT, V, 1024, 8>(a, s);
   return launch<DT, V, 1024, 64 / V>(a, s);
