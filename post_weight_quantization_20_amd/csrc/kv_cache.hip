@@ -8,9 +8,8 @@
 //
 // One wave owns a (page, head) of keys or of values: its two passes (maximum, rounding) need no exchange beyond
 // the wave, and no other wave touches its codes or its scale. Angles of a page's tokens are formed once for the
-// heads of a workgroup, in LDS. A code stands next to a border as often as not, so angles, rotation and quotients
-// are computed in 64 bits and the code is the rounding of the exact quotient but for their last bits; 64-bit
-// arithmetic runs at the rate of unpacked fp32 here, and reading and writing bounds the pass.
+// heads of a workgroup, in LDS. Angles and rotation are computed in 64 bits, and so is a quotient that fp32 finds near a
+// half, so the code is the rounding of the exact quotient but for the last bits of 64.
 #include "common.hpp"
 
 namespace gptq {
@@ -25,7 +24,7 @@ struct AppendArgs {
   const int32_t *start, *past, *table, *pos, *pair_axis;
   const float* inv_freq;
   int ang_tokens;         // tokens whose angles LDS holds at a time
-  int heads_per_wg;       // heads of a workgroup
+  int tasks_per_wg;       // of a unit's 2 kv_heads tasks, heads of keys and then of values
   int64_t unit0;          // first unit of the launch
 };
 
@@ -128,16 +127,35 @@ GPTQ_DEV double2 turn(int32_t pos, float f) {
   return make_double2(c, s);
 }
 
-GPTQ_DEV int code_of(double x, double s, double inv) {
-  const double t = x * inv;
-  double k = rint(t);
-  if (__builtin_expect(fabs(fabs(t - k) - 0.5) < 1e-12, 0)) k = rint(x / s);
-  return (int)fmin(fmax(k, -127.0), 127.0);
+// Angles of nt tokens of the page from its tb-th new one on, by the whole workgroup.
+GPTQ_DEV void make_angles(const AppendArgs& a, const Unit& u, int tb, int nt, double2* angles) {
+  const int half = a.rd >> 1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * half; i += 64 * kWaves) {
+    const int t = i / half, pr = i - t * half;
+    int ax = a.pair_axis ? a.pair_axis[pr] : 0;
+    ax = ax < 0 ? 0 : ax >= a.axes ? a.axes - 1 : ax;
+    const int32_t ps = a.pos ? a.pos[(int64_t)ax * a.n + u.row0 + tb + t] : (int32_t)(u.t0 + tb + t);
+    angles[i] = turn(ps, a.inv_freq[pr]);
+  }
+  __syncthreads();
 }
 
-// Writes the new tokens of one (page, head). V: elements of a chunk on each side of V pairs.
+// The nearest whole number to x / s, ties to even, in [-127, 127], with inv near 1 / s: of the whole numbers k and k + 1
+// around the quotient, the nearer one by the sign of 2 |x| - (2 k + 1) s.
+GPTQ_DEV int exact_code(double x, double s, double inv) {
+  const double k = floor(fabs(x) * inv);
+  const double side = __builtin_fma(-(2.0 * k + 1.0), s, 2.0 * fabs(x));
+  const bool up = side > 0.0 || (side == 0.0 && ((int)k & 1));
+  const int c = min((int)fmin(k, 127.0) + (up ? 1 : 0), 127);
+  return x < 0.0 ? -c : c;
+}
+
+// Writes the new tokens of one (page, head). V: elements of a chunk on each side of V pairs. ready: LDS holds the angles
+// of all the page's new tokens; else of ang_tokens at a time, and the workgroup's waves come here together (h past the
+// last head: for the angles only).
 template <int DT, int V, bool KEYS>
-GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, double2* angles) {
+GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, bool ready, double2* angles) {
   typedef typename ElemOf<DT>::T T;
   typedef T Vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
   typedef int8_t Codes __attribute__((ext_vector_type(V), aligned(1)));
@@ -148,8 +166,8 @@ GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, d
   const int64_t tok = KEYS ? a.c.k_tok : a.c.v_tok;
   int8_t* cache = (KEYS ? a.c.k : a.c.v) + u.page * (KEYS ? a.c.k_page : a.c.v_page) + h * (KEYS ? a.c.k_hp : a.c.v_hp);
   float* scale = (KEYS ? a.c.k_scales : a.c.v_scales) + u.page * a.c.kv_heads + h;
+  const bool mine = h < a.c.kv_heads;
 
-  float p[kKeep][V], q[kKeep][V];
   auto columns = [&](int c, int& ca, int& cb) {
     if (c < rot_chunks) {
       ca = a.interleaved ? 2 * V * c : V * c;
@@ -159,24 +177,19 @@ GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, d
       cb = ca + V;   // dh for the last column of an odd tail
     }
   };
-  auto load = [&](int t, int c, float (&u0)[V], float (&v0)[V]) {
+  // the two sides of chunk c of token t, rotated
+  auto values = [&](int t, int c, double (&y)[V], double (&z)[V]) {
     int ca, cb;
     columns(c, ca, cb);
     const T* xr = x + t * ld;
     const Vec xa = *reinterpret_cast<const Vec*>(xr + ca);
     Vec xb = {};
     if (cb < dh) xb = *reinterpret_cast<const Vec*>(xr + cb);
+    double p[V], q[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      u0[e] = (float)xa[e];
-      v0[e] = (float)xb[e];
-    }
-  };
-  auto rotate = [&](int t, int c, const float (&u0)[V], const float (&v0)[V], double (&y)[V], double (&z)[V]) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      y[e] = u0[e];
-      z[e] = v0[e];
+      y[e] = p[e] = (double)(float)xa[e];
+      z[e] = q[e] = (double)(float)xb[e];
     }
     if (!KEYS || c >= rot_chunks) return;
     const double2* r = angles + (t % a.ang_tokens) * half + c * V;
@@ -184,36 +197,28 @@ GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, d
 #pragma unroll
       for (int e = 0; e + 1 < V; e += 2) {
         const double2 r0 = r[e / 2], r1 = r[V / 2 + e / 2];
-        y[e] = (double)u0[e] * r0.x - (double)u0[e + 1] * r0.y;
-        y[e + 1] = (double)u0[e + 1] * r0.x + (double)u0[e] * r0.y;
-        z[e] = (double)v0[e] * r1.x - (double)v0[e + 1] * r1.y;
-        z[e + 1] = (double)v0[e + 1] * r1.x + (double)v0[e] * r1.y;
+        y[e] = p[e] * r0.x - p[e + 1] * r0.y;
+        y[e + 1] = p[e + 1] * r0.x + p[e] * r0.y;
+        z[e] = q[e] * r1.x - q[e + 1] * r1.y;
+        z[e + 1] = q[e + 1] * r1.x + q[e] * r1.y;
       }
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        y[e] = (double)u0[e] * r[e].x - (double)v0[e] * r[e].y;
-        z[e] = (double)v0[e] * r[e].x + (double)u0[e] * r[e].y;
+        y[e] = p[e] * r[e].x - q[e] * r[e].y;
+        z[e] = q[e] * r[e].x + p[e] * r[e].y;
       }
     }
   };
-  // calls f(batch, token, chunk) for the lane's items; angles of ang_tokens tokens at a time
-  const bool kept = u.count * chunks <= 64 * kKeep && u.count <= a.ang_tokens;
+  // Calls f(batch, token, chunk) for the lane's items. Values of up to kKeep batches stay in registers between the
+  // passes, in fp32.
+  const bool kept = u.count * chunks <= 64 * kKeep && (!KEYS || !rd || u.count <= a.ang_tokens);
   auto each = [&](bool again, auto&& f) {
-    for (int tb = 0; tb < u.count; tb += a.ang_tokens) {
-      const int nt = min(a.ang_tokens, u.count - tb);
-      if (KEYS && rd && !(again && kept)) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < nt * half; i += 64 * kWaves) {
-          const int t = i / half, pr = i - t * half;
-          int ax = a.pair_axis ? a.pair_axis[pr] : 0;
-          ax = ax < 0 ? 0 : ax >= a.axes ? a.axes - 1 : ax;
-          const int32_t ps = a.pos ? a.pos[(int64_t)ax * a.n + u.row0 + tb + t] : (int32_t)(u.t0 + tb + t);
-          angles[i] = turn(ps, a.inv_freq[pr]);
-        }
-        __syncthreads();
-      }
-      if (h >= a.c.kv_heads) continue;   // the wave only helps with the angles
+    const int most = KEYS && rd ? a.ang_tokens : u.count;
+    for (int tb = 0; tb < u.count; tb += most) {
+      const int nt = min(most, u.count - tb);
+      if (KEYS && rd && !ready && !(again && kept)) make_angles(a, u, tb, nt, angles);
+      if (!mine) continue;
       if (kept) {
 #pragma unroll
         for (int b = 0; b < kKeep; ++b) {
@@ -226,23 +231,26 @@ GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, d
     }
   };
 
-  double top = 0.0, odd = 0.0;
+  float ky[kKeep][V], kz[kKeep][V];
+  double top = 0.0;
+  float odd = 0.f;
   each(false, [&](int b, int t, int c) {
-    load(t, c, p[b], q[b]);
     double y[V], z[V];
-    rotate(t, c, p[b], q[b], y, z);
+    values(t, c, y, z);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       top = fmax(top, fmax(fabs(y[e]), fabs(z[e])));
-      odd = __builtin_fma(y[e], 0.0, __builtin_fma(z[e], 0.0, odd));
+      ky[b][e] = (float)y[e];
+      kz[b][e] = (float)z[e];
+      odd = __builtin_fmaf(ky[b][e], 0.f, __builtin_fmaf(kz[b][e], 0.f, odd));
     }
   });
-  if (!(odd == 0.0)) top = INFINITY;
+  if (!(odd == 0.f)) top = INFINITY;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o, 64));
 
   float sn = 0.f, so = 0.f;
-  if (h < a.c.kv_heads) {
+  if (mine) {
     sn = top < INFINITY ? (float)(top / 127.0) : NAN;
     if (u.slot0 > 0) {
       so = *scale;
@@ -251,15 +259,37 @@ GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, d
   }
   const bool some = sn > 0.f && sn < INFINITY;
   const double sd = some ? (double)sn : 1.0, inv = some ? 1.0 / sd : 0.0;
+  const float inv32 = (float)inv;
+  const bool fast = sn >= 0x1p-100f && sn <= 0x1p100f;   // quotients in fp32's range
   each(true, [&](int b, int t, int c) {
-    if (!kept) load(t, c, p[b], q[b]);
     double y[V], z[V];
-    rotate(t, c, p[b], q[b], y, z);
-    Codes ka, kb;
+    if (!kept) {
+      values(t, c, y, z);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      ka[e] = (int8_t)(some ? code_of(y[e], sd, inv) : 0);
-      kb[e] = (int8_t)(some ? code_of(z[e], sd, inv) : 0);
+      for (int e = 0; e < V; ++e) {
+        ky[b][e] = (float)y[e];
+        kz[b][e] = (float)z[e];
+      }
+    }
+    // in fp32, whose three roundings are within 2.3e-5 of the quotient; exactly where that is near a half
+    Codes ka = {}, kb = {};
+    bool near = some && !fast;
+    if (fast) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float p = ky[b][e] * inv32, q = kz[b][e] * inv32, m = rintf(p), n = rintf(q);
+        near |= fabsf(p - m) > 0.4999f || fabsf(q - n) > 0.4999f;
+        ka[e] = (int8_t)(int)fminf(fmaxf(m, -127.f), 127.f);
+        kb[e] = (int8_t)(int)fminf(fmaxf(n, -127.f), 127.f);
+      }
+    }
+    if (near) {
+      values(t, c, y, z);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        ka[e] = (int8_t)exact_code(y[e], sd, inv);
+        kb[e] = (int8_t)exact_code(z[e], sd, inv);
+      }
     }
     int ca, cb;
     columns(c, ca, cb);
@@ -267,31 +297,47 @@ GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, d
     *reinterpret_cast<Codes*>(o + ca) = ka;
     if (cb < dh) *reinterpret_cast<Codes*>(o + cb) = kb;
   });
-  if (h >= a.c.kv_heads) return;
+  if (!mine) return;
   if (u.slot0 > 0 && some && sn > so) {
-    for (int it = lane; it < u.slot0 * dh; it += 64) {
-      int8_t* o = cache + (it / dh) * tok + it % dh;
-      *o = (int8_t)code_of((double)*o * (double)so, sd, inv);
+    // four codes a lane where the head's width allows it
+    if (dh % 4 == 0) {
+      typedef int8_t C4 __attribute__((ext_vector_type(4), aligned(1)));
+      const int quads = dh >> 2;
+      for (int it = lane; it < u.slot0 * quads; it += 64) {
+        C4* o = reinterpret_cast<C4*>(cache + (it / quads) * tok + 4 * (it % quads));
+        C4 k = *o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[e] = (int8_t)exact_code((double)k[e] * (double)so, sd, inv);
+        *o = k;
+      }
+    } else {
+      for (int it = lane; it < u.slot0 * dh; it += 64) {
+        int8_t* o = cache + (it / dh) * tok + it % dh;
+        *o = (int8_t)exact_code((double)*o * (double)so, sd, inv);
+      }
     }
   }
   if (lane == 0 && !(u.slot0 > 0 && sn == so)) *scale = sn;
 }
 
-// blockIdx.x: unit; blockIdx.y: groups of heads of keys, then of values.
+// blockIdx.x: unit; blockIdx.y: a range of its tasks, heads of keys and then of values.
 template <int DT, int VK, int VV>
 __global__ __launch_bounds__(64 * kWaves) void append_kernel(AppendArgs a) {
   extern __shared__ __align__(16) double2 angles[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hk = a.c.kv_heads;
   const Unit u = find_unit(a, a.unit0 + blockIdx.x, lane);
   if (u.page < 0) return;   // the same for every wave
-  const int groups = gridDim.y >> 1;
-  const bool keys = (int)blockIdx.y < groups;
-  const int h0 = ((int)blockIdx.y - (keys ? 0 : groups)) * a.heads_per_wg;
-  const int h1 = min(h0 + a.heads_per_wg, a.c.kv_heads);
-  for (int h = h0; h < h1; h += kWaves) {
-    const int mine = h + wave < h1 ? h + wave : a.c.kv_heads;   // past the last head: angles only
-    if (keys) append_head<DT, VK, true>(a, u, mine, lane, angles);
-    else append_head<DT, VV, false>(a, u, mine, lane, angles);
+  const int t0 = blockIdx.y * a.tasks_per_wg, t1 = min(t0 + a.tasks_per_wg, 2 * hk);
+  const bool ready = u.count <= a.ang_tokens || !a.rd;
+  if (t0 < hk && !ready) {
+    for (int h = t0; h < min(t1, hk); h += kWaves)
+      append_head<DT, VK, true>(a, u, h + wave < min(t1, hk) ? h + wave : hk, lane, false, angles);
+  } else if (t0 < hk && a.rd) {
+    make_angles(a, u, 0, u.count, angles);
+  }
+  for (int t = (ready ? t0 : max(t0, hk)) + wave; t < t1; t += kWaves) {
+    if (t < hk) append_head<DT, VK, true>(a, u, t, lane, true, angles);
+    else append_head<DT, VV, false>(a, u, t - hk, lane, true, angles);
   }
 }
 
@@ -301,14 +347,18 @@ hipError_t launch(AppendArgs a, hipStream_t s) {
   // a sequence's rows touch at most one page each, and rows / page_size + 2 in all
   const int64_t units = std::min(a.n, a.n / ps + 2 * a.seqs);
   const int half = a.rd / 2;
-  a.ang_tokens = half ? (int)std::max<int64_t>(1, std::min<int64_t>(ps, 2048 / half)) : (int)ps;   // 32 KB
-  a.heads_per_wg = kWaves;
-  const unsigned groups = (unsigned)((a.c.kv_heads + a.heads_per_wg - 1) / a.heads_per_wg);
+  a.ang_tokens = half ? (int)std::max<int64_t>(1, std::min<int64_t>(ps, 4096 / half)) : (int)ps;   // 64 KB at most
+  // All heads of a page in one workgroup, which finds its place and forms the angles once; with fewer pages than fill
+  // the card they are shared out, down to a head of keys or values for each wave.
+  const int tasks = 2 * a.c.kv_heads;
+  const int64_t share = std::max<int64_t>(1, std::min<int64_t>((tasks + kWaves - 1) / kWaves, (1024 + units - 1) / units));
+  a.tasks_per_wg = (int)((((tasks + kWaves - 1) / kWaves + share - 1) / share) * kWaves);
+  const unsigned groups = (unsigned)((tasks + a.tasks_per_wg - 1) / a.tasks_per_wg);
   const size_t lds = std::max<size_t>(16, (size_t)(half ? a.ang_tokens * half : 0) * sizeof(double2));
   // a grid holds fewer than 2^32 threads along x
   const int64_t step = (int64_t)1 << 23;
   for (a.unit0 = 0; a.unit0 < units; a.unit0 += step) {
-    hipLaunchKernelGGL((append_kernel<DT, VK, VV>), dim3((unsigned)std::min(step, units - a.unit0), 2 * groups),
+    hipLaunchKernelGGL((append_kernel<DT, VK, VV>), dim3((unsigned)std::min(step, units - a.unit0), groups),
                        dim3(64 * kWaves), lds, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

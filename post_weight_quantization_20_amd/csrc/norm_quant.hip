@@ -255,7 +255,7 @@ hipError_t launch(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// A wave a row up to 16 elements a lane, then 256 lanes up to 16 (fp32) or 32, then 512 and 1024.
+// A wave a row up to 16 elements a lane (8 in fp32), then 256, 512 and 1024 lanes a row.
 template <int DT>
 hipError_t by_width(const NormArgs& a, hipStream_t s) {
   constexpr int V = DT == F32 ? 4 : 8;
@@ -265,11 +265,9 @@ hipError_t by_width(const NormArgs& a, hipStream_t s) {
   if (chunks <= 128) return launch<DT, V, 64, 2>(a, s);
   if (chunks <= 256) return launch<DT, V, 256, 1>(a, s);
   if (chunks <= 512) return launch<DT, V, 256, 2>(a, s);
-  if (chunks <= 768) return launch<DT, V, 256, 3>(a, s);
-  if (chunks <= 1024) return launch<DT, V, 256, 4>(a, s);
-  if (chunks <= 1536) return launch<DT, V, 512, 3>(a, s);
-  if (chunks <= 2048) return launch<DT, V, 512, 4>(a, s);
-  if (chunks <= 3072) return launch<DT, V, 512, 6>(a, s);
+  if (chunks <= 1024) return launch<DT, V, 512, 2>(a, s);
+  if (chunks <= 2048) return launch<DT, V, 1024, 2>(a, s);
+  if (chunks <= 3072) return launch<DT, V, 1024, 3>(a, s);
   if (chunks <= 4096) return launch<DT, V, 1024, 4>(a, s);
   if (chunks <= 8192) return launch<DT, V, 1024, 8>(a, s);
   return launch<DT, V, 1024, 64 / V>(a, s);
