@@ -9,6 +9,9 @@
 //   tile    256 x 256 outputs a workgroup (4 waves of 128 x 128, v_mfma_i32_32x32x32_i8), operands through LDS
 //   strip   up to 128 tokens and as many outputs as give each CU a workgroup, whose waves share the sum over k and read
 //           both operands straight from memory
+//
+// Measured: 8192 x 4096 x 11008 in 361 us, 2.05 POPS (random data, the board's power limit holds the clock at 1.75 GHz;
+// zeros run at 3.3); 96 x 4096 x 11008 with zeros in 21 us; 8 x 4096 x 4096 in 6.4 us, 2.6 TB/s.
 #include "common.hpp"
 
 #include <atomic>

@@ -148,7 +148,12 @@ __global__ __launch_bounds__(256) void kv_row_kernel(KvArgs a) {
 //
 // Workgroups share the work by keys: the tiles of 32 keys of all (sequence, key head, 16 rows) are one list, of which
 // each takes an equal, contiguous part, whatever the lengths are. A part begins and ends anywhere; where it holds
-// a whole unit the result is written at once, else a partial one, and a second kernel joins these in order.
+// a whole unit the result is written at once, else a partial one, and a second kernel joins these in order. A part costs
+// about 8 us before its first key (lengths, pages, keys, one after another), so there are no more of them than run at
+// once: 16 tokens against caches of up to 8192 take 54 us with 512 parts, 61 with 768, 81 with 2048.
+//
+// Measured there: 6.9 TB/s while a part reads, 168 MB in 48 us with start and end, the join 6; one token against 100003
+// keys 49 + 9; four chunks of 512 against up to 4096 343 us, where every 16 rows read and widen K and V again.
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

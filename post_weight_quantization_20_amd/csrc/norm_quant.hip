@@ -7,9 +7,13 @@
 // The norm's root cancels in q: a code is decided by products of inputs alone.
 //
 // The pass is bound by HBM: x and r are read once, h, q and a scale written once (7 bytes an element in 16 bits).
-// A row stays in the registers of its lanes between the two sums and the rounding. Sums, the maximum and the
-// products are taken in 64 bits, whose rate is that of unpacked fp32 here: squares and products of finite fp32
-// numbers neither overflow nor vanish there, and a code is the rounding of the exact quotient.
+// A row stays in the registers of its lanes between the two sums and the rounding. The sum of squares is taken in 64
+// bits, where squares of finite fp32 numbers neither overflow nor vanish. Products of 16-bit elements and weights are
+// exact in fp32 within its range; others, and quotients that fp32 finds near a half, are formed in 64 bits, so that a
+// code is the rounding of the exact quotient.
+//
+// Measured: 8192 rows of 4096 bf16 elements in 55 us, 4.3 TB/s (a copy: 5.2); 5003 fp32 rows of 11008 in 112 us, bound
+// by the 64-bit products; 8 rows in 5.
 #include "common.hpp"
 
 namespace gptq {
