@@ -862,3 +862,125 @@ def test_empty_calls():
     out = g.gptq_kv_attention(q, none, none, nos, nos, _ints([[0], [1]]), _ints([5, 0]))
     torch.cuda.synchronize()
     assert torch.all(out == 0)
+
+
+# -------------------------------------------------------------------------------------------- edges
+
+@pytest.mark.parametrize("m,d,rows,stored", [((1 << 20) + 300, 16, 3, False), (2, 16, (1 << 18) + 70, True),
+                                             (200, 32, (1 << 18) + 70, False)])
+def test_byte_gemm_more_than_one_launch_takes(m, d, rows, stored):
+    torch = torch_cuda()
+    x, xs, w, ws, z = _gemm_inputs(m, d, rows, stored, seed=9)
+    y = _g().gptq_byte_gemm(x, xs, w, ws, z, dtype=torch.float16)
+    torch.cuda.synchronize()
+    _check_gemm(x, xs, w, ws, z, y)
+
+
+@pytest.mark.parametrize("tiles", [(2, 16), (4, 20), (8, 30), (8, 33), (17, 17)], ids=str)
+def test_byte_gemm_rounds_of_tiles(tiles):
+    """Less than a round of the CUs, parts of one, and a part past whole ones; the last tile of each edge is narrow."""
+    torch = torch_cuda()
+    m, rows = 256 * tiles[0] - 97, 256 * tiles[1] - 130
+    for stored in (False, True):
+        x, xs, w, ws, z = _gemm_inputs(m, 208, rows, stored, seed=10)
+        y = _g().gptq_byte_gemm(x, xs, w, ws, z, dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+        _check_gemm(x, xs, w, ws, z, y)
+
+
+@pytest.mark.parametrize("m", [7, 300])
+def test_byte_gemm_and_norm_in_a_graph(m):
+    torch = torch_cuda()
+    g = _g()
+    x, r = _rand((m, 320), 1, "f16"), _rand((m, 320), 2, "f16")
+    w = _rand((320,), 3, "f16")
+    _, _, b, ws, z = _gemm_inputs(1, 320, 500, True)
+    codes = torch.empty(m, 320, dtype=torch.int8, device="cuda:0")
+    sc, y = torch.empty(m, device="cuda:0"), torch.empty(m, 500, device="cuda:0")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=side):
+        g.gptq_norm_quant(x, r, w, sum_out=r, codes=codes, scales=sc)      # the residual in place
+        g.gptq_byte_gemm(codes, sc, b, ws, z, y=y)
+    for i in range(4):
+        x.copy_(_rand((m, 320), 10 + i, "f16"))
+        before = r.clone()
+        gr.replay()
+        torch.cuda.synchronize()
+        _check_norm("f16", x, before, w, 1e-6, codes, sc, r)
+        _check_gemm(codes, sc, b, ws, z, y)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_norm_quant_more_rows_than_workgroups(dtype):
+    """Rows in turn: zeros, infinities and rows beyond fp32's squares between ordinary ones, in one workgroup's list."""
+    torch = torch_cuda()
+    n, d = 9000, 520
+    x = _rand((n, d), 11, dtype)
+    x[5::7] = 0
+    x[4096 + 3, 9] = float("inf")
+    if dtype != "f16":
+        x[2048 + 5] *= 1e25
+        x[4096 + 5] *= 1e-25
+    w = _rand((d,), 12, dtype)
+    codes, scales, _ = _g().gptq_norm_quant(x, None, w)
+    torch.cuda.synchronize()
+    _check_norm(dtype, x, None, w, 1e-6, codes, scales, None)
+
+
+def test_norm_quant_values_next_to_halves():
+    """Quotients at and beside halves: ties go to the even code, neighbours to their own."""
+    torch = torch_cuda()
+    k = torch.arange(0, 127, device="cuda:0", dtype=torch.float64)
+    half = (k + 0.5) / 127.0
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        row = torch.cat([half, -half, torch.ones(1, device="cuda:0", dtype=torch.float64)]) * 127.0 * 8
+        x = torch.stack([row.to(dtype), torch.nextafter(row.float(), torch.zeros_like(row.float())).to(dtype),
+                         torch.nextafter(row.float(), 2 * row.float()).to(dtype)])
+        codes, scales, _ = _g().gptq_norm_quant(x)
+        torch.cuda.synchronize()
+        h = _np(x)
+        want = np.rint(h * 127.0 / np.abs(h).max(1, keepdims=True))
+        assert np.array_equal(codes.cpu().numpy(), want)
+
+
+def test_kv_append_after_a_page_of_zeros():
+    """Earlier tokens of scale zero: their codes stay zero when the scale begins."""
+    torch = torch_cuda()
+    zeros = torch.zeros(5, 2, 32, device="cuda:0")
+    kc, vc, ks, vs = _run_append("f32", [5], [0], 2, 32, data=(zeros, zeros), table=np.array([[0]], np.int32), max_pages=1)
+    assert torch.all(ks[0] == 0) and torch.all(kc[0, :5] == 0)
+    k = _rand((3, 2, 32), 5, "f32")
+    _g().gptq_kv_append(k, k, kc, vc, ks, vs, _ints([[0]]), _ints([5]))
+    torch.cuda.synchronize()
+    assert torch.all(kc[0, :5] == 0) and torch.all(ks[0] > 0)
+    want = np.rint(_np(k) / _np(ks)[0][None, :, None])
+    assert np.array_equal(kc[0, 5:8].cpu().numpy(), want)
+
+
+def test_calls_between_devices_and_layouts_are_refused():
+    torch = torch_cuda()
+    g = _g()
+    x = torch.ones(4, 32, dtype=torch.int8, device="cuda:0")
+    with pytest.raises(ValueError):
+        g.gptq_byte_gemm(x, None, x.cpu(), None)
+    with pytest.raises(ValueError):
+        g.gptq_byte_gemm(x, None, x.to(torch.uint8), None)          # codes without zeros
+    with pytest.raises(ValueError):
+        g.gptq_byte_gemm(x, None, x.t().contiguous().t(), None)     # columns not side by side
+    with pytest.raises(ValueError):
+        g.gptq_byte_gemm(x, torch.ones(3, device="cuda:0"), x, None)
+    with pytest.raises(ValueError):
+        g.gptq_norm_quant(torch.ones(2, 8, device="cuda:0"), torch.ones(2, 7, device="cuda:0"))
+    kc, ks = _pool(2, 16, 2, 32, 1)
+    q = _rand((1, 4, 32), 1, "f16")
+    t, n = _ints([[0, 1]]), _ints([5])
+    with pytest.raises(ValueError):
+        g.gptq_kv_attention(q, kc, kc, ks, ks, t.long(), n)
+    with pytest.raises(ValueError):
+        g.gptq_kv_attention(q[:, :3], kc, kc, ks, ks, t, n)
+    with pytest.raises(ValueError):
+        g.gptq_kv_append(q[:, :1], q[:, :1], kc, kc.clone(), ks, ks.clone(), t, n)
+    with pytest.raises(g.GPTQError):
+        g.gptq_kv_append(q[:, :2], q[:, :2], kc, kc, ks, ks.clone(), t, n)   # keys and values in one place
