@@ -269,11 +269,11 @@ hipError_t by_width(const NormArgs& a, hipStream_t s) {
   if (chunks <= 128) return launch<DT, V, 64, 2>(a, s);
   if (chunks <= 256) return launch<DT, V, 256, 1>(a, s);
   if (chunks <= 512) return launch<DT, V, 256, 2>(a, s);
-  if (chunks <= 1024) return launch<DT, V, 512, 2>(a, s);
-  if (chunks <= 2048) return launch<DT, V, 1024, 2>(a, s);
-  if (chunks <= 3072) return launch<DT, V, 1024, 3>(a, s);
-  if (chunks <= 4096) return launch<DT, V, 1024, 4>(a, s);
-  if (chunks <= 8192) return launch<DT, V, 1024, 8>(a, s);
+  if (chunks <= 2 * 512) return launch<DT, V, 512, 2>(a, s);
+  if (chunks <= 2 * 1024) return launch<DT, V, 1024, 2>(a, s);
+  if (chunks <= 3 * 1024) return launch<DT, V, 1024, 3>(a, s);
+  if (chunks <= 4 * 1024) return launch<DT, V, 1024, 4>(a, s);
+  if (chunks <= 8 * 1024) return launch<DT, V, 1024, 8>(a, s);
   return launch<DT, V, 1024, 64 / V>(a, s);
 }
 
