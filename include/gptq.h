@@ -615,10 +615,9 @@ typedef struct {
  *             where there are few queries; with less they are not. Not shared with a concurrent call, two
  *             captured graphs included.
  * Codes are exact in the matrix cores' 16-bit type. Scores, the softmax's maximum and sum and the output's sums are
- * fp32. With fp16 and bf16 each query is used as it is and each probability (times its value's scale) is rounded
- * once to 11 bits before it weighs a code, which moves the output by at most half a step (2^-11) of sum p |v|;
- * with fp32 both are kept to 22 bits. Results do not
- * depend on scheduling. Launches on `stream` alone; the call may be captured in a graph.
+ * fp32. With fp16 and bf16 each query is used as it is, with fp32 it is kept to 22 bits; so is each probability
+ * (times its value's scale) before it weighs a code, whatever the type. Results do not depend on scheduling.
+ * Launches on `stream` alone; the call may be captured in a graph.
  */
 gptq_status_t gptq_kv_attention(const gptq_kv_attention_t *a, const gptq_kv_cache_t *cache, const void *q,
                                 const int32_t *q_start, const int32_t *lens, const int32_t *table,
