@@ -616,8 +616,10 @@ typedef struct {
  *             captured graphs included.
  * Codes are exact in the matrix cores' 16-bit type. Scores, the softmax's maximum and sum and the output's sums are
  * fp32. With fp16 and bf16 each query is used as it is, with fp32 it is kept to 22 bits; so is each probability
- * (times its value's scale) before it weighs a code, whatever the type. Results do not depend on scheduling.
- * Launches on `stream` alone; the call may be captured in a graph.
+ * times its value's scale before it weighs a code, whatever the type, or to 2^-30 of the largest such product of the
+ * query's keys where that is coarser (probabilities below fp32's normal range count as zero). Scales of pages that a
+ * query does not see take no part in its row. Results do not depend on scheduling. Launches on `stream` alone; the
+ * call may be captured in a graph.
  */
 gptq_status_t gptq_kv_attention(const gptq_kv_attention_t *a, const gptq_kv_cache_t *cache, const void *q,
                                 const int32_t *q_start, const int32_t *lens, const int32_t *table,

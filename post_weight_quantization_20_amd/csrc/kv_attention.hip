@@ -145,8 +145,11 @@ __global__ __launch_bounds__(256) void kv_row_kernel(KvArgs a) {
 // Queries are scaled to [1, 2) by a power of two (fp16 ones are taken as they are); fp32 ones are two fp16 terms.
 // Probabilities are two terms for every type: one of 11 bits moves an output by up to 2^-11 of sum p |v|, which is as
 // much as its own rounding to fp16 and shows wherever values cancel. The second product costs 0.5 of 55 us for 16 tokens
-// against caches of up to 8192, and 23 of 371 for four chunks of 512. A key block's scale multiplies its scores, a value block's its probabilities; those are
-// kept in fp16's range by a power of two common to the wave that bounds all value scales seen so far.
+// against caches of up to 8192, and 23 of 371 for four chunks of 512.
+// A key block's scale multiplies its scores, a value block's its probabilities. The products are kept in fp16's range by
+// a power of two a row, which bounds those of the keys that the row has seen, probability and scale together: neither a
+// scale that a row does not see nor one that its probabilities make small takes bits from the others. (One power for
+// the wave, of all scales that it loads, would save 9 of 380 us for the chunks, and loses rows whose scales are small.)
 //
 // Workgroups share the work by keys: the tiles of 32 keys of all (sequence, key head, 16 rows) are one list, of which
 // each takes an equal, contiguous part, whatever the lengths are. A part begins and ends anywhere; where it holds
@@ -167,6 +170,7 @@ constexpr int kMinTiles = 4;       // key tiles that a workgroup takes at least
 constexpr int kJoinRows = 1;       // rows of a unit that a workgroup joins
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kShift = 7.0f, kRaise = 8.0f;
+constexpr int kNoExp = -1000;      // the exponent of a scale that is zero or not finite
 
 struct FewArgs {
   KvArgs a;
@@ -392,8 +396,8 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
     const uint32_t per_page = (uint32_t)a.ps >> 4;
     uint64_t valid = 0;
     int64_t k_at = 0, v_at = 0;
-    float ks = 0.f, vs = 0.f;
-    int count = 0;
+    float ks = 0.f, vm = 0.f;                     // value scale vm 2^vx, |vm| in [1/2, 1)
+    int vx = kNoExp, count = 0;
     auto open = [&](int32_t tb) {
       // lane 2 i + e: subtile e (16 keys) of the batch's tile i
       const int32_t tile = tb + 4 * (lane >> 1);
@@ -404,10 +408,10 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
         if (page >= a.c.pages) page = -1;
       }
       valid = __ballot(page >= 0);
-      ks = vs = 0.f;
+      ks = vm = 0.f;
       if (page >= 0) {
         ks = a.c.k_scales[page * a.hk + kvh];
-        vs = a.c.v_scales[page * a.hk + kvh];
+        vm = a.c.v_scales[page * a.hk + kvh];
       }
       // where one half of a tile has no page, the other's is read in its place; without both there is no tile
       const int64_t slot = (sub - at_page * per_page) * 16;
@@ -486,22 +490,15 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
     floatx4 acc[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
-    int ve = -200;                                // value scales are below 2^ve
+    float m = -INFINITY, l = 0.f;                 // of the row: the scores' maximum and sum
+    float mt = -INFINITY;                         // and the maximum of score + exponent of the value's scale
+    int ve = 0;                                   // ceil(mt - m): acc is in units of 2^ve
 
     for (int32_t tb = tfirst; tb < tend;) {
-      {
-        const float top = wave_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.f);
-        if (top > 0.f) {
-          const int e = uniform((int32_t)ilogbf(top)) + 1;
-          if (e > ve) {
-            const float d = ldexpf(1.0f, max(ve - e, -200));
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t] *= d;
-            ve = e;
-          }
-        }
-        if (fabsf(vs) < INFINITY) vs = ldexpf(vs, -ve);
+      vx = kNoExp;
+      if (vm != 0.f && fabsf(vm) < INFINITY) {
+        vx = ilogbf(vm) + 1;
+        vm = ldexpf(vm, -vx);
       }
       auto compute = [&](int i, const Tile& x) {
         const int both = (int)(valid >> (2 * i)) & 3;
@@ -520,7 +517,6 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
         }
         const int32_t j0 = (int32_t)((tb + 4 * i) * kKeyTile);
         const int32_t jl = j0 + 4 * g;            // the key of register c of half e: jl + 16 e + c
-        float mx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float fk = ldexpf(read_lane(ks, 2 * i + e) * (ANY ? a.scale : a.scale * kLog2e), qe);
@@ -543,25 +539,38 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
               if (!((both >> e) & 1) || j >= lim || j < lo) S[e][c] = -INFINITY;
             }
         }
+        int sx[2];
+        float mx = -INFINITY, tx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mx = fmaxf(mx, S[e][c]);
-        if (__ballot(!(mx <= m + kRaise))) {
+        for (int e = 0; e < 2; ++e) {
+          sx[e] = __builtin_amdgcn_readlane(vx, 2 * i + e);
+          const float x = fmaxf(fmaxf(S[e][0], S[e][1]), fmaxf(S[e][2], S[e][3]));
+          mx = fmaxf(mx, x);
+          tx = fmaxf(tx, x + (float)sx[e]);
+        }
+        if (__ballot(!(mx <= m + kRaise && tx <= mt + kRaise))) {
           mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+          tx = fmaxf(tx, __shfl_xor(tx, 16, 64));
           mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+          tx = fmaxf(tx, __shfl_xor(tx, 32, 64));
           const float m2 = fmaxf(m, mx);
-          const float d = m2 == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m2);
-          m = m2;
-          l *= d;
+          mt = fmaxf(mt, tx);
+          if (m2 != -INFINITY) {
+            const int ve2 = (int)ceilf(fminf(fmaxf(mt - m2, -2000.f), 2000.f));
+            const float dm = m - m2, d = __builtin_amdgcn_exp2f(dm + (float)(ve - ve2));
+            l *= __builtin_amdgcn_exp2f(dm);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) acc[t] *= d;
+            for (int t = 0; t < NT; ++t) acc[t] *= d;
+            m = m2;
+            ve = ve2;
+          }
         }
         const float off = kShift - (m == -INFINITY ? 0.f : m);
         half8 w[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float sv = read_lane(vs, 2 * i + e);
+          // capped where the probability is too small for fp32, so that it is not zero times infinity
+          const float sv = ldexpf(read_lane(vm, 2 * i + e), min(sx[e] - ve, 120));
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float pr = __builtin_amdgcn_exp2f(S[e][c] + off);
@@ -617,21 +626,25 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
         for (int b = 0; b < VB; ++b) merge[wave][c][b][lane] = acc[u * VB + b][c];
       __syncthreads();
       if (u == 0) {
-        float mw[4];
+        float mw[4], lw[4];
         int ew[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           mw[w] = stats[w][0][lane];
+          lw[w] = stats[w][1][lane];
           ew[w] = __builtin_bit_cast(int, stats[w][2][lane]);
         }
         m = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
-        ve = max(max(ew[0], ew[1]), max(ew[2], ew[3]));
+        ve = -4000;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float lw = stats[w][1][lane];
-          const float fw = lw == 0.f ? 0.f : __builtin_amdgcn_exp2f(mw[w] - m);
-          lsum += lw * fw;
-          give[w] = fw * ldexpf(1.0f, max(ew[w] - ve, -200));
+          mw[w] -= m;
+          if (lw[w] != 0.f) ve = max(ve, ew[w] + (int)ceilf(fmaxf(mw[w], -2000.f)));
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          lsum += lw[w] == 0.f ? 0.f : lw[w] * __builtin_amdgcn_exp2f(mw[w]);
+          give[w] = lw[w] == 0.f ? 0.f : __builtin_amdgcn_exp2f(mw[w] + (float)(ew[w] - ve));
         }
       }
 #pragma unroll

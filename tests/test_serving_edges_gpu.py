@@ -53,6 +53,63 @@ def _attend(dtype, q, kc, vc, ks, vs, table, news, lens, split=True, **kw):
 
 
 @pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("ratio", [1e3, 1e6, 1e9, 1e12, 1e25], ids=str)
+@pytest.mark.parametrize("where", ["later", "before", "half"])
+def test_value_scales_of_unseen_pages_take_no_part(where, ratio, dtype):
+    """A page whose values are far larger, which some rows see and others do not: after a row's position, before its window
+    (and 128 keys before others that it sees), in the other half of 32 keys that it sees."""
+    torch = torch_cuda()
+    print(f"unseen scales {(where, ratio, dtype)}", flush=True)
+    hq, hk, dh, ps = 2, 2, 64, 16
+    news, lens, kw, page = {"later": ([32], [32], {}, 1), "before": ([100], [500], dict(window=200), 13),
+                            "half": ([64], [64], {}, 3)}[where]
+    pages = -(-lens[0] // ps)
+    kc, ks = _pool(pages, ps, hk, dh, 1)
+    vc, vs = _pool(pages, ps, hk, dh, 2)
+    table = _table(1, pages, pages, 3)
+    vs[int(table[0, page])] *= ratio
+    q = _rand((news[0], hq, dh), 4, dtype)
+    for split in (True, False):
+        _attend(dtype, q, kc, vc, ks, vs, table, news, lens, split=split, **kw)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("split", [True, False])
+def test_values_far_apart_weigh_by_their_products(split, dh, dtype):
+    """Early pages with values 2^40 times the others', whose probabilities are smaller by as much or by far more."""
+    torch = torch_cuda()
+    print(f"far values {(split, dh, dtype)}", flush=True)
+    hq, hk, ps, n = 4, 2, 32, 1700
+    pages = -(-n // ps)
+    kc, ks = _pool(pages, ps, hk, dh, 5)
+    vc, vs = _pool(pages, ps, hk, dh, 6)
+    table = _table(1, pages, pages, 7)
+    order = [int(p) for p in table[0]]
+    slopes = torch.tensor([1.0, 0.5, 0.02, 0.0], device="cuda:0")
+    q = _rand((3, hq, dh), 8, dtype, 0.5)
+    for early in (pages - 2, pages - 3, pages // 2, 1):
+        v2 = vs.clone()
+        v2[order[:early]] *= 2.0 ** 40 if dtype != "f16" else 2.0 ** 20
+        _attend(dtype, q, kc, vc, ks, v2, table, [3], [n], split=split, slopes=slopes)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_value_scales_of_zero_and_of_either_sign(dtype):
+    hq, hk, dh, ps = 4, 2, 64, 16
+    kc, ks = _pool(13, ps, hk, dh, 9)
+    vc, vs = _pool(13, ps, hk, dh, 10)
+    table = _table(1, 13, 13, 11)
+    for i, p in enumerate(int(p) for p in table[0]):
+        vs[p] *= [1.0, 0.0, -1.0, 1e-30, -1e4][i % 5]
+    q = _rand((50, hq, dh), 12, dtype)
+    _attend(dtype, q, kc, vc, ks, vs, table, [50], [200])
+    vs.zero_()
+    out, _ = _attend(dtype, q, kc, vc, ks, vs, table, [50], [200])
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("news,lens", [([1, 1], [1000, 130]), ([70], [200]), ([5, 3], [64, 900])], ids=str)
 def test_probabilities_keep_fp32s_accuracy(news, lens, dtype):
     """Values that nearly cancel: every second one is the negative of the one before, and all probabilities are much
