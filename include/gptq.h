@@ -615,11 +615,12 @@ typedef struct {
  *             where there are few queries; with less they are not. Not shared with a concurrent call, two
  *             captured graphs included.
  * Codes are exact in the matrix cores' 16-bit type. Scores, the softmax's maximum and sum and the output's sums are
- * fp32. With fp16 and bf16 each query is used as it is, with fp32 it is kept to 22 bits; so is each probability
- * times its value's scale before it weighs a code, whatever the type, or to 2^-30 of the largest such product of the
- * query's keys where that is coarser (probabilities below fp32's normal range count as zero). Scales of pages that a
- * query does not see take no part in its row. Results do not depend on scheduling. Launches on `stream` alone; the
- * call may be captured in a graph.
+ * fp32. A query's elements are used as they are with fp16, to 22 bits with fp32 and exactly with bf16, but to no less
+ * than 2^-39 of their row's largest with both (so fp32's keep 22 bits down to 2^-18 of it, and bf16's are exact down
+ * to 2^-31). Each probability times its value's scale keeps 22 bits before it weighs a code, whatever the type, or
+ * 2^-30 of the largest such product of the query's keys where that is coarser (probabilities below fp32's normal range
+ * count as zero). Scales of pages that a query does not see take no part in its row. Results do not depend on
+ * scheduling. Launches on `stream` alone; the call may be captured in a graph.
  */
 gptq_status_t gptq_kv_attention(const gptq_kv_attention_t *a, const gptq_kv_cache_t *cache, const void *q,
                                 const int32_t *q_start, const int32_t *lens, const int32_t *table,

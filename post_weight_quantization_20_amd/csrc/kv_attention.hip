@@ -142,7 +142,9 @@ __global__ __launch_bounds__(256) void kv_row_kernel(KvArgs a) {
 //                        l reads V of the 8 keys that it holds scores of, VB bytes of each, whose columns become
 //                        rows of VB products: bytes of two keys are put side by side while they are widened.
 // A code c becomes fp16 exactly: byte c ^ 128 under the exponent of 1024 is 1152 + c, and 1152 is subtracted.
-// Queries are scaled to [1, 2) by a power of two (fp16 ones are taken as they are); fp32 ones are two fp16 terms.
+// A query's row is scaled by a power of two that brings its largest element to fp16's last but one octave (fp16 ones are
+// taken as they are), so that its smaller elements stay above fp16's smallest steps: bf16 ones are exact down to 2^-31 of
+// the largest. fp32 ones are two fp16 terms.
 // Probabilities are two terms for every type: one of 11 bits moves an output by up to 2^-11 of sum p |v|, which is as
 // much as its own rounding to fp16 and shows wherever values cancel. The second product costs 0.5 of 55 us for 16 tokens
 // against caches of up to 8192, and 23 of 371 for four chunks of 512.
@@ -170,6 +172,7 @@ constexpr int kMinTiles = 4;       // key tiles that a workgroup takes at least
 constexpr int kJoinRows = 1;       // rows of a unit that a workgroup joins
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kShift = 7.0f, kRaise = 8.0f;
+constexpr int kQueryExp = 14;      // a scaled row's largest element is in [2^14, 2^15)
 constexpr int kNoExp = -1000;      // the exponent of a scale that is zero or not finite
 
 struct FewArgs {
@@ -450,7 +453,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
     }
 
     half8 q[TERMS][NK];
-    int qe = 0;                                   // queries are 2^qe larger than q
+    int qe = 0;                                   // the row is q times 2^qe
     {
       float v[NK][8], top = 0.f;
 #pragma unroll
@@ -471,7 +474,7 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         if (top > 0.f && top < INFINITY) {
-          qe = ilogbf(top);
+          qe = ilogbf(top) - kQueryExp;
 #pragma unroll
           for (int k = 0; k < NK; ++k)
 #pragma unroll

@@ -124,3 +124,23 @@ def test_probabilities_keep_fp32s_accuracy(news, lens, dtype):
     q = _rand((sum(news), hq, dh), 16, dtype, 0.02)
     for kw in ({}, dict(causal=False), dict(cap=20.0)):
         _attend(dtype, q, kc, vc, ks, vs, table, news, lens, **kw)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("news", [1, 40])
+def test_queries_with_a_channel_far_larger(news, dtype):
+    """A channel of a query that is far larger than the others, where the keys hold zeros: fp32's others keep their 22
+    bits down to 2^-18 of it, bf16's are exact down to 2^-31, fp16's always."""
+    torch = torch_cuda()
+    print(f"large channel {(news, dtype)}", flush=True)
+    hq, hk, dh, ps, n = 4, 2, 64, 16, 300
+    pages = -(-n // ps)
+    kc, ks = _pool(pages, ps, hk, dh, 17)
+    vc, vs = _pool(pages, ps, hk, dh, 18)
+    kc[..., 5] = 0
+    r = np.random.default_rng(19)
+    q = r.uniform(0.5, 1.0, (news, hq, dh)) * r.choice([-1.0, 1.0], (news, hq, dh))
+    q[..., 5] = {"f32": 2.0 ** 16, "f16": 2.0 ** 15, "bf16": 2.0 ** 29}[dtype]
+    q = torch.from_numpy(q).to(_dtype(dtype)).cuda()
+    for kw in ({}, dict(cap=8.0)):
+        _attend(dtype, q, kc, vc, ks, vs, _table(1, pages, pages, 20), [news], [n], **kw)
