@@ -45,6 +45,21 @@ GPTQ_DEV int exact_code(double p, double top, double inv) {
 #define GPTQ_OPAQUE(x) \
   if constexpr (sizeof(x) >= 8) asm volatile("" : "+v"(x))
 
+// A 64-bit number rounded to E once. For 16 bits it goes through fp32, where a result that is not exact takes the one of
+// its two neighbours whose last bit is set (rounding to odd): that lies on no border of the shorter type.
+template <typename E>
+GPTQ_DEV E rounded(double v) {
+  float f = (float)v;
+  if constexpr (sizeof(E) < 4) {
+    if ((double)f != v) {
+      uint32_t b = __builtin_bit_cast(uint32_t, f);
+      if (fabs((double)f) > fabs(v)) --b;
+      f = __builtin_bit_cast(float, b | 1u);
+    }
+  }
+  return (E)f;
+}
+
 // A weight in 64 bits, formed where it is used.
 GPTQ_DEV double wide(float w) {
   asm volatile("" : "+v"(w));
@@ -238,7 +253,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_quant_kernel(NormArgs 
       if (y) {
         Vec yv;
 #pragma unroll
-        for (int e = 0; e < V; ++e) yv[e] = (E)(float)((double)(float)h[i][e] * wide(wi[e]) * rho);
+        for (int e = 0; e < V; ++e) yv[e] = rounded<E>((double)(float)h[i][e] * wide(wi[e]) * rho);
         store(y, i, yv);
       }
     }

@@ -144,3 +144,33 @@ def test_queries_with_a_channel_far_larger(news, dtype):
     q = torch.from_numpy(q).to(_dtype(dtype)).cuda()
     for kw in ({}, dict(cap=8.0)):
         _attend(dtype, q, kc, vc, ks, vs, _table(1, pages, pages, 20), [news], [n], **kw)
+
+
+# -------------------------------------------------------------------------------------- norm_quant
+
+def _round_to(dtype, v):
+    """float64 numbers to the nearest of the type, ties to even, in one step, as float64; and where they are within 2^-40
+    of a tie: 64-bit sums of up to 4096 squares and a few roundings more do not decide those."""
+    bits, low = {"f16": (11, -24), "bf16": (8, -133), "f32": (24, -149)}[dtype]
+    _, e = np.frexp(v)
+    step = np.ldexp(1.0, np.maximum(e - bits, low))
+    q = v / step
+    return np.rint(q) * step, np.abs(q - np.floor(q) - 0.5) < np.ldexp(1.0, bits - 40)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("d,size", [(96, 1.0), (4096, 1.0), (1001, 1e-5)])
+def test_normed_rows_are_rounded_once(d, size, dtype):
+    """y is the rounding of the 64-bit result: many elements, since a second rounding shows in one of some ten thousand."""
+    torch = torch_cuda()
+    n = (1 << 21) // d
+    x = _rand((n, d), 35, dtype)
+    w = _rand((d,), 36, "f32", size)
+    y = torch.empty_like(x)
+    _g().gptq_norm_quant(x, None, w, eps=1e-5, y=y)
+    torch.cuda.synchronize()
+    h, wn = _np(x), _np(w)
+    v = h * wn / np.sqrt((h * h).sum(1, keepdims=True) / d + 1e-5)
+    want, unclear = _round_to(dtype, v)
+    off = (_np(y) != want) & ~unclear
+    assert not off.any(), int(off.sum())
