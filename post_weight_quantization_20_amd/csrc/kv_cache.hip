@@ -236,10 +236,11 @@ GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, b
 
   float ky[kKeep][V], kz[kKeep][V];
   double top = 0.0;
-  float odd = 0.f;
+  bool bad = false;   // a value is not finite
   each(false, [&](int b, int t, int c) {
     double y[V], z[V];
     values(t, c, y, z);
+    float odd = 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       top = fmax(top, fmax(fabs(y[e]), fabs(z[e])));
@@ -247,8 +248,12 @@ GPTQ_DEV void append_head(const AppendArgs& a, const Unit& u, int h, int lane, b
       kz[b][e] = (float)z[e];
       odd = __builtin_fmaf(ky[b][e], 0.f, __builtin_fmaf(kz[b][e], 0.f, odd));
     }
+    if (!(odd == 0.f)) {   // rotated beyond fp32's largest number, or not finite at all
+#pragma unroll
+      for (int e = 0; e < V; ++e) bad |= !(fabs(y[e]) < INFINITY && fabs(z[e]) < INFINITY);
+    }
   });
-  if (!(odd == 0.f)) top = INFINITY;
+  if (bad) top = INFINITY;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o, 64));
 

@@ -174,3 +174,43 @@ def test_normed_rows_are_rounded_once(d, size, dtype):
     want, unclear = _round_to(dtype, v)
     off = (_np(y) != want) & ~unclear
     assert not off.any(), int(off.sum())
+
+
+# --------------------------------------------------------------------------------------- kv_append
+
+@pytest.mark.parametrize("tokens", [3, 40])
+@pytest.mark.parametrize("dh", [32, 6])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_keys_whose_rotation_passes_fp32s_largest(dtype, dh, tokens):
+    """Finite keys near fp32's largest, rotated to up to sqrt(2) times it: their page's scale is the 127th of that, finite,
+    and the codes stand on it. An infinity or NaN still makes the scale NaN."""
+    torch = torch_cuda()
+    print(f"large keys {(dtype, dh, tokens)}", flush=True)
+    g = _g()
+    pages = -(-tokens // 16)
+    k = _rand((tokens, 2, dh), 40, dtype)
+    k[1:3] = 3.3e38 * torch.sign(k[1:3])
+    v = _rand((tokens, 2, dh), 41, dtype)
+    f = torch.from_numpy((10000.0 ** (-np.arange(dh // 2) * 2 / dh)).astype(np.float32)).cuda()
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda:0")
+    table = np.arange(pages, dtype=np.int32)[None]
+
+    def run(keys):
+        kc, vc = (torch.zeros(pages, 16, 2, dh, dtype=torch.int8, device="cuda:0") for _ in range(2))
+        ks, vs = (torch.zeros(pages, 2, device="cuda:0") for _ in range(2))
+        g.gptq_kv_append(keys, v, kc, vc, ks, vs, _ints(table), _ints([0]), positions=pos, inv_freq=f)
+        torch.cuda.synchronize()
+        return kc, ks
+
+    kc, ks = run(k)
+    turned = serve_ref.rotate(_np(k), pos.cpu().numpy()[None], _np(f))
+    assert np.abs(turned).max() > float(torch.finfo(torch.float32).max)
+    want, sc, quot = serve_ref.kv_append(turned, np.zeros((pages, 16, 2, dh)), np.zeros((pages, 2), np.float32), table,
+                                         [0, tokens], [0])
+    assert np.isfinite(sc).all() and np.array_equal(ks.cpu().numpy(), sc)
+    got = kc.cpu().numpy().astype(np.float64)
+    off = got != want
+    assert np.all(np.abs(quot - np.floor(quot) - 0.5)[off] < 1e-9)
+    k[2, 1, dh - 1] = float("inf")
+    _, ks = run(k)
+    assert torch.isnan(ks[0, 1]) and torch.isfinite(ks[0, 0]) and torch.isfinite(ks[1:]).all()
