@@ -62,8 +62,6 @@ def _heads(t: torch.Tensor, name: str, dtype=None) -> Tuple[int, int, int, int, 
         raise ValueError(f"{name} must be [tokens, heads, head_dim], "
                          + ("fp32/fp16/bf16" if dtype is None else str(dtype)))
     n, h, d = t.shape
-    if n == 0:   # no element: any strides
-        return n, h, d, h * d, d
     ld, hp, unit = t.stride()
     if d > 1 and unit != 1:
         raise ValueError(f"{name} must have unit stride along head_dim")

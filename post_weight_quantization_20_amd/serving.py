@@ -26,6 +26,13 @@ def _rows(t: torch.Tensor, shape: tuple, dtype, name: str) -> int:
     return t.stride(0) if shape[0] > 1 else max(shape[1], 1)
 
 
+def _tokens(t: torch.Tensor, name: str, dtype=None) -> Tuple[int, int, int, int, int]:
+    """_heads, where a tensor without tokens may have any strides."""
+    if t.dim() == 3 and t.shape[0] == 0:
+        t = t.new_empty(t.shape)
+    return _heads(t, name, dtype)
+
+
 def gptq_norm_quant(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
                     eps: float = 1e-6, sum_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                     codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
@@ -136,8 +143,8 @@ def gptq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     tokens' places unless given."""
     dev = _device(k, v, k_cache, v_cache, k_scales, v_scales, table, past, start, positions, inv_freq, pair_axis)
     c = _cache(k_cache, v_cache, k_scales, v_scales, table)
-    n, hk, dh, k_ld, k_hp = _heads(k, "k")
-    nv, hv, dv, v_ld, v_hp = _heads(v, "v", k.dtype)
+    n, hk, dh, k_ld, k_hp = _tokens(k, "k")
+    nv, hv, dv, v_ld, v_hp = _tokens(v, "v", k.dtype)
     if (hk, dh) != (c.kv_heads, c.head_dim) or (nv, hv, dv) != (n, hk, dh):
         raise ValueError("k and v must be [n, kv_heads, head_dim] with the cache's heads")
     seqs = table.shape[0]
@@ -165,12 +172,12 @@ def gptq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
 
 
 def _kv_attention_args(q, seqs, c, scale, causal, window, softcap, out=None) -> _lib.gptq_kv_attention_t:
-    nq, hq, dh, q_ld, q_hp = _heads(q, "q")
+    nq, hq, dh, q_ld, q_hp = _tokens(q, "q")
     if dh != c.head_dim or hq == 0 or c.kv_heads == 0 or hq % c.kv_heads:
         raise ValueError("q must have the cache's head_dim and a multiple of its heads")
     o_ld, o_hp = hq * dh, dh
     if out is not None:
-        no, ho, do, o_ld, o_hp = _heads(out, "out", q.dtype)
+        no, ho, do, o_ld, o_hp = _tokens(out, "out", q.dtype)
         if (no, ho, do) != (nq, hq, dh):
             raise ValueError("out must have q's shape")
     if scale is None:

@@ -252,3 +252,17 @@ def test_oracle_rotation_is_complex_multiplication():
     got = serve_ref.rotate(x, np.array([[1, 5, 9]]), f)
     z = (x[..., :2] + 1j * x[..., 2:4]) * np.exp(1j * np.array([1, 5, 9])[:, None] * f.astype(np.float64))[:, None]
     assert np.allclose(got[..., :2], z.real) and np.allclose(got[..., 2:4], z.imag) and np.array_equal(got[..., 4:], x[..., 4:])
+
+
+def test_binding_layouts_without_tokens():
+    """Without a token any strides pass here; attention over packed sequences refuses them, as ever."""
+    torch = pytest.importorskip("torch")
+    from post_weight_quantization_20_amd import attention, serving
+    z = torch.empty_strided((0, 2, 32), (0, 0, 0))
+    assert serving._tokens(z, "z")[:3] == (0, 2, 32)
+    with pytest.raises(ValueError, match="fp32"):
+        serving._tokens(z.int(), "z")
+    with pytest.raises(ValueError, match="unit stride"):
+        attention._heads(z, "z")
+    with pytest.raises(ValueError, match="unit stride"):
+        serving._tokens(torch.empty(32, 2, 3).permute(2, 1, 0), "z")

@@ -214,3 +214,24 @@ def test_keys_whose_rotation_passes_fp32s_largest(dtype, dh, tokens):
     k[2, 1, dh - 1] = float("inf")
     _, ks = run(k)
     assert torch.isnan(ks[0, 1]) and torch.isfinite(ks[0, 0]) and torch.isfinite(ks[1:]).all()
+
+
+# ---------------------------------------------------------------------------------------- no tokens
+
+def test_no_tokens_in_any_layout():
+    """Tensors without an element pass in whatever strides where serving in 8 bits takes them; attention over packed
+    sequences and norm with rotation refuse columns that are not side by side, as ever."""
+    torch = torch_cuda()
+    g = _g()
+    z = torch.empty_strided((0, 2, 32), (0, 0, 0), dtype=torch.float16, device="cuda:0")
+    kc, ks = _pool(2, 16, 2, 32, 1)
+    t, n = _ints([[0], [1]]), _ints([0, 0])
+    before = kc.clone()
+    g.gptq_kv_append(z, z, kc, kc.clone(), ks, ks.clone(), t, n)
+    assert g.gptq_kv_attention(z, kc, kc, ks, ks, t, n).shape == (0, 2, 32)
+    torch.cuda.synchronize()
+    assert torch.equal(kc, before)
+    with pytest.raises(ValueError, match="unit stride"):
+        g.gptq_norm_rotate(z)
+    with pytest.raises(ValueError, match="unit stride"):
+        g.gptq_attention(z, z, z)
