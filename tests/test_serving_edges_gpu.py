@@ -148,6 +148,57 @@ def test_queries_with_a_channel_far_larger(news, dtype):
 
 # -------------------------------------------------------------------------------------- norm_quant
 
+SIZES = [(1, 1), (3, 2), (5, 7), (2, 8), (9, 63), (4, 64), (7, 255), (3, 512), (6, 513), (5, 1000), (3, 1024), (2, 2049),
+         (3, 4097), (2, 8200), (2, 11008), (1, 16389), (1, 40001), (1, 65535), (3000, 97), (2500, 1030)]
+
+
+def _same_bits(got, want):
+    torch = torch_cuda()
+    kind = torch.int32 if got.dtype == torch.float32 else torch.int16
+    return torch.equal(got.contiguous().view(kind), want.contiguous().view(kind))
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("n,d", SIZES)
+def test_sums_bit_for_bit(n, d, dtype):
+    """The sum is x + residual rounded once, into a new array, a range of a wider one (what lies beside is left as it
+    was), over either input; without a residual it is x."""
+    torch = torch_cuda()
+    print(f"sums {(n, d, dtype)}", flush=True)
+    g = _g()
+    x, r = _rand((n, d), 31, dtype, 3.0), _rand((n, d), 32, dtype)
+    want = (x.float() + r.float()).to(x.dtype)
+    _, _, total = g.gptq_norm_quant(x, r)
+    torch.cuda.synchronize()
+    assert _same_bits(total, want)
+    base = torch.full((n + 2, d + 9), 7.0, dtype=x.dtype, device="cuda:0")
+    g.gptq_norm_quant(x, r, sum_out=base[1:n + 1, 4:4 + d])
+    alone = torch.full((n + 2, d + 9), 7.0, dtype=x.dtype, device="cuda:0")
+    g.gptq_norm_quant(x, sum_out=alone[1:n + 1, 3:3 + d])
+    torch.cuda.synchronize()
+    for got, at, held in ((base, 4, want), (alone, 3, x)):
+        assert _same_bits(got[1:n + 1, at:at + d], held)
+        got[1:n + 1, at:at + d] = 7.0
+        assert torch.all(got == 7.0)
+    x2, r2 = x.clone(), r.clone()
+    g.gptq_norm_quant(x2, r, sum_out=x2)
+    g.gptq_norm_quant(x, r2, sum_out=r2)
+    torch.cuda.synchronize()
+    assert _same_bits(x2, want) and _same_bits(r2, want)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_sums_that_are_not_finite(dtype):
+    torch = torch_cuda()
+    x, r = _rand((4, 600), 33, dtype), _rand((4, 600), 34, dtype)
+    x[1, 599], r[2, 0], x[3, 8], r[3, 8] = float("inf"), float("nan"), float("inf"), -float("inf")
+    want = (x.float() + r.float()).to(x.dtype)
+    _, _, total = _g().gptq_norm_quant(x, r)
+    torch.cuda.synchronize()
+    gone = want.isnan()
+    assert torch.equal(total.isnan(), gone) and torch.equal(total[~gone], want[~gone])
+
+
 def _round_to(dtype, v):
     """float64 numbers to the nearest of the type, ties to even, in one step, as float64; and where they are within 2^-40
     of a tie: 64-bit sums of up to 4096 squares and a few roundings more do not decide those."""
