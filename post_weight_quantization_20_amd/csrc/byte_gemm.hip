@@ -450,7 +450,7 @@ hipError_t ask_lds(K kernel, size_t lds, std::atomic<uint64_t>& asked) {
 template <bool WHOLE, bool CODES, int YT>
 hipError_t launch_tile(const GemmI8& a, hipStream_t s) {
   static std::atomic<uint64_t> asked{0};
-  constexpr size_t lds = 2 * 2 * BT * KB + 6144;   // two stages; the epilogue of fp32 outputs takes as much
+  constexpr size_t lds = 2 * 2 * BT * KB;   // two stages; the epilogue takes at most 69 KB of it
   auto f = tile_kernel<WHOLE, CODES, YT>;
   const hipError_t e = ask_lds(f, lds, asked);
   if (e != hipSuccess) return e;

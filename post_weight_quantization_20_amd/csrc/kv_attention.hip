@@ -163,13 +163,11 @@ __global__ __launch_bounds__(256) void kv_row_kernel(KvArgs a) {
 // keys 49 + 9; four chunks of 512 against up to 4096 343 us, where every 16 rows read and widen K and V again.
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 
 constexpr int kRowTile = 16, kKeyTile = 32;
 constexpr int kParts = 512;        // workgroups: two a CU
 constexpr int kMinTiles = 4;       // key tiles that a workgroup takes at least
-constexpr int kJoinRows = 1;       // rows of a unit that a workgroup joins
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kShift = 7.0f, kRaise = 8.0f;
 constexpr int kQueryExp = 14;      // a scaled row's largest element is in [2^14, 2^15)
@@ -278,8 +276,6 @@ GPTQ_DEV int64_t part_size(int64_t total, int parts) {
   const int64_t n = (total + parts - 1) / parts;
   return n < kMinTiles ? kMinTiles : n;
 }
-
-GPTQ_DEV float load_q(const KvArgs& a, int dtype, int64_t at) { return load_as_f32(a.q, dtype, at); }
 
 GPTQ_DEV half2v widen(uint32_t pair) {   // bytes c ^ 128 under the exponent of 1024
   return __builtin_bit_cast(half2v, pair) - half2v{(_Float16)1152.0f, (_Float16)1152.0f};
@@ -706,21 +702,18 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
   if (!whole && threadIdx.x == 0) f.head[blockIdx.x] = left;
 }
 
-// Joins the partial results of a unit that several workgroups shared, in their order: workgroup w the unit that
-// part w began and did not end.
+// Joins the partial results of a row of a unit that several workgroups shared, in their order: workgroup (w, n) row n of
+// the unit that part w began and did not end.
 __global__ __launch_bounds__(256) void kv_join_kernel(FewArgs f, int dtype) {
   const KvArgs& a = f.a;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w0 = blockIdx.x;
+  const int lane = threadIdx.x & 63, w0 = blockIdx.x, n = blockIdx.y;
   const Head hd = f.head[w0];
-  if (hd.last < 0) return;
+  if (hd.last < 0 || hd.row0 + n >= hd.lq * a.group) return;
   const int parts = hd.last - w0 + 1, dh = a.dh;
-  // rows n0 .. n0 + rows - 1 of the unit
-  const int n0 = kJoinRows * blockIdx.y, rows = (int)min((int64_t)kJoinRows, hd.lq * a.group - hd.row0 - n0);
-  if (rows <= 0) return;
-  __shared__ float share[kJoinRows][kParts];
+  __shared__ float share[kParts];
   __shared__ floatx4 sums[256];
-  auto slot = [&](int w, int n) { return ((int64_t)2 * (w0 + w) + (w == 0 ? 1 : 0)) * kRowTile + n0 + n; };
-  for (int n = wave; n < rows; n += 4) {
+  auto slot = [&](int w) { return ((int64_t)2 * (w0 + w) + (w == 0 ? 1 : 0)) * kRowTile + n; };
+  if (threadIdx.x < 64) {
     float m = -INFINITY, l = 0.f, mw[kParts / 64], lw[kParts / 64];
 #pragma unroll
     for (int i = 0; i < kParts / 64; ++i) {
@@ -728,7 +721,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(FewArgs f, int dtype) {
       mw[i] = -INFINITY;
       lw[i] = 0.f;
       if (w < parts) {
-        const float2 ml = *reinterpret_cast<const float2*>(f.part_ml + 2 * slot(w, n));
+        const float2 ml = *reinterpret_cast<const float2*>(f.part_ml + 2 * slot(w));
         lw[i] = ml.y;
         if (ml.y != 0.f) mw[i] = ml.x;
       }
@@ -743,49 +736,41 @@ __global__ __launch_bounds__(256) void kv_join_kernel(FewArgs f, int dtype) {
     l = wave_add(l);
 #pragma unroll
     for (int i = 0; i < kParts / 64; ++i)
-      if (64 * i + lane < parts) share[n][64 * i + lane] = lw[i] == 0.f ? 0.f : lw[i] / l;
+      if (64 * i + lane < parts) share[64 * i + lane] = lw[i] == 0.f ? 0.f : lw[i] / l;
   }
   __syncthreads();
-  // four columns a thread, and where that leaves threads over, the parts shared among them
-  const int quads = dh >> 2, items = rows * quads, split = max(1, 256 / items);
-  for (int i0 = 0; i0 < items; i0 += 256) {
-    const int it = split > 1 ? (int)threadIdx.x % items : i0 + (int)threadIdx.x;
-    const int z = split > 1 ? (int)threadIdx.x / items : 0;
-    const int n = it / quads, c = 4 * (it - n * quads);
-    floatx4 o = {0.f, 0.f, 0.f, 0.f};
-    if (it < items && z < split) {
-      for (int w = z; w < parts; w += 4 * split) {
-        floatx4 x[4];
+  // four columns a thread (dh <= 256: at most 64 of them), and the parts shared among the threads that leaves over
+  const int quads = dh >> 2, split = 256 / quads;
+  const int z = (int)threadIdx.x / quads, c = 4 * ((int)threadIdx.x - z * quads);
+  floatx4 o = {0.f, 0.f, 0.f, 0.f};
+  if (z < split) {
+    for (int w = z; w < parts; w += 4 * split) {
+      floatx4 x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int u = w + e * split;
-          x[e] = floatx4{0.f, 0.f, 0.f, 0.f};
-          if (u < parts && share[n][u] != 0.f)
-            x[e] = *reinterpret_cast<const floatx4*>(f.part_o + slot(u, n) * dh + c) * share[n][u];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o += x[e];
+      for (int e = 0; e < 4; ++e) {
+        const int u = w + e * split;
+        x[e] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (u < parts && share[u] != 0.f)
+          x[e] = *reinterpret_cast<const floatx4*>(f.part_o + slot(u) * dh + c) * share[u];
       }
-    }
-    if (split > 1) {
-      sums[threadIdx.x] = o;
-      __syncthreads();
-      if (z == 0)
-        for (int e = 1; e < split; ++e) o += sums[threadIdx.x + e * items];
-    }
-    if (it < items && z == 0) {
-      const int64_t r = hd.row0 + n0 + n, qi = r / a.group;
-      const int64_t o_at = (hd.q0 + qi) * a.o_ld + (hd.kvh * a.group + (r - qi * a.group)) * a.o_hp + c;
-      auto put = [&](auto* dst) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          dst[e] = (typename std::remove_reference<decltype(*dst)>::type)o[e];
-      };
-      if (dtype == F32) put(static_cast<float*>(a.out) + o_at);
-      else if (dtype == F16) put(static_cast<_Float16*>(a.out) + o_at);
-      else put(static_cast<__bf16*>(a.out) + o_at);
+      for (int e = 0; e < 4; ++e) o += x[e];
     }
   }
+  sums[threadIdx.x] = o;
+  __syncthreads();
+  if (z != 0) return;
+  for (int e = 1; e < split; ++e) o += sums[threadIdx.x + e * quads];
+  const int64_t r = hd.row0 + n, qi = r / a.group;
+  const int64_t o_at = (hd.q0 + qi) * a.o_ld + (hd.kvh * a.group + (r - qi * a.group)) * a.o_hp + c;
+  auto put = [&](auto* dst) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      dst[e] = (typename std::remove_reference<decltype(*dst)>::type)o[e];
+  };
+  if (dtype == F32) put(static_cast<float*>(a.out) + o_at);
+  else if (dtype == F16) put(static_cast<_Float16*>(a.out) + o_at);
+  else put(static_cast<__bf16*>(a.out) + o_at);
 }
 
 template <int DHP, int TERMS>
@@ -851,7 +836,7 @@ hipError_t kv_attention(const gptq_kv_attention_t& t, const gptq_kv_cache_t& c, 
                    : a.dh <= 128 ? (two ? launch_few<128, 2>(f, t.dtype, grid, s) : launch_few<128, 1>(f, t.dtype, grid, s))
                                  : (two ? launch_few<256, 2>(f, t.dtype, grid, s) : launch_few<256, 1>(f, t.dtype, grid, s));
     if (e != hipSuccess || !f.parts) return e;
-    hipLaunchKernelGGL(kv_join_kernel, dim3((unsigned)f.parts, kRowTile / kJoinRows), dim3(256), 0, s, f, t.dtype);
+    hipLaunchKernelGGL(kv_join_kernel, dim3((unsigned)f.parts, kRowTile), dim3(256), 0, s, f, t.dtype);
     return hipGetLastError();
   }
   const int64_t waves = a.nq * a.hq;

@@ -288,8 +288,9 @@ hipError_t by_width(const NormArgs& a, hipStream_t s) {
   if (chunks <= 2 * 1024) return launch<DT, V, 1024, 2>(a, s);
   if (chunks <= 3 * 1024) return launch<DT, V, 1024, 3>(a, s);
   if (chunks <= 4 * 1024) return launch<DT, V, 1024, 4>(a, s);
-  if (chunks <= 8 * 1024) return launch<DT, V, 1024, 8>(a, s);
-  return launch<DT, V, 1024, 64 / V>(a, s);
+  if constexpr (DT == F32)
+    if (chunks > 8 * 1024) return launch<DT, V, 1024, 16>(a, s);
+  return launch<DT, V, 1024, 8>(a, s);
 }
 
 }  // namespace
