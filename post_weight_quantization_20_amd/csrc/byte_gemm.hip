@@ -80,7 +80,10 @@ GPTQ_DEV int add_bytes(i32x4 v, int sum) {
 constexpr int BT = 256;                 // tile edge
 constexpr int KB = 128;                 // columns of a stage
 constexpr int GROUP = 8;                // row tiles that run side by side
-constexpr uint32_t kStripTiles = 96;    // fewer quarter tiles than this: strips
+// Up to so many tiles go to strips instead, which read x again for every strip but leave no CU idle: 256 tokens by 4096
+// outputs (16 tiles) of 4096 columns take 17.0 us as strips and 19.6 as tiles, by 5120 outputs (20 tiles) 24.5 and 19.8;
+// the two sides cross there with 1024 and 11008 columns and with 512 and 1024 tokens too.
+constexpr uint32_t kStripTiles = 16;
 
 // Tile `slot` of an order in which GROUP row tiles run side by side through the column tiles.
 GPTQ_DEV void tile_at(const GemmI8& a, uint32_t slot, uint32_t& tm, uint32_t& tn) {
@@ -491,7 +494,7 @@ hipError_t one(GemmI8 a, hipStream_t s) {
   a.whole_tiles = tiles / 256 * 256;
   const uint32_t rest = tiles - a.whole_tiles;
   a.cut = rest > 128 ? 1 : rest > 64 ? 2 : 4;
-  if (a.m > 128 && tiles * 4 >= kStripTiles) {
+  if (a.m > 128 && tiles > kStripTiles) {
     // 16-byte units inside rows of whole words, and a tile inside 31-bit offsets
     const bool whole = a.d % 16 == 0 && reinterpret_cast<uintptr_t>(a.x) % 4 == 0 &&
                        reinterpret_cast<uintptr_t>(a.w) % 4 == 0 && a.ld_x % 4 == 0 && a.ld_w % 4 == 0 &&
@@ -499,13 +502,15 @@ hipError_t one(GemmI8 a, hipStream_t s) {
     if (whole) return a.z ? tile_type<true, true>(a, s) : tile_type<true, false>(a, s);
     return a.z ? tile_type<false, true>(a, s) : tile_type<false, false>(a, s);
   }
-  // Strips as wide as leaves a workgroup to each CU: 16 NB outputs.
+  // Strips as wide as leaves a workgroup to each CU: 16 NB outputs. Of as many blocks of 16 tokens as hold the call's, or
+  // the next of 1, 2, 4, 6 and 8: with 4096 outputs of 4096 columns 48 tokens take the 10.5 us of 64, and 112 the 20 of
+  // 128, so blocks of 3 and 7 would gain little; 96 take 14.0 in blocks of 6 and 20.1 in blocks of 8.
   const int64_t mb = (std::min<int64_t>(a.m, 128) + 15) / 16, chunks = (a.m + 127) / 128;
   const int nb = (int)std::min<int64_t>(4, std::max<int64_t>(1, ((a.rows + 15) / 16 * chunks + 255) / 256));
   if (mb <= 1) return strip<1>(a, nb, s);
   if (mb <= 2) return strip<2>(a, nb, s);
   if (mb <= 4) return strip<4>(a, nb, s);
-  if (mb <= 6 && chunks == 1) return strip<6>(a, nb, s);
+  if (mb <= 6) return strip<6>(a, nb, s);
   return strip<8>(a, nb, s);
 }
 

@@ -16,7 +16,8 @@ import pytest
 
 from gpu_util import torch_cuda
 from oracle import serve_ref
-from test_serving_gpu import DT, U, _dtype, _g, _half_step, _ints, _np, _pool, _rand, _starts, _table
+from test_serving_gpu import (DT, U, _check_gemm, _dtype, _g, _gemm_inputs, _half_step, _ints, _np, _pool, _rand, _starts,
+                              _table)
 
 pytestmark = pytest.mark.gpu
 
@@ -265,6 +266,20 @@ def test_keys_whose_rotation_passes_fp32s_largest(dtype, dh, tokens):
     k[2, 1, dh - 1] = float("inf")
     _, ks = run(k)
     assert torch.isnan(ks[0, 1]) and torch.isfinite(ks[0, 0]) and torch.isfinite(ks[1:]).all()
+
+
+# --------------------------------------------------------------------------------------- byte_gemm
+
+@pytest.mark.parametrize("m,rows", [(256, 4096), (256, 4097), (257, 2048), (513, 1280), (129, 4224), (1000, 1030)])
+@pytest.mark.parametrize("stored", [False, True])
+def test_products_on_both_sides_of_strips_and_tiles(stored, m, rows):
+    """16 tiles of 256 x 256 and a few more, with a last partial stage of columns."""
+    torch = torch_cuda()
+    print(f"strips and tiles {(m, rows, stored)}", flush=True)
+    x, xs, w, ws, z = _gemm_inputs(m, 400, rows, stored, seed=50)
+    y = _g().gptq_byte_gemm(x, xs, w, ws, z, dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    _check_gemm(x, xs, w, ws, z, y)
 
 
 # ---------------------------------------------------------------------------------------- no tokens
