@@ -619,7 +619,7 @@ typedef struct {
  * than 2^-39 of their row's largest with both (so fp32's keep 22 bits down to 2^-18 of it, and bf16's are exact down
  * to 2^-31). Each probability times its value's scale keeps 22 bits before it weighs a code, whatever the type, or
  * 2^-30 of the largest such product of the query's keys where that is coarser (probabilities below fp32's normal range
- * count as zero). Scales of pages that a query does not see take no part in its row. Results do not depend on
+ * may count as zero). Scales of pages that a query does not see take no part in its row. Results do not depend on
  * scheduling. Launches on `stream` alone; the call may be captured in a graph.
  */
 gptq_status_t gptq_kv_attention(const gptq_kv_attention_t *a, const gptq_kv_cache_t *cache, const void *q,

@@ -10,8 +10,9 @@
 //   strip   up to 128 tokens and as many outputs as give each CU a workgroup, whose waves share the sum over k and read
 //           both operands straight from memory
 //
-// Measured: 8192 x 4096 x 11008 in 361 us, 2.05 POPS (random data, the board's power limit holds the clock at 1.75 GHz;
-// zeros run at 3.3); 96 x 4096 x 11008 with zeros in 21 us; 8 x 4096 x 4096 in 6.4 us, 2.6 TB/s.
+// Measured, calls after one another: 8192 x 4096 x 11008 in 369 us, 2.0 POPS (random data, the board's power limit holds
+// the clock at 1.73 GHz; 278 us where the data is zero), with codes 413 us; 96 x 4096 x 11008 with codes in 22 us;
+// 8 x 4096 x 4096 in 5.5 us, 3.0 TB/s.
 #include "common.hpp"
 
 #include <atomic>
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(256) void tile_kernel(GemmI8 a) {
 // The waves share the sum over k in blocks of 128 columns and add their sums up in LDS. Both operands come straight
 // from memory, the next block's while one is multiplied: a byte of w is read by one wave. An instruction reads 64
 // bytes of each of 16 rows, the first half of a line of even rows and the second of odd ones, which the cache serves
-// side by side (128 x 4096 x 4096: 17.5 us against 21 with one half of all); the halves change places in registers. Few
+// side by side (128 x 4096 x 4096: 15.6 us against 21.9 with one half of all); the halves change places in registers. Few
 // tokens are bound by reading w, more of them by reading x again for every strip.
 template <int MB, int NB, int WAVES, bool CODES>
 __global__ __launch_bounds__(64 * WAVES) void strip_kernel(GemmI8 a) {

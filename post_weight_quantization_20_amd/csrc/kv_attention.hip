@@ -146,12 +146,12 @@ __global__ __launch_bounds__(256) void kv_row_kernel(KvArgs a) {
 // taken as they are), so that its smaller elements stay above fp16's smallest steps: bf16 ones are exact down to 2^-31 of
 // the largest. fp32 ones are two fp16 terms.
 // Probabilities are two terms for every type: one of 11 bits moves an output by up to 2^-11 of sum p |v|, which is as
-// much as its own rounding to fp16 and shows wherever values cancel. The second product costs 0.5 of 55 us for 16 tokens
-// against caches of up to 8192, and 23 of 371 for four chunks of 512.
+// much as its own rounding to fp16 and shows wherever values cancel. The second product costs 1 % for 16 tokens against
+// caches of up to 8192, and 6 % for four chunks of 512 against up to 4096.
 // A key block's scale multiplies its scores, a value block's its probabilities. The products are kept in fp16's range by
 // a power of two a row, which bounds those of the keys that the row has seen, probability and scale together: neither a
 // scale that a row does not see nor one that its probabilities make small takes bits from the others. (One power for
-// the wave, of all scales that it loads, would save 9 of 380 us for the chunks, and loses rows whose scales are small.)
+// the wave, of all scales that it loads, would save 2 % for the chunks, and loses rows whose scales are small.)
 //
 // Workgroups share the work by keys: the tiles of 32 keys of all (sequence, key head, 16 rows) are one list, of which
 // each takes an equal, contiguous part, whatever the lengths are. A part begins and ends anywhere; where it holds
@@ -159,8 +159,9 @@ __global__ __launch_bounds__(256) void kv_row_kernel(KvArgs a) {
 // about 8 us before its first key (lengths, pages, keys, one after another), so there are no more of them than run at
 // once: 16 tokens against caches of up to 8192 take 54 us with 512 parts, 61 with 768, 81 with 2048.
 //
-// Measured there: 6.9 TB/s while a part reads, 168 MB in 48 us with start and end, the join 6; one token against 100003
-// keys 49 + 9; four chunks of 512 against up to 4096 343 us, where every 16 rows read and widen K and V again.
+// Measured there: 168 MB in 48 us with start and end, 3.5 TB/s, and the join 5; one token against 100003 keys 49 + 9; four
+// chunks of 512 against up to 4096 in 413 us after one another, 372 with pauses, where every 16 rows read and widen K and
+// V again.
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));

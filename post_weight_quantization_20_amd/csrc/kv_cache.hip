@@ -12,7 +12,7 @@
 // half, so the code is the rounding of the exact quotient but for the last bits of 64.
 //
 // Measured: 8 bf16 prompts of 10.7 thousand tokens, 8 heads of 128, into pages of 16 in 61 us (71 MB: 14 us at a copy's
-// rate), bound by about 50 vector instructions an element; one token of each of 32 sequences in 10 us.
+// rate), bound by about 50 vector instructions an element; one token of each of 32 sequences in 9 us.
 #include "common.hpp"
 
 namespace gptq {

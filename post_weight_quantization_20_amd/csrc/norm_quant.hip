@@ -12,7 +12,7 @@
 // exact in fp32 within its range; others, and quotients that fp32 finds near a half, are formed in 64 bits, so that a
 // code is the rounding of the exact quotient.
 //
-// Measured: 8192 rows of 4096 bf16 elements in 55 us, 4.3 TB/s (a copy: 5.2); 5003 fp32 rows of 11008 in 112 us, bound
+// Measured: 8192 rows of 4096 bf16 elements in 54 us, 4.3 TB/s (a copy: 5.1); 5003 fp32 rows of 11008 in 111 us, held up
 // by the 64-bit products; 8 rows in 5.
 #include "common.hpp"
 
