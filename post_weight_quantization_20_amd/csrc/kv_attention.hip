@@ -170,7 +170,9 @@ constexpr int kRowTile = 16, kKeyTile = 32;
 constexpr int kParts = 512;        // workgroups: two a CU
 constexpr int kMinTiles = 4;       // key tiles that a workgroup takes at least
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kShift = 7.0f, kRaise = 8.0f;
+// exp2(score - m + kShift), and its product with a value's scale in units of 2^ve, stay below 2^15 while a score passes m by
+// no more than kRaise: kShift - m may round up by one where m is large.
+constexpr float kShift = 7.0f, kRaise = 7.0f;
 constexpr int kQueryExp = 14;      // a scaled row's largest element is in [2^14, 2^15)
 constexpr int kNoExp = -1000;      // the exponent of a scale that is zero or not finite
 
@@ -491,8 +493,8 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;                 // of the row: the scores' maximum and sum
-    float mt = -INFINITY;                         // and the maximum of score + exponent of the value's scale
-    int ve = 0;                                   // ceil(mt - m): acc is in units of 2^ve
+    float mt = -INFINITY;                         // and that of score - m + exponent of the value's scale
+    int ve = 0;                                   // ceil(mt): acc is in units of 2^ve
 
     for (int32_t tb = tfirst; tb < tend;) {
       vx = kNoExp;
@@ -540,24 +542,26 @@ __global__ __launch_bounds__(256, DHP <= 128 ? 2 : 1) void kv_few_kernel(FewArgs
             }
         }
         int sx[2];
-        float mx = -INFINITY, tx = -INFINITY;
+        float ms[2], mx = -INFINITY, tx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           sx[e] = __builtin_amdgcn_readlane(vx, 2 * i + e);
-          const float x = fmaxf(fmaxf(S[e][0], S[e][1]), fmaxf(S[e][2], S[e][3]));
-          mx = fmaxf(mx, x);
-          tx = fmaxf(tx, x + (float)sx[e]);
+          ms[e] = fmaxf(fmaxf(S[e][0], S[e][1]), fmaxf(S[e][2], S[e][3]));
+          mx = fmaxf(mx, ms[e]);
+          tx = fmaxf(tx, (ms[e] - m) + (float)sx[e]);   // in this order: a large score has no room for an exponent
         }
         if (__ballot(!(mx <= m + kRaise && tx <= mt + kRaise))) {
           mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-          tx = fmaxf(tx, __shfl_xor(tx, 16, 64));
           mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-          tx = fmaxf(tx, __shfl_xor(tx, 32, 64));
           const float m2 = fmaxf(m, mx);
-          mt = fmaxf(mt, tx);
+          tx = fmaxf((ms[0] - m2) + (float)sx[0], (ms[1] - m2) + (float)sx[1]);
+          tx = fmaxf(tx, __shfl_xor(tx, 16, 64));
+          tx = fmaxf(tx, __shfl_xor(tx, 32, 64));
           if (m2 != -INFINITY) {
-            const int ve2 = (int)ceilf(fminf(fmaxf(mt - m2, -2000.f), 2000.f));
-            const float dm = m - m2, d = __builtin_amdgcn_exp2f(dm + (float)(ve - ve2));
+            const float dm = m - m2;
+            mt = fmaxf(mt + dm, tx);
+            const int ve2 = (int)ceilf(fminf(fmaxf(mt, -2000.f), 2000.f));
+            const float d = __builtin_amdgcn_exp2f(dm + (float)(ve - ve2));
             l *= __builtin_amdgcn_exp2f(dm);
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] *= d;

@@ -147,6 +147,41 @@ def test_queries_with_a_channel_far_larger(news, dtype):
         _attend(dtype, q, kc, vc, ks, vs, _table(1, pages, pages, 20), [news], [n], **kw)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("power", [18, 22, 23, 24, 25, 26, 27, 28, 30, 36, 40])
+@pytest.mark.parametrize("any_score", [False, True])
+def test_scores_so_large_that_fp32_counts_in_steps(any_score, power, dtype):
+    """Scores of 2^18 to 2^40 and more, exact in fp32, of which a row's best is one key's or two keys': the output is
+    that key's value, or the two's average, whatever the sizes of the values' scales."""
+    torch = torch_cuda()
+    print(f"large scores {(any_score, power, dtype)}", flush=True)
+    hq, hk, dh, ps, n = 2, 1, 64, 16, 160
+    pages = n // ps
+    r = np.random.default_rng(60)
+    kc = torch.zeros(pages, ps, hk, dh, dtype=torch.int8, device="cuda:0")
+    order = r.permutation(n) % 100 + 20       # 20 .. 79 stand twice
+    kc[..., 3] = torch.from_numpy(order.reshape(pages, ps, 1).astype(np.int8)).cuda()
+    kc[9, 15, 0, 3] = 127
+    kc[4, 2, 0, 3] = 126
+    vc, _ = _pool(pages, ps, hk, dh, 61)
+    top = 400.0 if dtype == "f16" else 3e7
+    vs = torch.tensor([top, 1e-3, top, 1.0, top, 2.0, 1e-6, top, 0.0, top], device="cuda:0")[:, None].contiguous()
+    ks = torch.full((pages, hk), 2.0 ** (power - 10), device="cuda:0")
+    q = torch.zeros(3, hq, dh, device="cuda:0")
+    q[:, 0, 3], q[:, 1, 3] = 64.0, -64.0                 # scores 2^(power - 7) times the code, or less
+    slopes = torch.zeros(hq, device="cuda:0") if any_score else None
+    table = np.arange(pages, dtype=np.int32)[None]
+    for split in (True, False):
+        work = None if split else torch.empty(0, dtype=torch.uint8, device="cuda:0")
+        out = _g().gptq_kv_attention(q.to(_dtype(dtype)), kc, vc, ks, vs, _ints(table), _ints([n]), slopes=slopes, work=work)
+        torch.cuda.synchronize()
+        want, mag, _, _ = serve_ref.kv_attention(_np(q), kc.cpu().numpy(), vc.cpu().numpy(), ks.cpu().numpy(), vs.cpu().numpy(),
+                                                 table, [0, 3], [n], 0.125, True, 0, 0.0, None)
+        bound = _half_step(dtype) * np.abs(want) + (2.0 ** -22 + 64 * U) * mag + 2.0 ** -25 * (dtype == "f16")
+        err = np.abs(_np(out) - want)
+        assert np.all(err <= bound), float(np.max(err / np.maximum(bound, 1e-300)))
+
+
 # -------------------------------------------------------------------------------------- norm_quant
 
 SIZES = [(1, 1), (3, 2), (5, 7), (2, 8), (9, 63), (4, 64), (7, 255), (3, 512), (6, 513), (5, 1000), (3, 1024), (2, 2049),
