@@ -147,11 +147,11 @@ __global__ __launch_bounds__(256) void kv_row_kernel(KvArgs a) {
 // the largest. fp32 ones are two fp16 terms.
 // Probabilities are two terms for every type: one of 11 bits moves an output by up to 2^-11 of sum p |v|, which is as
 // much as its own rounding to fp16 and shows wherever values cancel. The second product costs 1 % for 16 tokens against
-// caches of up to 8192, and 6 % for four chunks of 512 against up to 4096.
+// caches of up to 8192, and 7 % for four chunks of 512 against up to 4096.
 // A key block's scale multiplies its scores, a value block's its probabilities. The products are kept in fp16's range by
 // a power of two a row, which bounds those of the keys that the row has seen, probability and scale together: neither a
 // scale that a row does not see nor one that its probabilities make small takes bits from the others. (One power for
-// the wave, of all scales that it loads, would save 2 % for the chunks, and loses rows whose scales are small.)
+// the wave, of all scales that it loads, would save 4 % for the chunks, and loses rows whose scales are small.)
 //
 // Workgroups share the work by keys: the tiles of 32 keys of all (sequence, key head, 16 rows) are one list, of which
 // each takes an equal, contiguous part, whatever the lengths are. A part begins and ends anywhere; where it holds
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(256) void kv_row_kernel(KvArgs a) {
 // once: 16 tokens against caches of up to 8192 take 54 us with 512 parts, 61 with 768, 81 with 2048.
 //
 // Measured there: 168 MB in 48 us with start and end, 3.5 TB/s, and the join 5; one token against 100003 keys 49 + 9; four
-// chunks of 512 against up to 4096 in 413 us after one another, 372 with pauses, where every 16 rows read and widen K and
+// chunks of 512 against up to 4096 in 419 us after one another, 384 with pauses, where every 16 rows read and widen K and
 // V again.
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
